@@ -19,14 +19,23 @@ Calls (same names as the C ABI):
     balance_plan(counts, n_ranks, n_entries)       -> moe_balance_plan
     grouped_layout_rows(n_entries, E', tile_m)     -> moe_grouped_layout_rows
     sigmoid_rn32(x, mode=0)                        -> moe_sigmoid_rn32 (diagnostic)
+and the feed-forward operators on the routed rows and on the tokens (module
+``ffn``, C ABI ``include/moe_ffn.h``): gated_ffn, linear, combine, their
+expert forms and their backward passes.
 """
 from __future__ import annotations
 
 import ctypes
 import os
+import sys
 from typing import Dict, Optional
 
 import torch
+
+from . import ffn
+from .ffn import (combine, combine_backward, expert_gated_ffn, expert_gated_ffn_backward,
+                  expert_linear, expert_linear_backward, gated_ffn, gated_ffn_backward, linear,
+                  linear_backward)
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_lib", "libmoe_route.so")
@@ -101,7 +110,7 @@ def lib() -> ctypes.CDLL:
             raise MoeRouteError(
                 f"{LIB_PATH} is missing: build it with `python -m moe_expert_routing_amd.build`")
         handle = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in EXPORTS.items():
+        for name, (res, args) in (*EXPORTS.items(), *ffn.EXPORTS.items()):
             fn = getattr(handle, name)
             fn.restype = res
             fn.argtypes = args
@@ -518,3 +527,6 @@ def sigmoid_rn32(x: torch.Tensor, mode: int = 0) -> torch.Tensor:
                                 _stream_handle(x.device))
     _check(st, "moe_sigmoid_rn32")
     return y
+
+
+ffn._pkg = sys.modules[__name__]

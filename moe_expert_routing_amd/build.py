@@ -24,7 +24,8 @@ CSRC = os.path.join(PKG, "csrc")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libmoe_route.so")
 TEMPS = os.path.join(ROOT, "_build")
-SOURCES = [os.path.join(CSRC, "moe_route.hip"), os.path.join(CSRC, "router_gemm.hip")]
+SOURCES = [os.path.join(CSRC, name) for name in (
+    "moe_route.hip", "router_gemm.hip", "ffn.hip", "ffn_bf16.hip", "ffn_f16.hip")]
 ARCH = "gfx950"
 
 HIP_FLAGS = [

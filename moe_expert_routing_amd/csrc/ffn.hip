@@ -1,0 +1,447 @@
+// ffn.hip - the C entry points of the feed-forward operators: checks, padded
+// copies where an operand needs one, and the launches.
+#include "ffn.hpp"
+#include "ffn_rows.hpp"
+
+namespace moe_ffn {
+
+static const int64_t MAX_ROWS = (int64_t)1 << 30;
+
+static int round8(int v) { return (v + 7) & ~7; }
+static size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+// Hands out the workspace in 256-byte aligned parts. A dry one only counts
+// them: the same code sizes the workspace and then runs the call.
+struct Arena {
+  uint8_t *base;
+  bool dry;
+  size_t used;
+  uint16_t *take(size_t bytes) {
+    uint8_t *p = dry ? nullptr : base + used;
+    used += align256(bytes);
+    return reinterpret_cast<uint16_t *>(p);
+  }
+};
+
+static int launch_gemm(int dtype, int mode, int bm, const GemmArgs &g, hipStream_t st) {
+  return dtype == MOE_BF16 ? launch_gemm_bf16(mode, bm, g, st) : launch_gemm_f16(mode, bm, g, st);
+}
+
+static dim3 row_grid(int64_t rows, int cols8, int z) {
+  const int64_t y = (rows + ROW_THREADS - 1) / ROW_THREADS;
+  return dim3((uint32_t)((cols8 / 8 + COL_THREADS - 1) / COL_THREADS),
+              (uint32_t)(y < 65535 ? y : 65535), (uint32_t)z);
+}
+
+// An operand of a product: the matrix itself where its 16-byte pieces are
+// aligned, else a padded copy in the workspace. `mats` matrices of [rows,
+// cols].
+struct Operand {
+  const uint16_t *p;
+  int64_t ld, stride;
+};
+static Operand operand(const moe_matrix &m, int64_t rows, int cols, int mats, Arena &a,
+                       hipStream_t st, int *status) {
+  const bool fine = ((uintptr_t)m.p & 15) == 0 && ((m.ld | cols) & 7) == 0 &&
+                    (mats == 1 || (m.stride & 7) == 0);
+  if (fine || rows == 0) return {(const uint16_t *)m.p, m.ld, m.stride};
+  const int c8 = round8(cols);
+  uint16_t *dst = a.take((size_t)mats * rows * c8 * 2);
+  if (!a.dry && *status == MOE_OK) {
+    pad_rows_kernel<<<row_grid(rows, c8, mats), dim3(COL_THREADS, ROW_THREADS), 0, st>>>(
+        (const uint16_t *)m.p, m.ld, m.stride, rows, cols, dst, c8);
+    *status = hip_status();
+  }
+  return {dst, c8, rows * c8};
+}
+
+// Rows of a tile. Over experts a tile holds rows of one expert, so it divides
+// the layout's alignment. Dense: the smallest tile that holds all the
+// rows; above 64 rows 256-row tiles where they fill the chip's 256 compute
+// units at least to three quarters, else 128-row ones.
+static int tile_rows(const moe_expert_rows &r, int64_t M, int N) {
+  if (r.num_experts > 0) {
+    for (int bm = 256; bm > 16; bm >>= 1)
+      if (r.tile_m % bm == 0) return bm;
+    return 16;
+  }
+  if (M <= 16) return 16;
+  if (M <= 32) return 32;
+  if (M <= 64) return 64;
+  return ((M + 255) / 256) * ((N + 255) / 256) >= 192 ? 256 : 128;
+}
+static int tile_rows_wgrad(int mats, int M, int N) {
+  return (int64_t)mats * ((M + 255) / 256) * ((N + 255) / 256) >= 192 ? 256 : 128;
+}
+
+static int check_common(int dtype, int act, int64_t tokens, int w0, int w1,
+                        const moe_expert_rows &r, bool backward) {
+  if (dtype != MOE_BF16 && dtype != MOE_F16) return MOE_ERR_UNSUPPORTED;
+  if (act < MOE_ACT_NONE || act > MOE_ACT_GELU) return MOE_ERR_UNSUPPORTED;
+  if (tokens < 0 || w0 <= 0 || w1 <= 0) return MOE_ERR_SHAPE;
+  if (w0 > MOE_FFN_MAX_WIDTH || w1 > MOE_FFN_MAX_WIDTH || tokens > MAX_ROWS)
+    return MOE_ERR_UNSUPPORTED;
+  if (r.num_experts < 0) return MOE_ERR_SHAPE;
+  if (r.num_experts > 0) {
+    if (r.rows < 0) return MOE_ERR_SHAPE;
+    if (r.num_experts > MOE_FFN_MAX_EXPERTS || r.rows > MAX_ROWS) return MOE_ERR_UNSUPPORTED;
+    if (r.tile_m <= 0 || r.tile_m > MOE_GROUPED_MAX_TILE) return MOE_ERR_SHAPE;
+    if (r.tile_m % 16 != 0) return MOE_ERR_UNSUPPORTED;
+    if (r.rows > 0 && !r.m_indices) return MOE_ERR_NULL;
+    if (backward && (!r.counts || !r.padded_offsets)) return MOE_ERR_NULL;
+    if (r.row_entry && r.top_k <= 0) return MOE_ERR_SHAPE;
+  }
+  return MOE_OK;
+}
+
+// A matrix of `rows` x `cols`, one or `mats` of them. Optional matrices may be
+// NULL, and any may where it has no elements.
+static int check_matrix(const moe_matrix &m, int64_t rows, int cols, int mats, bool optional) {
+  if (!m.p) return optional || rows == 0 ? MOE_OK : MOE_ERR_NULL;
+  if ((uintptr_t)m.p % 2 != 0) return MOE_ERR_SHAPE;
+  if (rows > 1 && m.ld < cols) return MOE_ERR_SHAPE;
+  if (m.ld < 0 || m.stride < 0) return MOE_ERR_SHAPE;
+  if (m.ld > MOE_FFN_MAX_LD) return MOE_ERR_UNSUPPORTED;
+  if (mats > 1 && m.stride < (rows - 1) * m.ld + cols) return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+#define MOE_TRY(x)              \
+  do {                          \
+    const int st_ = (x);        \
+    if (st_ != MOE_OK) return st_; \
+  } while (0)
+
+static int64_t call_rows(const moe_expert_rows &r, int64_t tokens) {
+  return r.num_experts > 0 ? r.rows : tokens;
+}
+static int mats_of(const moe_expert_rows &r) { return r.num_experts > 0 ? r.num_experts : 1; }
+
+// ---------------------------------------------------------------- gated block
+
+static int check_gated(const moe_gated_ffn_args *a, bool backward) {
+  if (!a) return MOE_ERR_NULL;
+  MOE_TRY(check_common(a->dtype, a->activation, a->tokens, a->hidden, a->inter, a->rows, backward));
+  if (a->inter > MOE_FFN_MAX_WIDTH / 2) return MOE_ERR_UNSUPPORTED;
+  const int64_t rows = call_rows(a->rows, a->tokens);
+  const int mats = mats_of(a->rows), H = a->hidden, F = a->inter;
+  const bool gather = a->rows.num_experts > 0 && a->rows.row_entry;
+  if (!gather && a->tokens < rows) return MOE_ERR_SHAPE;
+  MOE_TRY(check_matrix(a->x, a->tokens, H, 1, backward && !a->dw_gate.p));
+  MOE_TRY(check_matrix(a->w_gate, F, H, mats, backward && !a->dx.p));
+  MOE_TRY(check_matrix(a->w_up, F, H, mats, backward && !a->dx.p));
+  MOE_TRY(check_matrix(a->pre, rows, 2 * F, 1, !backward));
+  if (!backward) return check_matrix(a->h, rows, F, 1, false);
+  MOE_TRY(check_matrix(a->dh, rows, F, 1, false));
+  MOE_TRY(check_matrix(a->dx, rows, H, 1, true));
+  MOE_TRY(check_matrix(a->dw_gate, F, H, mats, true));
+  MOE_TRY(check_matrix(a->dw_up, F, H, mats, true));
+  return !a->dw_gate.p != !a->dw_up.p ? MOE_ERR_NULL : MOE_OK;
+}
+
+static GemmArgs gemm_args(const moe_expert_rows &r, int64_t rows, bool gather) {
+  GemmArgs g = {};
+  g.r = {r.counts, r.padded_offsets, r.m_indices, gather ? r.row_entry : nullptr, rows,
+         r.num_experts, r.top_k};
+  g.segs = 1;
+  return g;
+}
+static void set_b0(GemmArgs &g, const Operand &b) {
+  g.b0 = b.p, g.ldb0 = b.ld, g.b_stride0 = b.stride;
+}
+static void set_b1(GemmArgs &g, const Operand &b) {
+  g.b1 = b.p, g.ldb1 = b.ld, g.b_stride1 = b.stride;
+}
+static void set_c0(GemmArgs &g, const moe_matrix &c) {
+  g.c0 = (uint16_t *)c.p, g.ldc0 = c.ld, g.c_stride0 = c.stride;
+}
+static void set_c1(GemmArgs &g, const moe_matrix &c) {
+  g.c1 = (uint16_t *)c.p, g.ldc1 = c.ld, g.c_stride1 = c.stride;
+}
+
+static int run_gated(const moe_gated_ffn_args *a, Arena &ws, hipStream_t st) {
+  const int64_t rows = call_rows(a->rows, a->tokens);
+  const int mats = mats_of(a->rows), H = a->hidden, F = a->inter;
+  int status = MOE_OK;
+  if (rows == 0) return MOE_OK;
+  const Operand x = operand(a->x, a->tokens, H, 1, ws, st, &status);
+  const Operand wg = operand(a->w_gate, F, H, mats, ws, st, &status);
+  const Operand wu = operand(a->w_up, F, H, mats, ws, st, &status);
+  if (ws.dry || status != MOE_OK) return status;
+  GemmArgs g = gemm_args(a->rows, rows, a->rows.num_experts > 0);
+  g.a = x.p, g.lda = x.ld, g.a_rows = a->tokens;
+  set_b0(g, wg);
+  set_b1(g, wu);
+  set_c0(g, a->h);
+  g.pre = (uint16_t *)a->pre.p, g.ldp = a->pre.ld;
+  g.M = (int)rows, g.N = F, g.K = H, g.act = a->activation;
+  return launch_gemm(a->dtype, GATED, tile_rows(a->rows, rows, 2 * F), g, st);
+}
+
+static int run_gated_backward(const moe_gated_ffn_args *a, Arena &ws, hipStream_t st) {
+  const int64_t rows = call_rows(a->rows, a->tokens);
+  const int mats = mats_of(a->rows), H = a->hidden, F = a->inter, Fa = round8(F);
+  const bool gather = a->rows.num_experts > 0 && a->rows.row_entry;
+  int status = MOE_OK;
+  uint16_t *dz = ws.take((size_t)rows * 2 * Fa * 2);
+  Operand x = {}, wg = {}, wu = {};
+  if (a->dw_gate.p) x = operand(a->x, a->tokens, H, 1, ws, st, &status);
+  if (a->dx.p && rows > 0) {
+    wg = operand(a->w_gate, F, H, mats, ws, st, &status);
+    wu = operand(a->w_up, F, H, mats, ws, st, &status);
+  }
+  if (ws.dry || status != MOE_OK) return status;
+  GemmArgs g = gemm_args(a->rows, rows, gather);
+  if (rows > 0) {
+    const dim3 grid = row_grid(rows, Fa, 1), block(COL_THREADS, ROW_THREADS);
+    const auto kernel = a->dtype == MOE_BF16 ? gated_dz_kernel<Bf16> : gated_dz_kernel<F16>;
+    kernel<<<grid, block, 0, st>>>((const uint16_t *)a->dh.p, a->dh.ld,
+                                   (const uint16_t *)a->pre.p, a->pre.ld, rows, F, a->activation,
+                                   g.r, dz);
+    MOE_TRY(hip_status());
+  }
+  g.a = dz, g.lda = 2 * Fa, g.a_seg = Fa, g.segs = 2;
+  if (a->dx.p && rows > 0) {
+    GemmArgs d = g;
+    d.r.row_entry = nullptr;
+    d.a_rows = rows;
+    set_b0(d, wg);
+    set_b1(d, wu);
+    set_c0(d, a->dx);
+    d.M = (int)rows, d.N = H, d.K = F;
+    MOE_TRY(launch_gemm(a->dtype, DGRAD, tile_rows(a->rows, rows, H), d, st));
+  }
+  if (a->dw_gate.p) {
+    set_b0(g, x);
+    g.a_rows = a->tokens;
+    set_c0(g, a->dw_gate);
+    set_c1(g, a->dw_up);
+    g.M = F, g.N = H, g.K = (int)rows;
+    MOE_TRY(launch_gemm(a->dtype, WGRAD, tile_rows_wgrad(2 * mats, F, H), g, st));
+  }
+  return MOE_OK;
+}
+
+// --------------------------------------------------------------------- linear
+
+static int check_linear(const moe_linear_args *a, bool backward) {
+  if (!a) return MOE_ERR_NULL;
+  MOE_TRY(check_common(a->dtype, a->activation, a->tokens, a->in, a->out, a->rows, backward));
+  const int64_t rows = call_rows(a->rows, a->tokens);
+  const int mats = mats_of(a->rows), I = a->in, O = a->out;
+  MOE_TRY(check_matrix(a->x, rows, I, 1, backward && !a->dw.p));
+  MOE_TRY(check_matrix(a->w, O, I, mats, backward && !a->dx.p));
+  MOE_TRY(check_matrix(a->pre, rows, O, 1, !backward || a->activation == MOE_ACT_NONE));
+  if (!backward) {
+    MOE_TRY(check_matrix(a->bias, 1, O, mats, true));
+    MOE_TRY(check_matrix(a->residual, rows, O, 1, true));
+    return check_matrix(a->y, rows, O, 1, false);
+  }
+  MOE_TRY(check_matrix(a->dy, rows, O, 1, false));
+  MOE_TRY(check_matrix(a->dx, rows, I, 1, true));
+  MOE_TRY(check_matrix(a->dw, O, I, mats, true));
+  return check_matrix(a->dbias, 1, O, mats, true);
+}
+
+static int run_linear(const moe_linear_args *a, Arena &ws, hipStream_t st) {
+  const int64_t rows = call_rows(a->rows, a->tokens);
+  const int mats = mats_of(a->rows), I = a->in, O = a->out;
+  int status = MOE_OK;
+  if (rows == 0) return MOE_OK;
+  const Operand x = operand(a->x, rows, I, 1, ws, st, &status);
+  const Operand w = operand(a->w, O, I, mats, ws, st, &status);
+  if (ws.dry || status != MOE_OK) return status;
+  GemmArgs g = gemm_args(a->rows, rows, false);
+  g.a = x.p, g.lda = x.ld, g.a_rows = rows;
+  set_b0(g, w);
+  set_c0(g, a->y);
+  g.pre = (uint16_t *)a->pre.p, g.ldp = a->pre.ld;
+  g.bias = (const uint16_t *)a->bias.p, g.bias_stride = a->bias.stride;
+  g.res = (const uint16_t *)a->residual.p, g.ldr = a->residual.ld;
+  g.M = (int)rows, g.N = O, g.K = I, g.act = a->activation;
+  return launch_gemm(a->dtype, LINEAR, tile_rows(a->rows, rows, O), g, st);
+}
+
+// Row ranges of the bias gradient's partial sums: dense, one for every 256
+// rows, at most 64; one for an expert.
+static int bias_splits(const moe_expert_rows &r, int64_t rows) {
+  if (r.num_experts > 0) return 1;
+  const int64_t s = rows / 256;
+  return s < 1 ? 1 : s > 64 ? 64 : (int)s;
+}
+
+static int run_linear_backward(const moe_linear_args *a, Arena &ws, hipStream_t st) {
+  const int64_t rows = call_rows(a->rows, a->tokens);
+  const int mats = mats_of(a->rows), I = a->in, O = a->out, Oa = round8(O);
+  const bool bf = a->dtype == MOE_BF16;
+  int status = MOE_OK;
+  GemmArgs g = gemm_args(a->rows, rows, false);
+  const uint16_t *dy = (const uint16_t *)a->dy.p, *pre = (const uint16_t *)a->pre.p;
+  if (a->dbias.p) {
+    const int S = bias_splits(a->rows, rows);
+    float *part = reinterpret_cast<float *>(ws.take((size_t)mats * S * O * 4));
+    if (!ws.dry) {
+      const auto sums = bf ? bias_grad_kernel<Bf16> : bias_grad_kernel<F16>;
+      sums<<<dim3((O + 63) / 64, S, mats), dim3(8, BIAS_ROWS), 0, st>>>(
+          dy, a->dy.ld, pre, a->pre.ld, rows, O, a->activation, g.r, S, part);
+      MOE_TRY(hip_status());
+      const auto join = bf ? bias_sum_kernel<Bf16> : bias_sum_kernel<F16>;
+      join<<<dim3((O + 255) / 256, 1, mats), 256, 0, st>>>(part, S, O, (uint16_t *)a->dbias.p,
+                                                           a->dbias.stride);
+      MOE_TRY(hip_status());
+    }
+  }
+  if (!a->dx.p && !a->dw.p) return MOE_OK;
+  // dz: dy itself without an activation, where its pieces are aligned
+  Operand dz;
+  if (a->activation == MOE_ACT_NONE) {
+    dz = operand(a->dy, rows, O, 1, ws, st, &status);
+  } else {
+    uint16_t *p = ws.take((size_t)rows * Oa * 2);
+    dz = {p, Oa, 0};
+    if (!ws.dry && rows > 0) {
+      const auto kernel = bf ? linear_dz_kernel<Bf16> : linear_dz_kernel<F16>;
+      kernel<<<row_grid(rows, Oa, 1), dim3(COL_THREADS, ROW_THREADS), 0, st>>>(
+          dy, a->dy.ld, pre, a->pre.ld, rows, O, a->activation, g.r, p);
+      MOE_TRY(hip_status());
+    }
+  }
+  Operand x = {}, w = {};
+  if (a->dw.p) x = operand(a->x, rows, I, 1, ws, st, &status);
+  if (a->dx.p && rows > 0) w = operand(a->w, O, I, mats, ws, st, &status);
+  if (ws.dry || status != MOE_OK) return status;
+  g.a = dz.p, g.lda = dz.ld, g.a_rows = rows;
+  if (a->dx.p && rows > 0) {
+    GemmArgs d = g;
+    set_b0(d, w);
+    set_c0(d, a->dx);
+    d.M = (int)rows, d.N = I, d.K = O;
+    MOE_TRY(launch_gemm(a->dtype, DGRAD, tile_rows(a->rows, rows, I), d, st));
+  }
+  if (a->dw.p) {
+    set_b0(g, x);
+    set_c0(g, a->dw);
+    g.M = O, g.N = I, g.K = (int)rows;
+    MOE_TRY(launch_gemm(a->dtype, WGRAD, tile_rows_wgrad(mats, O, I), g, st));
+  }
+  return MOE_OK;
+}
+
+// -------------------------------------------------------------------- combine
+
+static int check_combine(const moe_combine_args *a, bool backward) {
+  if (!a) return MOE_ERR_NULL;
+  if (a->dtype != MOE_BF16 && a->dtype != MOE_F16) return MOE_ERR_UNSUPPORTED;
+  if (a->tokens < 0 || a->rows < 0 || a->width <= 0 || a->top_k <= 0 || a->num_experts < 0 ||
+      a->num_ids < a->num_experts)
+    return MOE_ERR_SHAPE;
+  if (a->width > MOE_FFN_MAX_WIDTH || a->top_k > COMBINE_MAX_TOPK || a->tokens > MAX_ROWS ||
+      a->rows > MAX_ROWS || a->tokens * a->top_k > 0x7fffffff)
+    return MOE_ERR_UNSUPPORTED;
+  const bool entries = a->tokens > 0 && (!backward || a->dweights);
+  if (entries && (!a->packed || !a->inv_perm || !a->offsets || !a->padded_offsets))
+    return MOE_ERR_NULL;
+  if (!backward) {
+    MOE_TRY(check_matrix(a->y, a->rows, a->width, 1, false));
+    MOE_TRY(check_matrix(a->residual, a->tokens, a->width, 1, true));
+    return check_matrix(a->out, a->tokens, a->width, 1, false);
+  }
+  if (a->rows > 0 && (!a->m_indices || !a->row_entry)) return MOE_ERR_NULL;
+  MOE_TRY(check_matrix(a->y, a->rows, a->width, 1, !a->dweights));
+  MOE_TRY(check_matrix(a->dout, a->tokens, a->width, 1, false));
+  return check_matrix(a->dy, a->rows, a->width, 1, false);
+}
+
+static CombineArgs combine_args(const moe_combine_args *a) {
+  CombineArgs c = {};
+  c.width = a->width, c.top_k = a->top_k, c.num_experts = a->num_experts, c.num_ids = a->num_ids;
+  c.tokens = a->tokens, c.rows = a->rows;
+  c.packed = a->packed, c.inv_perm = a->inv_perm, c.offsets = a->offsets;
+  c.padded_offsets = a->padded_offsets, c.m_indices = a->m_indices, c.row_entry = a->row_entry;
+  c.weights = a->weights;
+  c.y = (const uint16_t *)a->y.p, c.residual = (const uint16_t *)a->residual.p;
+  c.dout = (const uint16_t *)a->dout.p;
+  c.out = (uint16_t *)a->out.p, c.dy = (uint16_t *)a->dy.p;
+  c.ld_y = a->y.ld, c.ld_res = a->residual.ld, c.ld_out = a->out.ld, c.ld_dout = a->dout.ld;
+  c.ld_dy = a->dy.ld;
+  c.dweights = a->dweights;
+  return c;
+}
+
+template <class Args>
+static int64_t sized(const Args *a, int check, int (*run)(const Args *, Arena &, hipStream_t)) {
+  if (check != MOE_OK) return -1;
+  Arena ws = {nullptr, true, 0};
+  run(a, ws, nullptr);
+  return (int64_t)ws.used;
+}
+template <class Args>
+static int checked_run(const Args *a, int check, int (*run)(const Args *, Arena &, hipStream_t),
+                       void *workspace, size_t bytes, void *stream) {
+  MOE_TRY(check);
+  const int64_t need = sized(a, MOE_OK, run);
+  if (need > 0 && (!workspace || (uintptr_t)workspace % 16 != 0 || bytes < (size_t)need))
+    return MOE_ERR_WORKSPACE;
+  Arena ws = {(uint8_t *)workspace, false, 0};
+  return run(a, ws, (hipStream_t)stream);
+}
+
+}  // namespace moe_ffn
+
+extern "C" {
+
+int64_t moe_gated_ffn_workspace_bytes(const moe_gated_ffn_args *a, int32_t backward) {
+  using namespace moe_ffn;
+  return sized(a, check_gated(a, backward != 0), backward ? run_gated_backward : run_gated);
+}
+int moe_gated_ffn(const moe_gated_ffn_args *a, void *workspace, size_t workspace_bytes,
+                  void *stream) {
+  using namespace moe_ffn;
+  return checked_run(a, check_gated(a, false), run_gated, workspace, workspace_bytes, stream);
+}
+int moe_gated_ffn_backward(const moe_gated_ffn_args *a, void *workspace, size_t workspace_bytes,
+                           void *stream) {
+  using namespace moe_ffn;
+  return checked_run(a, check_gated(a, true), run_gated_backward, workspace, workspace_bytes,
+                     stream);
+}
+
+int64_t moe_linear_workspace_bytes(const moe_linear_args *a, int32_t backward) {
+  using namespace moe_ffn;
+  return sized(a, check_linear(a, backward != 0), backward ? run_linear_backward : run_linear);
+}
+int moe_linear(const moe_linear_args *a, void *workspace, size_t workspace_bytes, void *stream) {
+  using namespace moe_ffn;
+  return checked_run(a, check_linear(a, false), run_linear, workspace, workspace_bytes, stream);
+}
+int moe_linear_backward(const moe_linear_args *a, void *workspace, size_t workspace_bytes,
+                        void *stream) {
+  using namespace moe_ffn;
+  return checked_run(a, check_linear(a, true), run_linear_backward, workspace, workspace_bytes,
+                     stream);
+}
+
+int moe_combine(const moe_combine_args *a, void *stream) {
+  using namespace moe_ffn;
+  MOE_TRY(check_combine(a, false));
+  if (a->tokens == 0) return MOE_OK;
+  const CombineArgs c = combine_args(a);
+  const int y = (round8(a->width) / 8 + COMBINE_THREADS - 1) / COMBINE_THREADS;
+  const auto kernel = a->dtype == MOE_BF16 ? combine_kernel<Bf16> : combine_kernel<F16>;
+  kernel<<<dim3((uint32_t)a->tokens, y), COMBINE_THREADS, 0, (hipStream_t)stream>>>(c);
+  return hip_status();
+}
+int moe_combine_backward(const moe_combine_args *a, void *stream) {
+  using namespace moe_ffn;
+  MOE_TRY(check_combine(a, true));
+  const CombineArgs c = combine_args(a);
+  int64_t blocks = a->rows;
+  if (a->dweights)
+    blocks += (a->tokens * a->top_k + COMBINE_THREADS - 1) / COMBINE_THREADS;
+  if (blocks == 0) return MOE_OK;
+  const auto kernel =
+      a->dtype == MOE_BF16 ? combine_backward_kernel<Bf16> : combine_backward_kernel<F16>;
+  kernel<<<dim3((uint32_t)blocks), COMBINE_THREADS, 0, (hipStream_t)stream>>>(c);
+  return hip_status();
+}
+
+}  // extern "C"

@@ -1,0 +1,299 @@
+// ffn_rows.hpp - the memory-bound kernels of the feed-forward operators: the
+// gradient of the pre-activations, the bias gradient, padded copies of
+// operands, and the combination of the experts' rows. All of them are bound by
+// the bytes they move and read and write 16 bytes a lane where the rows allow.
+#pragma once
+
+#include "ffn_types.hpp"
+
+namespace moe_ffn {
+
+// Eight elements at column c of a row that has n columns; zeros past n.
+template <class D>
+__device__ __forceinline__ f32x8 load8(const uint16_t *row, int c, int n, bool vec) {
+  s16x8 w = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (vec && c + 8 <= n) {
+    w = *reinterpret_cast<const s16x8 *>(row + c);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < n) w[i] = (short)row[c + i];
+  }
+  return unpack8<D>(w);
+}
+__device__ __forceinline__ void store8_raw(uint16_t *row, int c, int n, bool vec, s16x8 w) {
+  if (vec && c + 8 <= n) {
+    *reinterpret_cast<s16x8 *>(row + c) = w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < n) row[c + i] = (uint16_t)w[i];
+  }
+}
+template <class D>
+__device__ __forceinline__ void store8(uint16_t *row, int c, int n, bool vec, f32x8 v) {
+  store8_raw(row, c, n, vec, pack8<D>(v));
+}
+// whether 8 consecutive elements at a multiple-of-8 column are one aligned load
+__device__ __forceinline__ bool vec8(const void *p, int64_t ld, int64_t off = 0) {
+  return (((uintptr_t)p & 15) | (uintptr_t)((ld | off) & 7)) == 0;
+}
+__device__ __forceinline__ bool row_is_real(const Rows &r, int64_t row) {
+  if (r.num_experts == 0) return true;
+  const int32_t e = r.m_indices[row];
+  return e >= 0 && e < r.num_experts;
+}
+
+constexpr int COL_THREADS = 64, ROW_THREADS = 4;  // block of the row-wise kernels
+
+// dst [mats][rows, cols8] = src [mats][rows, cols] with zeros in the padding.
+__global__ __launch_bounds__(COL_THREADS *ROW_THREADS) void pad_rows_kernel(
+    const uint16_t *__restrict__ src, int64_t ld, int64_t stride, int64_t rows, int cols,
+    uint16_t *__restrict__ dst, int cols8) {
+  const int c = (blockIdx.x * COL_THREADS + threadIdx.x) * 8;
+  if (c >= cols8) return;
+  src += blockIdx.z * stride;
+  dst += (int64_t)blockIdx.z * rows * cols8;
+  const bool vec = vec8(src, ld);
+  for (int64_t r = blockIdx.y * ROW_THREADS + threadIdx.y; r < rows;
+       r += (int64_t)gridDim.y * ROW_THREADS) {
+    s16x8 w = {0, 0, 0, 0, 0, 0, 0, 0};
+    const uint16_t *p = src + r * ld;
+    if (vec && c + 8 <= cols) {
+      w = *reinterpret_cast<const s16x8 *>(p + c);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i < cols) w[i] = (short)p[c + i];
+    }
+    *reinterpret_cast<s16x8 *>(dst + r * cols8 + c) = w;
+  }
+}
+
+// Gradient of a gated block's pre-activations, rounded once: dz [rows, 2 Fa]
+// with dg = dh u act'(g) in the first Fa = round_up(F, 8) columns and
+// du = dh act(g) in the others, zeros in the padding. Rows without an entry
+// are left as they are: the products never read them.
+template <class D>
+__global__ __launch_bounds__(COL_THREADS *ROW_THREADS) void gated_dz_kernel(
+    const uint16_t *__restrict__ dh, int64_t ld_dh, const uint16_t *__restrict__ pre,
+    int64_t ld_pre, int64_t rows, int F, int act, Rows r, uint16_t *__restrict__ dz) {
+  const int Fa = (F + 7) & ~7;
+  const int c = (blockIdx.x * COL_THREADS + threadIdx.x) * 8;
+  if (c >= Fa) return;
+  const bool vh = vec8(dh, ld_dh), vp = vec8(pre, ld_pre), vu = vec8(pre, ld_pre, F);
+  for (int64_t m = blockIdx.y * ROW_THREADS + threadIdx.y; m < rows;
+       m += (int64_t)gridDim.y * ROW_THREADS) {
+    if (!row_is_real(r, m)) continue;
+    const f32x8 d = load8<D>(dh + m * ld_dh, c, F, vh);
+    const f32x8 gt = load8<D>(pre + m * ld_pre, c, F, vp);
+    const f32x8 up = load8<D>(pre + m * ld_pre + F, c, F, vu);
+    f32x8 dg, du;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float v, s;
+      act_value_slope(gt[i], act, v, s);
+      dg[i] = d[i] * up[i] * s;
+      du[i] = d[i] * v;
+    }
+    uint16_t *o = dz + m * (2 * (int64_t)Fa);
+    *reinterpret_cast<s16x8 *>(o + c) = pack8<D>(dg);
+    *reinterpret_cast<s16x8 *>(o + Fa + c) = pack8<D>(du);
+  }
+}
+
+// dz [rows, Oa] = dy act'(pre), rounded once; as above. Without an
+// activation pre is not read and this is a padded copy.
+template <class D>
+__global__ __launch_bounds__(COL_THREADS *ROW_THREADS) void linear_dz_kernel(
+    const uint16_t *__restrict__ dy, int64_t ld_dy, const uint16_t *__restrict__ pre,
+    int64_t ld_pre, int64_t rows, int O, int act, Rows r, uint16_t *__restrict__ dz) {
+  const int Oa = (O + 7) & ~7;
+  const int c = (blockIdx.x * COL_THREADS + threadIdx.x) * 8;
+  if (c >= Oa) return;
+  const bool vd = vec8(dy, ld_dy), vp = vec8(pre, ld_pre);
+  for (int64_t m = blockIdx.y * ROW_THREADS + threadIdx.y; m < rows;
+       m += (int64_t)gridDim.y * ROW_THREADS) {
+    if (!row_is_real(r, m)) continue;
+    f32x8 d = load8<D>(dy + m * ld_dy, c, O, vd);
+    if (act != MOE_ACT_NONE) {
+      const f32x8 z = load8<D>(pre + m * ld_pre, c, O, vp);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float v, s;
+        act_value_slope(z[i], act, v, s);
+        d[i] *= s;
+      }
+    }
+    *reinterpret_cast<s16x8 *>(dz + m * (int64_t)Oa + c) = pack8<D>(d);
+  }
+}
+
+// Column sums of dz = dy act'(pre) in fp32, from dy and pre themselves: the
+// bias gradient does not see dz's rounding. A block sums 64 columns of one of
+// S row ranges: 8 lanes across, 32 rows at a time, then the 32 partial
+// sums in a fixed order. part [mats][S][O].
+constexpr int BIAS_ROWS = 32;
+template <class D>
+__global__ __launch_bounds__(8 * BIAS_ROWS) void bias_grad_kernel(
+    const uint16_t *__restrict__ dy, int64_t ld_dy, const uint16_t *__restrict__ pre,
+    int64_t ld_pre, int64_t rows, int O, int act, Rows r, int S, float *__restrict__ part) {
+  __shared__ float sum[BIAS_ROWS][65];
+  const int c = blockIdx.x * 64 + threadIdx.x * 8;
+  int64_t first = 0, n = rows;
+  if (r.num_experts > 0) {
+    first = min(max((int64_t)r.padded_offsets[blockIdx.z], (int64_t)0), r.rows);
+    n = min(max((int64_t)r.counts[blockIdx.z], (int64_t)0), r.rows - first);
+  }
+  const int64_t per = (n + S - 1) / S, lo = min(n, blockIdx.y * per), hi = min(n, lo + per);
+  const bool vd = vec8(dy, ld_dy), vp = vec8(pre, ld_pre);
+  f32x8 a = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (c < O) {
+    for (int64_t m = first + lo + threadIdx.y; m < first + hi; m += BIAS_ROWS) {
+      const f32x8 d = load8<D>(dy + m * ld_dy, c, O, vd);
+      if (act != MOE_ACT_NONE) {
+        const f32x8 z = load8<D>(pre + m * ld_pre, c, O, vp);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float v, s;
+          act_value_slope(z[i], act, v, s);
+          a[i] += d[i] * s;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[i] += d[i];
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum[threadIdx.y][threadIdx.x * 8 + i] = a[i];
+  __syncthreads();
+  const int t = threadIdx.y * 8 + threadIdx.x;
+  if (t < 64 && blockIdx.x * 64 + t < O) {
+    float v = 0.f;
+    for (int y = 0; y < BIAS_ROWS; ++y) v += sum[y][t];
+    part[((int64_t)blockIdx.z * S + blockIdx.y) * O + blockIdx.x * 64 + t] = v;
+  }
+}
+template <class D>
+__global__ __launch_bounds__(256) void bias_sum_kernel(const float *__restrict__ part, int S, int O,
+                                                       uint16_t *__restrict__ db, int64_t stride) {
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= O) return;
+  const float *p = part + (int64_t)blockIdx.z * S * O + c;
+  float v = 0.f;
+  for (int s = 0; s < S; ++s) v += p[(int64_t)s * O];
+  db[blockIdx.z * stride + c] = from_f<D>(v);
+}
+
+// ------------------------------------------------------------------ combine
+
+struct CombineArgs {
+  int width, top_k, num_experts, num_ids;
+  int64_t tokens, rows;
+  const int32_t *packed, *inv_perm, *offsets, *padded_offsets, *m_indices, *row_entry;
+  const float *weights;
+  const uint16_t *y, *residual, *dout;
+  uint16_t *out, *dy;
+  int64_t ld_y, ld_res, ld_out, ld_dout, ld_dy;
+  float *dweights;
+};
+
+// Row of an entry, or -1 where it is left out.
+__device__ __forceinline__ int64_t entry_row(const CombineArgs &a, int64_t entry) {
+  const int32_t e = a.packed[entry] >> 16;
+  if (e < 0 || e >= a.num_experts || e >= a.num_ids) return -1;
+  const int64_t row = (int64_t)a.inv_perm[entry] - a.offsets[e] + a.padded_offsets[e];
+  return row >= 0 && row < a.rows ? row : -1;
+}
+
+constexpr int COMBINE_MAX_TOPK = 64;
+constexpr int COMBINE_THREADS = 256;
+
+// One block per token and run of columns. The token's rows are found once,
+// by one lane each, and closed up in the order of k.
+template <class D>
+__global__ __launch_bounds__(COMBINE_THREADS) void combine_kernel(const CombineArgs a) {
+  __shared__ int64_t rows[COMBINE_MAX_TOPK];
+  __shared__ float ws[COMBINE_MAX_TOPK];
+  __shared__ int n_rows;
+  const int64_t t = blockIdx.x;
+  if (threadIdx.x < 64) {
+    const int k = threadIdx.x;
+    int64_t row = -1;
+    float w = 1.f;
+    if (k < a.top_k) {
+      row = entry_row(a, t * a.top_k + k);
+      if (a.weights) w = a.weights[t * a.top_k + k];
+    }
+    const uint64_t there = __ballot(row >= 0);
+    if (row >= 0) {
+      const int at = __popcll(there & ((1ull << k) - 1));
+      rows[at] = row;
+      ws[at] = w;
+    }
+    if (k == 0) n_rows = __popcll(there);
+  }
+  __syncthreads();
+  const int n = n_rows;
+  const bool vy = vec8(a.y, a.ld_y), vr = vec8(a.residual, a.ld_res), vo = vec8(a.out, a.ld_out);
+  for (int c = (blockIdx.y * COMBINE_THREADS + threadIdx.x) * 8; c < a.width;
+       c += gridDim.y * COMBINE_THREADS * 8) {
+    f32x8 s = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (a.residual) s = load8<D>(a.residual + t * a.ld_res, c, a.width, vr);
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const f32x8 v = load8<D>(a.y + rows[k] * a.ld_y, c, a.width, vy);
+      const float w = ws[k];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] = fmaf(w, v[i], s[i]);
+    }
+    store8<D>(a.out + t * a.ld_out, c, a.width, vo, s);
+  }
+}
+
+// One block per row: dy of the row, and its entry's dweights. The blocks
+// after the rows' clear dweights of the entries that have no row.
+template <class D>
+__global__ __launch_bounds__(COMBINE_THREADS) void combine_backward_kernel(const CombineArgs a) {
+  __shared__ float part[COMBINE_THREADS / 64];
+  const int64_t row = blockIdx.x;
+  if (row >= a.rows) {
+    const int64_t i = (row - a.rows) * COMBINE_THREADS + threadIdx.x;
+    if (i < a.tokens * a.top_k && entry_row(a, i) < 0) a.dweights[i] = 0.f;
+    return;
+  }
+  const int32_t e = a.m_indices[row], entry = a.row_entry[row];
+  const bool real = e >= 0 && e < a.num_experts && entry >= 0 &&
+                    entry < a.tokens * a.top_k;
+  const int64_t t = real ? entry / a.top_k : 0;
+  const float w = real ? (a.weights ? a.weights[entry] : 1.f) : 0.f;
+  const bool vy = vec8(a.y, a.ld_y), vd = vec8(a.dout, a.ld_dout), vo = vec8(a.dy, a.ld_dy);
+  float dot = 0.f;
+  for (int c = threadIdx.x * 8; c < a.width; c += COMBINE_THREADS * 8) {
+    f32x8 d = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (real) {
+      d = load8<D>(a.dout + t * a.ld_dout, c, a.width, vd);
+      if (a.dweights) {
+        const f32x8 v = load8<D>(a.y + row * a.ld_y, c, a.width, vy);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dot = fmaf(d[i], v[i], dot);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d[i] *= w;
+    }
+    store8<D>(a.dy + row * a.ld_dy, c, a.width, vo, d);
+  }
+  if (!real || !a.dweights) return;
+#pragma unroll
+  for (int s = 32; s > 0; s >>= 1) dot += __shfl_xor(dot, s);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = dot;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float v = 0.f;
+    for (int i = 0; i < COMBINE_THREADS / 64; ++i) v += part[i];
+    a.dweights[entry] = v;
+  }
+}
+
+}  // namespace moe_ffn
