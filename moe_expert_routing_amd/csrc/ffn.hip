@@ -40,11 +40,13 @@ struct Operand {
   const uint16_t *p;
   int64_t ld, stride;
 };
+static bool is_aligned(const moe_matrix &m, int cols, int mats) {
+  return ((uintptr_t)m.p & 15) == 0 && ((m.ld | cols) & 7) == 0 &&
+         (mats == 1 || (m.stride & 7) == 0);
+}
 static Operand operand(const moe_matrix &m, int64_t rows, int cols, int mats, Arena &a,
-                       hipStream_t st, int *status) {
-  const bool fine = ((uintptr_t)m.p & 15) == 0 && ((m.ld | cols) & 7) == 0 &&
-                    (mats == 1 || (m.stride & 7) == 0);
-  if (fine || rows == 0) return {(const uint16_t *)m.p, m.ld, m.stride};
+                       hipStream_t st, int *status, bool copy = false) {
+  if ((is_aligned(m, cols, mats) && !copy) || rows == 0) return {(const uint16_t *)m.p, m.ld, m.stride};
   const int c8 = round8(cols);
   uint16_t *dst = a.take((size_t)mats * rows * c8 * 2);
   if (!a.dry && *status == MOE_OK) {
@@ -143,7 +145,31 @@ static GemmArgs gemm_args(const moe_expert_rows &r, int64_t rows, bool gather) {
   g.r = {r.counts, r.padded_offsets, r.m_indices, gather ? r.row_entry : nullptr, rows,
          r.num_experts, r.top_k};
   g.segs = 1;
+  // entry / top_k for entries below 2^31: magic = ceil(2^(31 + s) / top_k) with
+  // s = ceil(log2 top_k) fits 32 bits, and the product's error stays below 1
+  if (gather && r.top_k > 1) {
+    int s = 1;
+    while ((int64_t)1 << s < r.top_k) ++s;
+    g.top_k_magic = (uint32_t)((((uint64_t)1 << (31 + s)) + r.top_k - 1) / r.top_k);
+    g.top_k_shift = s - 1;
+  }
   return g;
+}
+// Gathered rows are addressed by 32-bit offsets from x. Where x is larger
+// than that its rows are gathered into the workspace first.
+static bool is_wide(const moe_matrix &x, int64_t tokens) {
+  return tokens * x.ld * 2 >= 0xfffff000ll;
+}
+static Operand gathered(const moe_matrix &x, int64_t tokens, int cols, const Rows &r,
+                        int64_t rows, Arena &a, hipStream_t st, int *status) {
+  const int c8 = round8(cols);
+  uint16_t *dst = a.take((size_t)rows * c8 * 2);
+  if (!a.dry && *status == MOE_OK) {
+    gather_rows_kernel<<<row_grid(rows, c8, 1), dim3(COL_THREADS, ROW_THREADS), 0, st>>>(
+        (const uint16_t *)x.p, x.ld, tokens, cols, rows, r, dst, c8);
+    *status = hip_status();
+  }
+  return {dst, c8, 0};
 }
 static void set_b0(GemmArgs &g, const Operand &b) {
   g.b0 = b.p, g.ldb0 = b.ld, g.b_stride0 = b.stride;
@@ -163,12 +189,21 @@ static int run_gated(const moe_gated_ffn_args *a, Arena &ws, hipStream_t st) {
   const int mats = mats_of(a->rows), H = a->hidden, F = a->inter;
   int status = MOE_OK;
   if (rows == 0) return MOE_OK;
-  const Operand x = operand(a->x, a->tokens, H, 1, ws, st, &status);
+  const bool gather = a->rows.num_experts > 0 && a->rows.row_entry;
+  GemmArgs g = gemm_args(a->rows, rows, gather);
+  g.a_rows = a->tokens;
+  Operand x;
+  if (gather && is_wide(a->x, a->tokens)) {
+    x = gathered(a->x, a->tokens, H, g.r, rows, ws, st, &status);
+    g.r.row_entry = nullptr;
+    g.a_rows = rows;
+  } else {
+    x = operand(a->x, a->tokens, H, 1, ws, st, &status);
+  }
   const Operand wg = operand(a->w_gate, F, H, mats, ws, st, &status);
   const Operand wu = operand(a->w_up, F, H, mats, ws, st, &status);
   if (ws.dry || status != MOE_OK) return status;
-  GemmArgs g = gemm_args(a->rows, rows, a->rows.num_experts > 0);
-  g.a = x.p, g.lda = x.ld, g.a_rows = a->tokens;
+  g.a = x.p, g.lda = x.ld;
   set_b0(g, wg);
   set_b1(g, wu);
   set_c0(g, a->h);
@@ -184,13 +219,18 @@ static int run_gated_backward(const moe_gated_ffn_args *a, Arena &ws, hipStream_
   int status = MOE_OK;
   uint16_t *dz = ws.take((size_t)rows * 2 * Fa * 2);
   Operand x = {}, wg = {}, wu = {};
-  if (a->dw_gate.p) x = operand(a->x, a->tokens, H, 1, ws, st, &status);
+  GemmArgs g = gemm_args(a->rows, rows, gather);
+  const bool wide = gather && is_wide(a->x, a->tokens);
+  if (a->dw_gate.p && wide) x = gathered(a->x, a->tokens, H, g.r, rows, ws, st, &status);
+  if (a->dw_gate.p && !wide) x = operand(a->x, a->tokens, H, 1, ws, st, &status);
   if (a->dx.p && rows > 0) {
-    wg = operand(a->w_gate, F, H, mats, ws, st, &status);
-    wu = operand(a->w_up, F, H, mats, ws, st, &status);
+    // the product goes from one weight to the other with the same offsets
+    const bool copy = !is_aligned(a->w_gate, H, mats) || !is_aligned(a->w_up, H, mats) ||
+                      a->w_gate.ld != a->w_up.ld;
+    wg = operand(a->w_gate, F, H, mats, ws, st, &status, copy);
+    wu = operand(a->w_up, F, H, mats, ws, st, &status, copy);
   }
   if (ws.dry || status != MOE_OK) return status;
-  GemmArgs g = gemm_args(a->rows, rows, gather);
   if (rows > 0) {
     const dim3 grid = row_grid(rows, Fa, 1), block(COL_THREADS, ROW_THREADS);
     const auto kernel = a->dtype == MOE_BF16 ? gated_dz_kernel<Bf16> : gated_dz_kernel<F16>;
@@ -212,7 +252,8 @@ static int run_gated_backward(const moe_gated_ffn_args *a, Arena &ws, hipStream_
   }
   if (a->dw_gate.p) {
     set_b0(g, x);
-    g.a_rows = a->tokens;
+    g.a_rows = wide ? rows : a->tokens;
+    if (wide) g.r.row_entry = nullptr;
     set_c0(g, a->dw_gate);
     set_c1(g, a->dw_up);
     g.M = F, g.N = H, g.K = (int)rows;

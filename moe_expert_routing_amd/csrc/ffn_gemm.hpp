@@ -30,6 +30,7 @@
 #pragma once
 
 #include <type_traits>
+#include <utility>
 
 #include "ffn_types.hpp"
 
@@ -39,44 +40,52 @@ typedef __attribute__((address_space(3))) void *lds_ptr_t;
 typedef __attribute__((address_space(3))) s16x4 *lds_s16x4_ptr_t;
 typedef __attribute__((address_space(1))) void *gbl_ptr_t;
 
-constexpr int TK = 64;  // k per stage
+#define MOE_INLINE __attribute__((always_inline))  // the kernel's lambdas hold its registers
 
-// 16 bytes of zeros that out-of-range pieces are loaded from
-__device__ const uint4 zero_piece = {0, 0, 0, 0};
+// Offset past a buffer's end: loads zeros.
+constexpr uint32_t PAST = 0xffffffffu;
 
-template <int BM_, int BN_, int WM_, int WN_, int NS_, int BLOCKS_>
+// The device pass alone knows the buffer builtins.
+#if defined(__HIP_DEVICE_COMPILE__)
+// Buffer of 4 GB - 1 at p: 32-bit unsigned byte offsets from a uniform base.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const uint8_t *p) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, PAST, 0x00020000);
+}
+#endif
+
+template <int BM_, int BN_, int WM_, int WN_, int TK_, int NS_, int BLOCKS_>
 struct Tile {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, TK = TK_, NS = NS_;
   static constexpr int BLOCKS = BLOCKS_;  // blocks per compute unit
   static constexpr int WAVES_N = BN / WN, NW = (BM / WM) * WAVES_N;
   static constexpr int NTHREADS = 64 * NW;
-  static constexpr int FM = WM / 16, FN = WN / 16;
-  static constexpr int A_INSTR = BM / 8, B_INSTR = BN / 8;  // 1 KB loads per stage
-  static constexpr int INSTR = A_INSTR + B_INSTR;
-  static constexpr int LOADS = (INSTR + NW - 1) / NW;        // most of one wave
-  static constexpr int LOADS_MIN = INSTR / NW;               // of every wave
+  static constexpr int FM = WM / 16, FN = WN / 16, KS = TK / 32;
+  static constexpr int A_INSTR = BM * TK / 512, B_INSTR = BN * TK / 512;  // 1 KB pieces
+  // pieces of one wave, where they do not come out even the most; and what
+  // every wave has at least
+  static constexpr int A_LOADS = (A_INSTR + NW - 1) / NW, B_LOADS = (B_INSTR + NW - 1) / NW;
+  static constexpr int LOADS = A_LOADS + B_LOADS, LOADS_MIN = A_INSTR / NW + B_INSTR / NW;
   static constexpr int A_BYTES = BM * TK * 2, STAGE_BYTES = (BM + BN) * TK * 2;
+  static_assert(TK == 32 || TK == 64, "one or two MFMA k-steps in a stage");
+  static_assert(A_INSTR * 512 == BM * TK && B_INSTR * 512 == BN * TK, "whole pieces");
   static_assert((NS - 2) * LOADS_MIN <= 63, "vmcnt range");
+  static_assert(BLOCKS * NS * STAGE_BYTES <= 160 * 1024, "LDS of a compute unit");
 };
+
+// f(0) .. f(N - 1) with compile-time arguments: unrolled whatever the size.
+template <class F, int... I>
+__device__ __forceinline__ void unrolled(F &&f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void unrolled(F &&f) {
+  unrolled(f, std::make_integer_sequence<int, N>());
+}
 
 template <int N>
 __device__ __forceinline__ void wait_vmcnt_imm() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
-// s_waitcnt vmcnt(k * STEP) for a run-time k in [0, MAXK]
-template <int STEP, int MAXK>
-__device__ __forceinline__ void wait_vmcnt_steps(int k) {
-  if constexpr (MAXK > 0) {
-    if (k >= MAXK) {
-      wait_vmcnt_imm<MAXK * STEP>();
-      return;
-    }
-    wait_vmcnt_steps<STEP, MAXK - 1>(k);
-  } else {
-    wait_vmcnt_imm<0>();
-  }
-}
-
 // Position of 16-byte chunk c in k-row k of an operand staged as it lies in
 // memory, R columns wide.
 template <int R>
@@ -100,38 +109,11 @@ __device__ __forceinline__ void tile_of_block(int b, int total, int m_tiles, int
   nt = t / size;
 }
 
-template <class D>
-__device__ __forceinline__ void store4(uint16_t *p, f32x4 v, int left, bool vec) {
-  const s16x4 w = pack4<D>(v);
-  if (vec && left >= 4) {
-    *reinterpret_cast<s16x4 *>(p) = w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < left) p[i] = (uint16_t)w[i];
-  }
-}
-template <class D>
-__device__ __forceinline__ f32x4 load4(const uint16_t *p, int left, bool vec) {
-  s16x4 w = {0, 0, 0, 0};
-  if (vec && left >= 4) {
-    w = *reinterpret_cast<const s16x4 *>(p);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < left) w[i] = (short)p[i];
-  }
-  return unpack4<D>(w);
-}
-// whether 4 consecutive elements at a multiple-of-4 column are one aligned load
-__device__ __forceinline__ bool vec4(const void *p, int64_t ld, int64_t stride = 0) {
-  return (((uintptr_t)p & 7) | (uintptr_t)((ld | stride) & 3)) == 0;
-}
-
-template <class D, int MODE, class C>
+template <class D, int MODE, class C, bool GATHER>
 __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm_kernel(
     const GemmArgs g) {
-  constexpr int BM = C::BM, BN = C::BN, NS = C::NS;
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int BM = C::BM, BN = C::BN, NS = C::NS, TK = C::TK;
   constexpr bool A_TR = MODE == WGRAD, B_TR = MODE == DGRAD || MODE == WGRAD;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * C::STAGE_BYTES];
   const int lane = threadIdx.x & 63;
@@ -188,101 +170,136 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
   const int nk = seg_stages * (MODE == DGRAD ? g.segs : 1);
   // last 8-element piece of an operand whose m or n is contiguous
   const int m_last = ((g.M + 7) & ~7) - 8, n_last = ((g.N + 7) & ~7) - 8;
-  const bool gather = (MODE == GATED || MODE == WGRAD) && g.r.row_entry != nullptr;
+  const uint32_t magic = g.top_k_magic, shift = g.top_k_shift;
+  auto gathered_row = [&](int32_t entry) MOE_INLINE {  // a bad entry reads row 0, in bounds
+    const uint32_t t = magic ? __umulhi((uint32_t)entry, magic) >> shift : (uint32_t)entry;
+    return t < (uint64_t)g.a_rows ? t : 0u;
+  };
 
-  // Load q of this wave is piece id = q * NW + wave of the stage: 1 KB, the A
-  // pieces first. Per lane: where it reads next, how far one stage is, and
-  // the k of its 8 elements within a stage.
-  const uint16_t *src[C::LOADS];
-  int kpos[C::LOADS];
-  auto start = [&](int seg) {
+  // Where this wave's pieces come from. A piece is 1 KB, 16 bytes a lane:
+  // number q * NW + wave of the A side for q < A_LOADS, of the B side after
+  // those. A lane reads at the operand's base of the stage (uniform, advanced
+  // by a stage at a time) plus off[q] bytes.
+  auto is_a = [&](int q) MOE_INLINE { return q < C::A_LOADS; };
+  auto number = [&](int q) MOE_INLINE {
+    return (is_a(q) ? q : q - C::A_LOADS) * C::NW + wave;
+  };
+  auto exists = [&](int q) MOE_INLINE {
+    return is_a(q) ? C::A_INSTR % C::NW == 0 || number(q) < C::A_INSTR
+                   : C::B_INSTR % C::NW == 0 || number(q) < C::B_INSTR;
+  };
+  // GATED: B rows alternate, 16 of the gate's and 16 of the other's. A wave's
+  // pieces are all of one projection.
+  constexpr int PIECE_ROWS = 512 / TK;
+  static_assert(MODE != GATED || C::NW * PIECE_ROWS % 32 == 0, "one projection for a wave");
+  const bool up = MODE == GATED && ((wave * PIECE_ROWS) >> 4 & 1);
+  const int64_t ldb = up ? g.ldb1 : g.ldb0;
+  const uint8_t *a_base, *b_base, *b_next = nullptr;
+  int64_t a_step, b_step;
+  if constexpr (A_TR) {
+    a_base = reinterpret_cast<const uint8_t *>(g.a + k_row0 * g.lda + seg0 * g.a_seg);
+    a_step = TK * g.lda * 2;
+  } else {
+    a_base = reinterpret_cast<const uint8_t *>(g.a + (GATHER ? 0 : m0 * g.lda));
+    a_step = TK * 2;
+  }
+  if constexpr (MODE == WGRAD) {
+    b_base = reinterpret_cast<const uint8_t *>(b0 + (GATHER ? 0 : k_row0 * ldb));
+    b_step = GATHER ? 0 : TK * ldb * 2;
+  } else if constexpr (MODE == DGRAD) {
+    b_base = reinterpret_cast<const uint8_t *>(b0);
+    b_next = reinterpret_cast<const uint8_t *>(b1);
+    b_step = TK * ldb * 2;
+  } else {
+    b_base = reinterpret_cast<const uint8_t *>((up ? b1 : b0) + n0 * ldb);
+    b_step = TK * 2;
+  }
+  // (row, 8-element chunk) of a lane in piece `id` of an operand with
+  // contiguous k. 64 k: 128-byte rows, chunk c at c ^ (row & 7). 32 k: two
+  // rows in a 128-byte line, the line's chunk c at c ^ (line & 7).
+  auto row_chunk = [&](int id, int &row, int &c) MOE_INLINE {
+    if constexpr (TK == 64) {
+      row = id * 8 + (lane >> 3);
+      c = (lane & 7) ^ (lane >> 3);
+    } else {
+      const int line = lane >> 3, c8 = (lane & 7) ^ line;
+      row = id * 16 + line * 2 + (c8 >> 2);
+      c = c8 & 3;
+    }
+  };
+  uint32_t off[C::LOADS];
+  auto start = [&]() MOE_INLINE {
 #pragma unroll
     for (int q = 0; q < C::LOADS; ++q) {
-      const int id = q * C::NW + wave;
-      if (id < C::A_INSTR) {
-        if constexpr (A_TR) {
-          constexpr int PER = BM / 8, KR = 64 / PER;  // chunks in a k-row, k-rows of a piece
-          const int k = id * KR + lane / PER, c = (lane % PER) ^ swz<BM>(k);
-          kpos[q] = k;
-          src[q] = g.a + (k_row0 + k) * g.lda + seg0 * g.a_seg + min(m0 + c * 8, m_last);
-        } else {
-          const int r = id * 8 + (lane >> 3), c = (lane & 7) ^ (lane >> 3);
-          int64_t row = min(m0 + r, g.M - 1);
-          if (gather) {
-            const uint32_t tok = (uint32_t)g.r.row_entry[row] / (uint32_t)g.r.top_k;
-            row = tok < (uint64_t)g.a_rows ? tok : 0;
-          }
-          kpos[q] = c * 8;
-          src[q] = g.a + row * g.lda + seg * g.a_seg + c * 8;
-        }
+      const int id = number(q);
+      if (is_a(q) && A_TR) {
+        constexpr int PER = BM / 8;  // chunks of a k-row
+        const int k = (id * 64 + lane) / PER, c = (lane % PER) ^ swz<BM>(k);
+        off[q] = (uint32_t)(k * g.lda + min(m0 + c * 8, m_last)) * 2;
+      } else if (is_a(q)) {
+        int r, c;
+        row_chunk(id, r, c);
+        const int row = min(m0 + r, g.M - 1);
+        const int64_t at = GATHER ? gathered_row(g.r.row_entry[row]) : row - m0;
+        off[q] = (uint32_t)(at * g.lda + c * 8) * 2;
+      } else if (B_TR) {
+        constexpr int PER = BN / 8;
+        const int k = (id * 64 + lane) / PER, c = (lane % PER) ^ swz<BN>(k);
+        // gathered: the row is added when its entry is known
+        off[q] = (uint32_t)((MODE == WGRAD && GATHER ? 0 : k * ldb) + min(n0 + c * 8, n_last)) * 2;
       } else {
-        const int ib = id - C::A_INSTR;
-        if constexpr (B_TR) {
-          constexpr int PER = BN / 8, KR = 64 / PER;
-          const int k = ib * KR + lane / PER, c = (lane % PER) ^ swz<BN>(k);
-          kpos[q] = k;
-          const bool second = MODE == DGRAD && seg;
-          src[q] = (second ? b1 : b0) + (k_row0 + k) * (second ? g.ldb1 : g.ldb0) +
-                   min(n0 + c * 8, n_last);
-        } else {
-          const int j = ib * 8 + (lane >> 3), c = (lane & 7) ^ (lane >> 3);
-          kpos[q] = c * 8;
-          if constexpr (MODE == GATED) {  // 16 gate rows, their 16 up rows, ...
-            const int f = min(n0 + (j >> 5) * 16 + (j & 15), g.N - 1);
-            const bool up = (j >> 4) & 1;
-            src[q] = (up ? b1 : b0) + f * (up ? g.ldb1 : g.ldb0) + c * 8;
-          } else {
-            src[q] = b0 + min(n0 + j, g.N - 1) * g.ldb0 + c * 8;
-          }
-        }
+        int j, c;
+        row_chunk(id, j, c);
+        if (MODE == GATED) j = (j >> 5) * 16 + (j & 15);
+        off[q] = (uint32_t)(min(j, g.N - 1 - n0) * ldb + c * 8) * 2;
       }
     }
   };
-  // WGRAD with gathered x: the tokens of the next stage's rows
-  int32_t entry[C::LOADS];
-  auto fetch_entries = [&](int s) {
-    if constexpr (MODE == WGRAD) {
-      if (gather) {
+  // Whether piece q of a stage with `left` k from its start on lies past them:
+  // such pieces, a stage's tail or stages after the last, load zeros.
+  int k_chunk, c_row;
+  row_chunk(0, c_row, k_chunk);
+  auto past = [&](int q, int left) MOE_INLINE {
+    if (is_a(q) && A_TR) return lane / (BM / 8) >= left - number(q) * (512 / BM);
+    if (!is_a(q) && B_TR) return lane / (BN / 8) >= left - number(q) * (512 / BN);
+    return k_chunk * 8 >= left;
+  };
+  // WGRAD with gathered x: the entries of the next stage's rows
+  int32_t entry[C::B_LOADS];
+  auto fetch_entries = [&](int s) MOE_INLINE {
+    if constexpr (MODE == WGRAD && GATHER) {
 #pragma unroll
-        for (int q = 0; q < C::LOADS; ++q)
-          if (q * C::NW + wave >= C::A_INSTR)
-            entry[q] = g.r.row_entry[k_row0 + min(s * TK + kpos[q], K - 1)];
+      for (int q = C::A_LOADS; q < C::LOADS; ++q) {
+        const int k = number(q) * (512 / BN) + lane / (BN / 8);
+        entry[q - C::A_LOADS] = g.r.row_entry[k_row0 + min(s * TK + k, K - 1)];
       }
     }
   };
-  const uint16_t *zeros = reinterpret_cast<const uint16_t *>(&zero_piece);
-  // Stages are issued in order, each once.
-  auto issue = [&](int s) {
-    uint8_t *base = smem + (s % NS) * C::STAGE_BYTES;
-    int ls = s;
-    int64_t ldb = g.ldb0;
-    if (MODE == DGRAD && g.segs > 1 && s >= seg_stages) {
-      ls = s - seg_stages;
-      ldb = g.ldb1;
-      if (ls == 0) start(1);
-    }
-    const bool tail = (ls + 1) * TK > K;
-#pragma unroll
-    for (int q = 0; q < C::LOADS; ++q) {
-      const int id = q * C::NW + wave;
-      if (C::INSTR % C::NW != 0 && id >= C::INSTR) break;
-      const uint16_t *p = src[q];
-      const bool is_a = id < C::A_INSTR;
-      if constexpr (MODE == WGRAD) {
-        if (gather && !is_a) {
-          const uint32_t tok = (uint32_t)entry[q] / (uint32_t)g.r.top_k;
-          // src holds the column in row 0 .. of x: rebuilt from the token
-          p = tok < (uint64_t)g.a_rows
-                  ? g.b0 + (int64_t)tok * ldb +
-                        min(n0 + ((lane % (BN / 8)) ^ swz<BN>(kpos[q])) * 8, n_last)
-                  : zeros;
-        }
-      }
-      if (tail && ls * TK + kpos[q] >= K) p = zeros;
-      __builtin_amdgcn_global_load_lds((gbl_ptr_t)p, (lds_ptr_t)(base + id * 1024), 16, 0, 0);
-      src[q] += is_a ? (A_TR ? TK * g.lda : TK) : (B_TR ? TK * ldb : TK);
-    }
+  // Stages are issued in order, each followed by next_stage.
+  int left = K;  // of the segment, from the next stage to be issued on
+  auto issue_piece = [&](int s, int q) MOE_INLINE {
+    if (!exists(q)) return;
+    uint32_t o = off[q];
+    if (MODE == WGRAD && GATHER && !is_a(q))
+      o += (uint32_t)(gathered_row(entry[q - C::A_LOADS]) * ldb) * 2;
+    o = past(q, left) ? PAST : o;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        buffer_at(is_a(q) ? a_base : b_base),
+        (lds_ptr_t)(smem + (s % NS) * C::STAGE_BYTES + (is_a(q) ? 0 : C::A_BYTES) +
+                    number(q) * 1024),
+        16, o, 0, 0, 0);
+  };
+  auto next_stage = [&](int s) MOE_INLINE {  // after stage s
     fetch_entries(s + 1);
+    a_base += a_step;
+    b_base += b_step;
+    left -= TK;
+    if (MODE == DGRAD) {
+      const bool second = g.segs > 1 && s + 1 == seg_stages;
+      a_base = second ? reinterpret_cast<const uint8_t *>(g.a + m0 * g.lda + g.a_seg) : a_base;
+      b_base = second ? b_next : b_base;
+      left = second ? K : left;
+    }
   };
 
   f32x4 acc[C::FM][C::FN];
@@ -295,155 +312,227 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
   const int fr = lane & 15, fq = lane >> 4;
 
   s16x8 fa[2][C::FM], fb[2][C::FN];
-  // one operand's fragment of 16 rows (columns) x 32 k at k-step ks
-  auto frag_k = [&](const uint8_t *t, int row, int ks) {
-    return *reinterpret_cast<const s16x8 *>(t + (row + fr) * 128 +
-                                            (((ks * 4 + fq) ^ (fr & 7)) * 16));
+  auto frag_k = [&](const uint8_t *t, int row, int ks) MOE_INLINE {
+    if constexpr (TK == 64)
+      return *reinterpret_cast<const s16x8 *>(t + (row + fr) * 128 +
+                                              (((ks * 4 + fq) ^ (fr & 7)) * 16));
+    else
+      return *reinterpret_cast<const s16x8 *>(
+          t + (row + fr) * 64 - (fr & 1) * 64 + ((((fr & 1) * 4 + fq) ^ ((fr >> 1) & 7)) * 16));
   };
-  auto frag_tr = [&](const uint8_t *t, int col, int ks, auto width) {
+  auto frag_tr = [&](const uint8_t *t, uint32_t lane_off, int f, int ks, auto width) MOE_INLINE {
     constexpr int R = decltype(width)::value;
-    s16x8 f;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k = ks * 32 + fq * 8 + h * 4 + (fr >> 2);
-      const int c = (col >> 3) + ((fr & 3) >> 1);
-      const uint8_t *p = t + k * (R * 2) + ((c ^ swz<R>(k)) * 16) + (fr & 1) * 8;
-      const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr_t)p);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[h * 4 + i] = v[i];
-    }
-    return f;
+    const uint8_t *p = t + (lane_off ^ (f * 32)) + ks * 32 * (R * 2);
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr_t)p);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr_t)(p + 4 * (R * 2)));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
-  auto read_frags = [&](int s, int ks, int set) {
+  // a lane's k-row and swizzled chunk of the first fragment, transposed reads
+  auto lane_tr = [&](int first, auto width) MOE_INLINE {
+    constexpr int R = decltype(width)::value;
+    const int k = fq * 8 + (fr >> 2);
+    return (uint32_t)(k * (R * 2) + (((first >> 3) + ((fr & 3) >> 1)) ^ swz<R>(k)) * 16 +
+                      (fr & 1) * 8);
+  };
+  const uint32_t a_lane = lane_tr(wm, std::integral_constant<int, BM>());
+  const uint32_t b_lane = lane_tr(wn, std::integral_constant<int, BN>());
+  // fragment f of a k-step: the N side's first, then the M side's
+  auto read_frag = [&](int s, int ks, int set, int f) MOE_INLINE {
     const uint8_t *As = smem + (s % NS) * C::STAGE_BYTES, *Bs = As + C::A_BYTES;
-#pragma unroll
-    for (int i = 0; i < C::FM; ++i)
+    if (f < C::FN) {
+      if constexpr (B_TR)
+        fb[set][f] = frag_tr(Bs, b_lane, f, ks, std::integral_constant<int, BN>());
+      else
+        fb[set][f] = frag_k(Bs, wn + 16 * f, ks);
+    } else {
+      const int i = f - C::FN;
       if constexpr (A_TR)
-        fa[set][i] = frag_tr(As, wm + 16 * i, ks, std::integral_constant<int, BM>());
+        fa[set][i] = frag_tr(As, a_lane, i, ks, std::integral_constant<int, BM>());
       else
         fa[set][i] = frag_k(As, wm + 16 * i, ks);
-#pragma unroll
-    for (int j = 0; j < C::FN; ++j)
-      if constexpr (B_TR)
-        fb[set][j] = frag_tr(Bs, wn + 16 * j, ks, std::integral_constant<int, BN>());
-      else
-        fb[set][j] = frag_k(Bs, wn + 16 * j, ks);
+    }
   };
-  // The wait in stage_ready has drained this set's LDS reads, which the
+  // The wait in wait_stage has drained this set's LDS reads, which the
   // compiler cannot see: naming the registers here keeps it from waiting
   // for the next set's reads as well.
-  auto settle = [&](int set) {
+  auto settle = [&](int set) MOE_INLINE {
 #pragma unroll
     for (int i = 0; i < C::FM; ++i) asm volatile("" : "+v"(fa[set][i]));
 #pragma unroll
     for (int j = 0; j < C::FN; ++j) asm volatile("" : "+v"(fb[set][j]));
   };
-  auto mfmas = [&](int set) {
+  // One MFMA k-step on `set`. Between the MFMAs, one at a time, go the fragment
+  // reads of k-step rks of stage rs (over the first three quarters) and, with
+  // ISSUE, the pieces of stage `is`: an MFMA holds its pipe for 16 cycles, in
+  // which the wave can issue the few other instructions.
+  auto step = [&](int set, int rs, int rks, auto issue_tag, int is) MOE_INLINE {
+    constexpr bool ISSUE = decltype(issue_tag)::value;
+    constexpr int FRAGS = C::FM + C::FN, MFMAS = C::FM * C::FN;
+    constexpr int SPAN = MFMAS > FRAGS ? MFMAS * 3 / 4 : MFMAS;
+    unrolled<MFMAS>([&](auto tc) MOE_INLINE {
+      constexpr int t = decltype(tc)::value, i = t / C::FN, j = t % C::FN;
+      // read f goes before MFMA f * SPAN / FRAGS, piece q before q * MFMAS / LOADS
+      constexpr int F0 = (t * FRAGS + SPAN - 1) / SPAN, F1 = ((t + 1) * FRAGS + SPAN - 1) / SPAN;
 #pragma unroll
-    for (int i = 0; i < C::FM; ++i)
+      for (int f = F0; f < (F1 < FRAGS ? F1 : FRAGS); ++f) read_frag(rs, rks, set ^ 1, f);
+      if constexpr (ISSUE) {
+        constexpr int Q0 = (t * C::LOADS + MFMAS - 1) / MFMAS,
+                      Q1 = ((t + 1) * C::LOADS + MFMAS - 1) / MFMAS;
 #pragma unroll
-      for (int j = 0; j < C::FN; ++j) acc[i][j] = D::mfma(fb[set][j], fa[set][i], acc[i][j]);
+        for (int q = Q0; q < (Q1 < C::LOADS ? Q1 : C::LOADS); ++q) issue_piece(is, q);
+      }
+      acc[i][j] = D::mfma(fb[set][j], fa[set][i], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    if constexpr (ISSUE) next_stage(is);
   };
-  // Stage s has landed for every wave, and every wave has read the buffer
-  // that the next issue fills.
-  auto stage_ready = [&](int s) {
-    wait_vmcnt_steps<C::LOADS_MIN, NS - 2>(min(NS - 2, nk - 1 - s));
+  // The oldest stage in flight has landed for every wave (NS - 2 younger ones
+  // may not have), and every wave has read the buffer that is filled next.
+  auto wait_stage = [&]() MOE_INLINE {
+    wait_vmcnt_imm<C::LOADS_MIN *(NS - 2)>();
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (s + NS - 1 < nk) issue(s + NS - 1);
+  };
+  // A stage's k-steps; the last one reads the next stage's first fragments and
+  // issues the stage NS ahead. After the last stage both go on with zeros,
+  // so that the loop has no branches.
+  auto stage = [&](int s, int set) MOE_INLINE {
+    if constexpr (C::KS == 2) step(0, s, 1, std::false_type(), 0);
+    wait_stage();
+    settle(set);
+    step(set, s + 1, 0, std::true_type(), s + NS);
   };
 
   if (nk > 0) {
-    start(0);
+    start();
     fetch_entries(0);
+#pragma unroll 1
+    for (int s = 0; s < NS; ++s) {
+      if (s == NS - 1) wait_stage();
 #pragma unroll
-    for (int s = 0; s < NS - 1; ++s)
-      if (s < nk) issue(s);
-    stage_ready(0);
-    read_frags(0, 0, 0);
-    for (int s = 0; s < nk; ++s) {
-      read_frags(s, 1, 1);
-      mfmas(0);
-      if (s + 1 < nk) {
-        stage_ready(s + 1);
-        settle(1);
-        read_frags(s + 1, 0, 0);
+      for (int q = 0; q < C::LOADS; ++q) issue_piece(s, q);
+      next_stage(s);
+    }
+#pragma unroll
+    for (int f = 0; f < C::FM + C::FN; ++f) read_frag(0, 0, 0, f);
+    if constexpr (C::KS == 2) {
+#pragma unroll 1
+      for (int s = 0; s < nk; ++s) stage(s, 1);
+    } else {  // the register sets alternate by stage
+#pragma unroll 1
+      for (int s = 0; s < nk; s += 2) {
+        stage(s, 0);
+        stage(s + 1, 1);
       }
-      mfmas(1);
     }
   }
 
-  // Lane: row m = fr, columns n = 4 fq .. 4 fq + 3 of every 16 x 16 tile.
-  if constexpr (MODE == WGRAD) {
-    uint16_t *c = seg0 ? g.c1 + e * g.c_stride1 : g.c0 + e * g.c_stride0;
-    const int64_t ldc = seg0 ? g.ldc1 : g.ldc0;
-    const bool vec = vec4(c, ldc);
+  // Epilogue. A lane holds row fr and columns 4 fq .. 4 fq + 3 of every 16 x 16
+  // tile. Each wave turns 16 rows at a time through LDS of its own (fp32, 16-byte
+  // chunk c of row r at c ^ r) so that a lane gets 8 consecutive columns of
+  // a row: 16-byte loads and stores that fill whole lines, and the epilogue's
+  // column vectors stay the same for all rows.
+  wait_vmcnt_imm<0>();  // the zeros still on their way to LDS
+  __syncthreads();
+  constexpr int OUT = MODE == GATED ? C::WN / 2 : C::WN;  // columns of a wave
+  constexpr int CH = OUT / 4, LPR = OUT / 8;               // chunks, lanes in a row
+  constexpr int PASSES = LPR > 4 ? LPR / 4 : 1, ROWS = 16 / PASSES;
+  static_assert(C::NW * 16 * OUT * 4 <= NS * C::STAGE_BYTES, "the waves' LDS");
+  float *turn_lds = reinterpret_cast<float *>(smem) + wave * (16 * OUT);
+  const int tr = lane / LPR, tc = lane % LPR;  // row of a pass, 8-column run
+  const bool on = LPR * 16 >= 64 || lane < LPR * 16;
+  auto turn_in = [&](int j, f32x4 v) MOE_INLINE {
+    *reinterpret_cast<f32x4 *>(turn_lds + fr * OUT + (((4 * j + fq) ^ fr) & (CH - 1)) * 4) = v;
+  };
+  auto turn_out = [&](int p) MOE_INLINE {
+    const int r = (p * ROWS + tr) & 15;
+    const float *row = turn_lds + r * OUT;
+    const f32x4 a = *reinterpret_cast<const f32x4 *>(row + (((2 * tc) ^ r) & (CH - 1)) * 4);
+    const f32x4 b = *reinterpret_cast<const f32x4 *>(row + (((2 * tc + 1) ^ r) & (CH - 1)) * 4);
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  // LDS keeps a wave's accesses in order; the compiler must too, between what
+  // other lanes wrote and this lane reads.
+  auto turn_order = [&]() MOE_INLINE {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+  };
+  const int n = n0 + (MODE == GATED ? wn >> 1 : wn) + tc * 8;  // this lane's columns
+  const bool cols = on && n < g.N;
+  auto row_of = [&](int i, int p) MOE_INLINE {
+    return (int64_t)m0 + wm + 16 * i + p * ROWS + tr;
+  };
+  auto is_real = [&](int64_t m) MOE_INLINE {
+    return !grouped || MODE == WGRAD || g.r.m_indices[m] == e;
+  };
+  const f32x8 zero8 = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  uint16_t *out = MODE == WGRAD ? (seg0 ? g.c1 + e * g.c_stride1 : g.c0 + e * g.c_stride0) : g.c0;
+  const int64_t ldc = MODE == WGRAD && seg0 ? g.ldc1 : g.ldc0;
+  const bool vec_c = vec8(out, ldc), vec_p = vec8(g.pre, g.ldp), vec_u = vec8(g.pre, g.ldp, g.N);
+  const bool vec_r = vec8(g.res, g.ldr);
+  if constexpr (MODE == GATED) {
+    // what is turned: h, and with pre the two projections as well
+    auto rows_out = [&](int i, auto value, uint16_t *to, int64_t ld, int width, int col, bool vec)
+        MOE_INLINE {
+      turn_order();
+#pragma unroll
+      for (int j = 0; j < C::FN / 2; ++j) turn_in(j, value(acc[i][2 * j], acc[i][2 * j + 1]));
+      turn_order();
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        const f32x8 v = turn_out(p);
+        const int64_t m = row_of(i, p);
+        if (cols && m < g.M)
+          store8<D>(to + m * ld, col, width, vec, is_real(m) ? v : zero8);
+      }
+    };
 #pragma unroll
     for (int i = 0; i < C::FM; ++i) {
-      const int m = m0 + wm + 16 * i + fr;
-      if (m >= g.M) continue;
+      rows_out(i, [&](f32x4 gt, f32x4 up4) MOE_INLINE {
+        f32x4 h;
 #pragma unroll
-      for (int j = 0; j < C::FN; ++j) {
-        const int n = n0 + wn + 16 * j + 4 * fq;
-        if (n < g.N) store4<D>(c + m * ldc + n, acc[i][j], g.N - n, vec);
+        for (int v = 0; v < 4; ++v) h[v] = act_value(gt[v], g.act) * up4[v];
+        return h;
+      }, out, ldc, g.N, n, vec_c);
+      if (g.pre) {
+        rows_out(i, [&](f32x4 gt, f32x4) MOE_INLINE { return gt; }, g.pre, g.ldp, g.N, n, vec_p);
+        rows_out(i, [&](f32x4, f32x4 up4) MOE_INLINE { return up4; }, g.pre + g.N, g.ldp, g.N, n,
+                 vec_u);
       }
     }
   } else {
-    const bool vec_c = vec4(g.c0, g.ldc0), vec_p = vec4(g.pre, g.ldp, g.N);
-    const bool vec_r = vec4(g.res, g.ldr);
-    const uint16_t *bias = g.bias ? g.bias + e * g.bias_stride : nullptr;
+    f32x8 bias = zero8;
+    if (MODE == LINEAR && g.bias && cols) bias = load8<D>(g.bias + e * g.bias_stride, n, g.N, false);
 #pragma unroll
     for (int i = 0; i < C::FM; ++i) {
-      const int64_t m = m0 + wm + 16 * i + fr;
-      if (m >= g.M) continue;
-      const bool real = !grouped || g.r.m_indices[m] == e;
-      if constexpr (MODE == GATED) {
+      turn_order();
 #pragma unroll
-        for (int j = 0; j < C::FN / 2; ++j) {
-          const int n = n0 + (wn >> 1) + 16 * j + 4 * fq, left = g.N - n;
-          if (left <= 0) continue;
-          f32x4 gt = acc[i][2 * j], up = acc[i][2 * j + 1], h;
+      for (int j = 0; j < C::FN; ++j) turn_in(j, acc[i][j]);
+      turn_order();
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            if (!real) gt[v] = up[v] = 0.f;
-            h[v] = real ? act_value(gt[v], g.act) * up[v] : 0.f;
+      for (int p = 0; p < PASSES; ++p) {
+        f32x8 z = turn_out(p);
+        const int64_t m = row_of(i, p);
+        if (!cols || m >= g.M) continue;
+        const bool real = is_real(m);
+        if constexpr (MODE == LINEAR) {
+#pragma unroll
+          for (int v = 0; v < 8; ++v) z[v] += bias[v];
+          if (g.pre) store8<D>(g.pre + m * g.ldp, n, g.N, vec_p, real ? z : zero8);
+          if (g.act != MOE_ACT_NONE) {
+#pragma unroll
+            for (int v = 0; v < 8; ++v) z[v] = act_value(z[v], g.act);
           }
-          store4<D>(g.c0 + m * g.ldc0 + n, h, left, vec_c);
-          if (g.pre) {
-            store4<D>(g.pre + m * g.ldp + n, gt, left, vec_p);
-            store4<D>(g.pre + m * g.ldp + g.N + n, up, left, vec_p);
+          if (g.res && real) {
+            const f32x8 r = load8<D>(g.res + m * g.ldr, n, g.N, vec_r);
+#pragma unroll
+            for (int v = 0; v < 8; ++v) z[v] += r[v];
           }
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < C::FN; ++j) {
-          const int n = n0 + wn + 16 * j + 4 * fq, left = g.N - n;
-          if (left <= 0) continue;
-          f32x4 z = acc[i][j];
-          if constexpr (MODE == LINEAR) {
-            if (bias) {
-#pragma unroll
-              for (int v = 0; v < 4; ++v)
-                if (v < left) z[v] += to_f<D>(bias[n + v]);
-            }
-            if (!real) z = f32x4{0.f, 0.f, 0.f, 0.f};
-            if (g.pre) store4<D>(g.pre + m * g.ldp + n, z, left, vec_p);
-            if (g.act != MOE_ACT_NONE) {
-#pragma unroll
-              for (int v = 0; v < 4; ++v) z[v] = act_value(z[v], g.act);
-            }
-            if (g.res && real) {
-              const f32x4 r = load4<D>(g.res + m * g.ldr + n, left, vec_r);
-#pragma unroll
-              for (int v = 0; v < 4; ++v) z[v] += r[v];
-            }
-          } else if (!real) {
-            z = f32x4{0.f, 0.f, 0.f, 0.f};
-          }
-          store4<D>(g.c0 + m * g.ldc0 + n, z, left, vec_c);
-        }
+        store8<D>(out + m * ldc, n, g.N, vec_c, real ? z : zero8);
       }
     }
   }
+#endif
 }
 
 }  // namespace moe_ffn

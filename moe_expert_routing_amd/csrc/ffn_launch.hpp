@@ -3,15 +3,16 @@
 
 #include "ffn.hpp"
 #include "ffn_gemm.hpp"
+#include "ffn_skinny.hpp"
 
 namespace moe_ffn {
 
-//            BM   BN   WM  WN NS blocks/CU
-typedef Tile<256, 256, 128, 64, 2, 1> Tile256;
-typedef Tile<128, 128, 64, 64, 2, 2> Tile128;
-typedef Tile<64, 128, 64, 32, 3, 2> Tile64;
-typedef Tile<32, 128, 32, 32, 3, 2> Tile32;
-typedef Tile<16, 128, 16, 32, 4, 2> Tile16;
+//           BM   BN   WM  WN TK NS blocks/CU
+typedef Tile<256, 256, 128, 64, 64, 2, 1> Tile256;
+typedef Tile<128, 128, 64, 64, 64, 2, 2> Tile128;
+typedef Tile<64, 128, 64, 32, 64, 3, 2> Tile64;
+typedef Tile<32, 128, 32, 32, 64, 3, 2> Tile32;
+typedef Tile<16, 128, 16, 32, 64, 4, 2> Tile16;
 
 template <class D, int MODE, class C>
 static int launch(GemmArgs g, hipStream_t st) {
@@ -22,15 +23,51 @@ static int launch(GemmArgs g, hipStream_t st) {
   if (MODE == WGRAD) blocks *= (int64_t)(g.r.num_experts > 0 ? g.r.num_experts : 1) * g.segs;
   if (blocks == 0) return MOE_OK;
   if (blocks > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
-  gemm_kernel<D, MODE, C><<<dim3((uint32_t)blocks), dim3(C::NTHREADS), 0, st>>>(g);
+  const dim3 grid((uint32_t)blocks), block(C::NTHREADS);
+  if constexpr (MODE == GATED || MODE == WGRAD) {
+    if (g.r.row_entry) {
+      gemm_kernel<D, MODE, C, true><<<grid, block, 0, st>>>(g);
+      return hip_status();
+    }
+  }
+  gemm_kernel<D, MODE, C, false><<<grid, block, 0, st>>>(g);
   return hip_status();
+}
+
+// Waves that share weight rows: a wave's k range is at least 512.
+template <class D, int MODE, int RX, int KW, int U>
+static int launch_skinny_kw(GemmArgs g, hipStream_t st) {
+  constexpr int COLS = SKINNY_WAVES / KW * (MODE == GATED ? 8 : 16);
+  g.m_tiles = (g.M + 16 * RX - 1) / (16 * RX);
+  g.n_tiles = (g.N + COLS - 1) / COLS;
+  const int64_t blocks = (int64_t)g.m_tiles * g.n_tiles;
+  if (blocks == 0) return MOE_OK;
+  if (blocks > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+  const dim3 grid((uint32_t)blocks), block(64 * SKINNY_WAVES);
+  if (MODE == GATED && g.r.row_entry)
+    skinny_kernel<D, MODE, RX, KW, U, MODE == GATED><<<grid, block, 0, st>>>(g);
+  else
+    skinny_kernel<D, MODE, RX, KW, U, false><<<grid, block, 0, st>>>(g);
+  return hip_status();
+}
+template <class D, int MODE, int RX, int U>
+static int launch_skinny(const GemmArgs &g, hipStream_t st) {
+  if (g.K >= 4096) return launch_skinny_kw<D, MODE, RX, 8, U>(g, st);
+  if (g.K >= 2048) return launch_skinny_kw<D, MODE, RX, 4, U>(g, st);
+  if (g.K >= 1024) return launch_skinny_kw<D, MODE, RX, 2, U>(g, st);
+  return launch_skinny_kw<D, MODE, RX, 1, U>(g, st);
 }
 
 template <class D, int MODE>
 static int launch_bm(int bm, const GemmArgs &g, hipStream_t st) {
+  if constexpr (MODE == GATED || MODE == LINEAR) {
+    if (bm == 16) return launch_skinny<D, MODE, 1, 8>(g, st);
+    if (bm == 32) return launch_skinny<D, MODE, 2, 4>(g, st);
+    if (bm == 64) return launch_skinny<D, MODE, 4, 4>(g, st);
+  }
   if (bm == 256) return launch<D, MODE, Tile256>(g, st);
   if (bm == 128) return launch<D, MODE, Tile128>(g, st);
-  if constexpr (MODE != WGRAD) {
+  if constexpr (MODE == DGRAD) {
     if (bm == 64) return launch<D, MODE, Tile64>(g, st);
     if (bm == 32) return launch<D, MODE, Tile32>(g, st);
     if (bm == 16) return launch<D, MODE, Tile16>(g, st);

@@ -8,36 +8,6 @@
 
 namespace moe_ffn {
 
-// Eight elements at column c of a row that has n columns; zeros past n.
-template <class D>
-__device__ __forceinline__ f32x8 load8(const uint16_t *row, int c, int n, bool vec) {
-  s16x8 w = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (vec && c + 8 <= n) {
-    w = *reinterpret_cast<const s16x8 *>(row + c);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < n) w[i] = (short)row[c + i];
-  }
-  return unpack8<D>(w);
-}
-__device__ __forceinline__ void store8_raw(uint16_t *row, int c, int n, bool vec, s16x8 w) {
-  if (vec && c + 8 <= n) {
-    *reinterpret_cast<s16x8 *>(row + c) = w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < n) row[c + i] = (uint16_t)w[i];
-  }
-}
-template <class D>
-__device__ __forceinline__ void store8(uint16_t *row, int c, int n, bool vec, f32x8 v) {
-  store8_raw(row, c, n, vec, pack8<D>(v));
-}
-// whether 8 consecutive elements at a multiple-of-8 column are one aligned load
-__device__ __forceinline__ bool vec8(const void *p, int64_t ld, int64_t off = 0) {
-  return (((uintptr_t)p & 15) | (uintptr_t)((ld | off) & 7)) == 0;
-}
 __device__ __forceinline__ bool row_is_real(const Rows &r, int64_t row) {
   if (r.num_experts == 0) return true;
   const int32_t e = r.m_indices[row];
@@ -67,6 +37,33 @@ __global__ __launch_bounds__(COL_THREADS *ROW_THREADS) void pad_rows_kernel(
         if (c + i < cols) w[i] = (short)p[c + i];
     }
     *reinterpret_cast<s16x8 *>(dst + r * cols8 + c) = w;
+  }
+}
+
+// dst [rows, cols8] = the token rows of x that the rows of a layout are made
+// from, zeros on rows without one and in the padding.
+__global__ __launch_bounds__(COL_THREADS *ROW_THREADS) void gather_rows_kernel(
+    const uint16_t *__restrict__ x, int64_t ld, int64_t tokens, int cols, int64_t rows, Rows r,
+    uint16_t *__restrict__ dst, int cols8) {
+  const int c = (blockIdx.x * COL_THREADS + threadIdx.x) * 8;
+  if (c >= cols8) return;
+  const bool vec = vec8(x, ld);
+  for (int64_t m = blockIdx.y * ROW_THREADS + threadIdx.y; m < rows;
+       m += (int64_t)gridDim.y * ROW_THREADS) {
+    s16x8 w = {0, 0, 0, 0, 0, 0, 0, 0};
+    const int32_t entry = row_is_real(r, m) ? r.row_entry[m] : -1;
+    const int64_t t = entry / r.top_k;
+    if (entry >= 0 && t < tokens) {
+      const uint16_t *p = x + t * ld;
+      if (vec && c + 8 <= cols) {
+        w = *reinterpret_cast<const s16x8 *>(p + c);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c + i < cols) w[i] = (short)p[c + i];
+      }
+    }
+    *reinterpret_cast<s16x8 *>(dst + m * cols8 + c) = w;
   }
 }
 

@@ -1,0 +1,138 @@
+// ffn_skinny.hpp - the forward products for few rows (decode): h or y for at
+// most 64 rows of one weight matrix, bound by reading that matrix once.
+//
+// The weights go from global memory straight into MFMA operands, with no
+// LDS and no barrier in the loop: a wave takes 16 weight rows (GATED: 8 of
+// the gate, their 8 of the other projection) and a range of k, loads U k-steps of
+// them (1 KB each) and of the few x rows, and multiplies one batch while the
+// next is on its way. KW waves of a block share their weight rows, each with
+// its own k range; their partial sums are added through LDS in the order of
+// k. GW such groups stand in a block.
+#pragma once
+
+#include "ffn_gemm.hpp"
+
+namespace moe_ffn {
+
+constexpr int SKINNY_WAVES = 8;
+
+// rows of a block: 16 RX
+template <class D, int MODE, int RX, int KW, int U, bool GATHER>
+__global__ __launch_bounds__(64 * SKINNY_WAVES) void skinny_kernel(const GemmArgs g) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int GW = SKINNY_WAVES / KW, NC = MODE == GATED ? 8 : 16, BM = 16 * RX;
+  __shared__ __attribute__((aligned(16))) float part[SKINNY_WAVES][RX][16][20];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kw = wave % KW, gw = wave / KW;
+  const bool grouped = g.r.num_experts > 0;
+  const int nt = blockIdx.x % g.n_tiles, mt = blockIdx.x / g.n_tiles;
+  const int m0 = mt * BM, n0 = nt * GW * NC;
+  int e = 0;
+  bool live = true;
+  if (grouped) {
+    e = g.r.m_indices[m0];
+    live = e >= 0 && e < g.r.num_experts && g.a_rows > 0;
+  }
+  const int K = g.K, fr = lane & 15, fq = lane >> 4;
+  f32x4 acc[RX];
+#pragma unroll
+  for (int x = 0; x < RX; ++x) acc[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  if (live) {
+    // whole k-steps, handed out in pairs so that waves part at 128-byte lines
+    const int steps = (K + 31) / 32, per = ((steps + KW - 1) / KW + 1) & ~1;
+    const int s0 = min(steps, kw * per), s1 = min(steps, s0 + per);
+    const bool second = MODE == GATED && fr >= 8;
+    const int nb = n0 + gw * NC + (MODE == GATED ? fr & 7 : fr);
+    const uint16_t *w = second ? g.b1 + e * g.b_stride1 + (int64_t)min(nb, g.N - 1) * g.ldb1
+                               : g.b0 + e * g.b_stride0 + (int64_t)min(nb, g.N - 1) * g.ldb0;
+    w += s0 * 32 + fq * 8;
+    const uint16_t *xr[RX];
+    const uint32_t magic = g.top_k_magic, shift = g.top_k_shift;
+#pragma unroll
+    for (int x = 0; x < RX; ++x) {
+      int64_t row = min(m0 + 16 * x + fr, g.M - 1);
+      if (GATHER) {
+        const uint32_t en = (uint32_t)g.r.row_entry[row];
+        const uint32_t t = magic ? __umulhi(en, magic) >> shift : en;
+        row = t < (uint64_t)g.a_rows ? t : 0;
+      }
+      xr[x] = g.a + row * g.lda + s0 * 32 + fq * 8;
+    }
+    s16x8 fw[2][U], fx[2][U][RX];
+    auto load = [&](int set, int s) MOE_INLINE {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        fw[set][u] = *reinterpret_cast<const s16x8 *>(w + (s + u) * 32);
+#pragma unroll
+        for (int x = 0; x < RX; ++x)
+          fx[set][u][x] = *reinterpret_cast<const s16x8 *>(xr[x] + (s + u) * 32);
+      }
+    };
+    auto multiply = [&](int set) MOE_INLINE {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int x = 0; x < RX; ++x) acc[x] = D::mfma(fw[set][u], fx[set][u][x], acc[x]);
+    };
+    // batches whose last step lies inside K
+    const int whole = max(0, (min(s1, K / 32) - s0) / U);
+    int b = 0;
+    if (whole > 0) load(0, 0);
+    for (; b + 2 <= whole; b += 2) {
+      load(1, (b + 1) * U);
+      multiply(0);
+      if (b + 2 < whole) load(0, (b + 2) * U);
+      multiply(1);
+    }
+    if (b < whole) multiply(0);
+    for (int s = whole * U; s < s1 - s0; ++s) {  // the rest, and K's own tail
+      s16x8 a = {0, 0, 0, 0, 0, 0, 0, 0}, c[RX];
+      const bool in = (s0 + s) * 32 + fq * 8 < K;
+      if (in) a = *reinterpret_cast<const s16x8 *>(w + s * 32);
+#pragma unroll
+      for (int x = 0; x < RX; ++x) {
+        c[x] = s16x8{0, 0, 0, 0, 0, 0, 0, 0};
+        if (in) c[x] = *reinterpret_cast<const s16x8 *>(xr[x] + s * 32);
+      }
+#pragma unroll
+      for (int x = 0; x < RX; ++x) acc[x] = D::mfma(a, c[x], acc[x]);
+    }
+#pragma unroll
+    for (int x = 0; x < RX; ++x) *reinterpret_cast<f32x4 *>(&part[wave][x][fr][4 * fq]) = acc[x];
+  }
+  __syncthreads();
+  // one output a thread: consecutive threads, consecutive columns
+  for (int o = threadIdx.x; o < GW * BM * NC; o += 64 * SKINNY_WAVES) {
+    const int c = o % NC, r = o / NC % BM, gr = o / (NC * BM);
+    const int n = n0 + gr * NC + c;
+    const int64_t m = m0 + r;
+    if (n >= g.N || m >= g.M) continue;
+    const bool real = live && (!grouped || g.r.m_indices[m] == e);
+    float z = 0.f, u = 0.f;
+    if (real) {
+#pragma unroll
+      for (int k = 0; k < KW; ++k) {
+        z += part[gr * KW + k][r >> 4][r & 15][c];
+        if (MODE == GATED) u += part[gr * KW + k][r >> 4][r & 15][8 + c];
+      }
+    }
+    if constexpr (MODE == GATED) {
+      g.c0[m * g.ldc0 + n] = real ? from_f<D>(act_value(z, g.act) * u) : 0;
+      if (g.pre) {
+        g.pre[m * g.ldp + n] = from_f<D>(z);
+        g.pre[m * g.ldp + g.N + n] = from_f<D>(u);
+      }
+    } else {
+      if (real && g.bias) z += to_f<D>(g.bias[e * g.bias_stride + n]);
+      if (g.pre) g.pre[m * g.ldp + n] = from_f<D>(z);
+      if (real) z = act_value(z, g.act);
+      if (real && g.res) z += to_f<D>(g.res[m * g.ldr + n]);
+      g.c0[m * g.ldc0 + n] = real ? from_f<D>(z) : 0;
+    }
+  }
+#endif
+}
+
+}  // namespace moe_ffn
