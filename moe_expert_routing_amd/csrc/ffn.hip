@@ -23,8 +23,8 @@ struct Arena {
   }
 };
 
-static int launch_gemm(int dtype, int mode, int bm, const GemmArgs &g, hipStream_t st) {
-  return dtype == MOE_BF16 ? launch_gemm_bf16(mode, bm, g, st) : launch_gemm_f16(mode, bm, g, st);
+static int launch_gemm(int dtype, int mode, int kind, const GemmArgs &g, hipStream_t st) {
+  return dtype == MOE_BF16 ? launch_gemm_bf16(mode, kind, g, st) : launch_gemm_f16(mode, kind, g, st);
 }
 
 static dim3 row_grid(int64_t rows, int cols8, int z) {
@@ -57,23 +57,44 @@ static Operand operand(const moe_matrix &m, int64_t rows, int cols, int mats, Ar
   return {dst, c8, rows * c8};
 }
 
-// Rows of a tile. Over experts a tile holds rows of one expert, so it divides
-// the layout's alignment. Dense: the smallest tile that holds all the
-// rows; above 64 rows 256-row tiles where they fill the chip's 256 compute
-// units at least to three quarters, else 128-row ones.
-static int tile_rows(const moe_expert_rows &r, int64_t M, int N) {
-  if (r.num_experts > 0) {
-    for (int bm = 256; bm > 16; bm >>= 1)
-      if (r.tile_m % bm == 0) return bm;
-    return 16;
+// Tile of `mats` products of M x N over K: the one with the least estimated
+// time, its rounds over the 256 compute units times (64-k stages times a stage's
+// time, plus a fixed part). The stage times, in microseconds, are measured
+// with one tile on a compute unit, and with two where two fit. What
+// the choice does, in us, for 256 / 128 / 64 / 32-row tiles:
+//   1024 x 1024 x 2816     60 / 22 / 14 / 14    8192 x 7168 x 2048  265 / 295 / - / -
+//   2048 x 2048 x 2048     49 / 21 / 31 / -     64 x 7168 x 2048    - / - / 11 / 8.7
+static int dense_tile(int64_t mats, int64_t M, int64_t N, int64_t K) {
+  static const struct {
+    int kind, bm, bn, blocks;
+    float one, full, fixed;
+  } tiles[] = {{TILE_256, 256, 256, 1, 1.5f, 1.5f, 10.f},
+               {TILE_128, 128, 128, 1, 0.46f, 0.46f, 4.f},
+               {TILE_64, 64, 64, 2, 0.30f, 0.48f, 2.5f},
+               {TILE_32, 32, 64, 2, 0.26f, 0.36f, 2.5f}};
+  const float stages = (float)((K + 63) / 64);
+  int best = TILE_256;
+  float least = 0.f;
+  for (const auto &t : tiles) {
+    const int64_t n = mats * ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
+    const int64_t rounds = (n + 256 * t.blocks - 1) / (256 * t.blocks);
+    const float time = (float)rounds * (stages * (n <= 256 ? t.one : t.full) + t.fixed);
+    if (least == 0.f || time < least) least = time, best = t.kind;
   }
-  if (M <= 16) return 16;
-  if (M <= 32) return 32;
-  if (M <= 64) return 64;
-  return ((M + 255) / 256) * ((N + 255) / 256) >= 192 ? 256 : 128;
+  return best;
 }
-static int tile_rows_wgrad(int mats, int M, int N) {
-  return (int64_t)mats * ((M + 255) / 256) * ((N + 255) / 256) >= 192 ? 256 : 128;
+// Tile of the products whose M is the call's rows. Over experts a tile
+// holds rows of one expert, so it divides the layout's alignment; 256 rows only
+// where experts have that many by far, as shorter tiles that hold padding
+// alone are skipped. (128 x 256 against 128 x 128 tiles, 112 experts with about
+// 146 rows, 2048 -> 1024: gated 262 against 302 us.)
+static int row_tile(const moe_expert_rows &r, int64_t M, int N, int64_t K) {
+  if (r.num_experts > 0) {
+    if (r.tile_m % 256 == 0 && M / r.num_experts >= 2048) return TILE_256;
+    return r.tile_m % 128 == 0 ? TILE_128W
+           : r.tile_m % 64 == 0 ? TILE_64 : r.tile_m % 32 == 0 ? TILE_32 : TILE_16;
+  }
+  return M <= 16 ? TILE_16 : dense_tile(1, M, N, K);
 }
 
 static int check_common(int dtype, int act, int64_t tokens, int w0, int w1,
@@ -209,7 +230,7 @@ static int run_gated(const moe_gated_ffn_args *a, Arena &ws, hipStream_t st) {
   set_c0(g, a->h);
   g.pre = (uint16_t *)a->pre.p, g.ldp = a->pre.ld;
   g.M = (int)rows, g.N = F, g.K = H, g.act = a->activation;
-  return launch_gemm(a->dtype, GATED, tile_rows(a->rows, rows, 2 * F), g, st);
+  return launch_gemm(a->dtype, GATED, row_tile(a->rows, rows, 2 * F, H), g, st);
 }
 
 static int run_gated_backward(const moe_gated_ffn_args *a, Arena &ws, hipStream_t st) {
@@ -248,7 +269,7 @@ static int run_gated_backward(const moe_gated_ffn_args *a, Arena &ws, hipStream_
     set_b1(d, wu);
     set_c0(d, a->dx);
     d.M = (int)rows, d.N = H, d.K = F;
-    MOE_TRY(launch_gemm(a->dtype, DGRAD, tile_rows(a->rows, rows, H), d, st));
+    MOE_TRY(launch_gemm(a->dtype, DGRAD, row_tile(a->rows, rows, H, 2 * F), d, st));
   }
   if (a->dw_gate.p) {
     set_b0(g, x);
@@ -257,7 +278,7 @@ static int run_gated_backward(const moe_gated_ffn_args *a, Arena &ws, hipStream_
     set_c0(g, a->dw_gate);
     set_c1(g, a->dw_up);
     g.M = F, g.N = H, g.K = (int)rows;
-    MOE_TRY(launch_gemm(a->dtype, WGRAD, tile_rows_wgrad(2 * mats, F, H), g, st));
+    MOE_TRY(launch_gemm(a->dtype, WGRAD, dense_tile(2 * mats, F, H, rows / mats), g, st));
   }
   return MOE_OK;
 }
@@ -299,7 +320,7 @@ static int run_linear(const moe_linear_args *a, Arena &ws, hipStream_t st) {
   g.bias = (const uint16_t *)a->bias.p, g.bias_stride = a->bias.stride;
   g.res = (const uint16_t *)a->residual.p, g.ldr = a->residual.ld;
   g.M = (int)rows, g.N = O, g.K = I, g.act = a->activation;
-  return launch_gemm(a->dtype, LINEAR, tile_rows(a->rows, rows, O), g, st);
+  return launch_gemm(a->dtype, LINEAR, row_tile(a->rows, rows, O, I), g, st);
 }
 
 // Row ranges of the bias gradient's partial sums: dense, one for every 256
@@ -356,13 +377,13 @@ static int run_linear_backward(const moe_linear_args *a, Arena &ws, hipStream_t 
     set_b0(d, w);
     set_c0(d, a->dx);
     d.M = (int)rows, d.N = I, d.K = O;
-    MOE_TRY(launch_gemm(a->dtype, DGRAD, tile_rows(a->rows, rows, I), d, st));
+    MOE_TRY(launch_gemm(a->dtype, DGRAD, row_tile(a->rows, rows, I, O), d, st));
   }
   if (a->dw.p) {
     set_b0(g, x);
     set_c0(g, a->dw);
     g.M = O, g.N = I, g.K = (int)rows;
-    MOE_TRY(launch_gemm(a->dtype, WGRAD, tile_rows_wgrad(mats, O, I), g, st));
+    MOE_TRY(launch_gemm(a->dtype, WGRAD, dense_tile(mats, O, I, rows / mats), g, st));
   }
   return MOE_OK;
 }

@@ -2,7 +2,7 @@
 #include "ffn_launch.hpp"
 
 namespace moe_ffn {
-int launch_gemm_bf16(int mode, int bm, const GemmArgs &g, hipStream_t st) {
-  return launch_mode<Bf16>(mode, bm, g, st);
+int launch_gemm_bf16(int mode, int kind, const GemmArgs &g, hipStream_t st) {
+  return launch_mode<Bf16>(mode, kind, g, st);
 }
 }  // namespace moe_ffn

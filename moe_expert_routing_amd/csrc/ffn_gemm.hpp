@@ -47,9 +47,27 @@ constexpr uint32_t PAST = 0xffffffffu;
 
 // The device pass alone knows the buffer builtins.
 #if defined(__HIP_DEVICE_COMPILE__)
-// Buffer of 4 GB - 1 at p: 32-bit unsigned byte offsets from a uniform base.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const uint8_t *p) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, PAST, 0x00020000);
+// 16 bytes a lane from byte offset `o` of the 4 GB - 1 at p into LDS: lane i
+// writes at dst + 16 i; p and dst are uniform. With TRANSPOSED the compiler
+// is not told of the write to LDS: before every transposing LDS read it
+// would wait for all such loads in flight, while the kernel's own waits already
+// order a stage's loads before its reads. (s_nop: one wait state between writing
+// m0 and an LDS load that reads it.)
+template <bool TRANSPOSED>
+__device__ __forceinline__ void lds_piece(const uint8_t *p, uint32_t o, uint8_t *dst) {
+  if constexpr (TRANSPOSED) {
+    typedef int i32x4 __attribute__((ext_vector_type(4)));
+    const uint64_t at = (uint64_t)p;
+    const i32x4 rsrc = {(int)(uint32_t)at, (int)(at >> 32) & 0xffff, (int)PAST, 0x00020000};
+    const uint32_t to = (uint32_t)(uintptr_t)(lds_ptr_t)dst;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(o),
+                 "s"(rsrc)
+                 : "m0");
+  } else {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, PAST, 0x00020000),
+        (lds_ptr_t)dst, 16, o, 0, 0, 0);
+  }
 }
 #endif
 
@@ -90,7 +108,7 @@ __device__ __forceinline__ void wait_vmcnt_imm() {
 // memory, R columns wide.
 template <int R>
 __device__ __forceinline__ int swz(int k) {
-  return R >= 128 ? ((k & 3) << 1) | (((k >> 3) & 1) << 3) : (k & 3) << 1;
+  return R >= 128 ? ((k & 3) << 1) | (((k >> 3) & 1) << 3) : R >= 64 ? (k & 3) << 1 : (k & 1) << 1;
 }
 
 // Tile of this block. The hardware sends block b to XCD b % 8: each XCD takes
@@ -115,6 +133,7 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int BM = C::BM, BN = C::BN, NS = C::NS, TK = C::TK;
   constexpr bool A_TR = MODE == WGRAD, B_TR = MODE == DGRAD || MODE == WGRAD;
+  static_assert((!A_TR || BM >= 32) && (!B_TR || BN >= 32), "chunks for swz to permute");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * C::STAGE_BYTES];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -283,11 +302,9 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
     if (MODE == WGRAD && GATHER && !is_a(q))
       o += (uint32_t)(gathered_row(entry[q - C::A_LOADS]) * ldb) * 2;
     o = past(q, left) ? PAST : o;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        buffer_at(is_a(q) ? a_base : b_base),
-        (lds_ptr_t)(smem + (s % NS) * C::STAGE_BYTES + (is_a(q) ? 0 : C::A_BYTES) +
-                    number(q) * 1024),
-        16, o, 0, 0, 0);
+    lds_piece<A_TR || B_TR>(is_a(q) ? a_base : b_base, o,
+                            smem + (s % NS) * C::STAGE_BYTES + (is_a(q) ? 0 : C::A_BYTES) +
+                                number(q) * 1024);
   };
   auto next_stage = [&](int s) MOE_INLINE {  // after stage s
     fetch_entries(s + 1);

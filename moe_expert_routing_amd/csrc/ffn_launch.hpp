@@ -9,9 +9,10 @@ namespace moe_ffn {
 
 //           BM   BN   WM  WN TK NS blocks/CU
 typedef Tile<256, 256, 128, 64, 64, 2, 1> Tile256;
-typedef Tile<128, 128, 64, 64, 64, 2, 2> Tile128;
-typedef Tile<64, 128, 64, 32, 64, 3, 2> Tile64;
-typedef Tile<32, 128, 32, 32, 64, 3, 2> Tile32;
+typedef Tile<128, 256, 64, 64, 64, 3, 1> Tile128w;
+typedef Tile<128, 128, 64, 32, 64, 4, 1> Tile128;
+typedef Tile<64, 64, 32, 32, 64, 4, 2> Tile64;
+typedef Tile<32, 64, 16, 32, 64, 4, 2> Tile32;
 typedef Tile<16, 128, 16, 32, 64, 4, 2> Tile16;
 
 template <class D, int MODE, class C>
@@ -34,54 +35,64 @@ static int launch(GemmArgs g, hipStream_t st) {
   return hip_status();
 }
 
-// Waves that share weight rows: a wave's k range is at least 512.
-template <class D, int MODE, int RX, int KW, int U>
+template <class D, int MODE, int KW>
 static int launch_skinny_kw(GemmArgs g, hipStream_t st) {
   constexpr int COLS = SKINNY_WAVES / KW * (MODE == GATED ? 8 : 16);
-  g.m_tiles = (g.M + 16 * RX - 1) / (16 * RX);
+  g.m_tiles = (g.M + 15) / 16;
   g.n_tiles = (g.N + COLS - 1) / COLS;
   const int64_t blocks = (int64_t)g.m_tiles * g.n_tiles;
   if (blocks == 0) return MOE_OK;
   if (blocks > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
   const dim3 grid((uint32_t)blocks), block(64 * SKINNY_WAVES);
   if (MODE == GATED && g.r.row_entry)
-    skinny_kernel<D, MODE, RX, KW, U, MODE == GATED><<<grid, block, 0, st>>>(g);
+    skinny_kernel<D, MODE, 1, KW, 4, MODE == GATED><<<grid, block, 0, st>>>(g);
   else
-    skinny_kernel<D, MODE, RX, KW, U, false><<<grid, block, 0, st>>>(g);
+    skinny_kernel<D, MODE, 1, KW, 4, false><<<grid, block, 0, st>>>(g);
   return hip_status();
 }
-template <class D, int MODE, int RX, int U>
+// Waves that share weight rows. Dense calls have few blocks: all 8, or 4 where
+// that already gives more than one block and a half for each compute unit
+// (1 row, 2048 -> 7168: 7.9 us with 4, 8.5 with 8; 7168 -> 2048 gated: 12.6 with
+// 8, 19.1 with 4). Over experts there are enough blocks, and longer ranges of k
+// read faster (28 live experts: 7168 -> 1024 gated 147 us with 4, 151 with 8, 159
+// with 1; 1024 -> 7168 111 us with 1, 121 with 2, 148 with 8).
+template <class D, int MODE>
 static int launch_skinny(const GemmArgs &g, hipStream_t st) {
-  if (g.K >= 4096) return launch_skinny_kw<D, MODE, RX, 8, U>(g, st);
-  if (g.K >= 2048) return launch_skinny_kw<D, MODE, RX, 4, U>(g, st);
-  if (g.K >= 1024) return launch_skinny_kw<D, MODE, RX, 2, U>(g, st);
-  return launch_skinny_kw<D, MODE, RX, 1, U>(g, st);
+  if (g.r.num_experts == 0) {
+    const int blocks = g.N / (MODE == GATED ? 8 : 16);
+    return blocks >= 384 ? launch_skinny_kw<D, MODE, 4>(g, st)
+                         : launch_skinny_kw<D, MODE, 8>(g, st);
+  }
+  if (g.K >= 4096) return launch_skinny_kw<D, MODE, 4>(g, st);
+  if (g.K >= 2048) return launch_skinny_kw<D, MODE, 2>(g, st);
+  return launch_skinny_kw<D, MODE, 1>(g, st);
 }
 
 template <class D, int MODE>
-static int launch_bm(int bm, const GemmArgs &g, hipStream_t st) {
-  if constexpr (MODE == GATED || MODE == LINEAR) {
-    if (bm == 16) return launch_skinny<D, MODE, 1, 8>(g, st);
-    if (bm == 32) return launch_skinny<D, MODE, 2, 4>(g, st);
-    if (bm == 64) return launch_skinny<D, MODE, 4, 4>(g, st);
+static int launch_kind(int kind, const GemmArgs &g, hipStream_t st) {
+  switch (kind) {
+    case TILE_256: return launch<D, MODE, Tile256>(g, st);
+    case TILE_128: return launch<D, MODE, Tile128>(g, st);
+    case TILE_64: return launch<D, MODE, Tile64>(g, st);
+    case TILE_32: return launch<D, MODE, Tile32>(g, st);
   }
-  if (bm == 256) return launch<D, MODE, Tile256>(g, st);
-  if (bm == 128) return launch<D, MODE, Tile128>(g, st);
+  if constexpr (MODE != WGRAD)
+    if (kind == TILE_128W) return launch<D, MODE, Tile128w>(g, st);
   if constexpr (MODE == DGRAD) {
-    if (bm == 64) return launch<D, MODE, Tile64>(g, st);
-    if (bm == 32) return launch<D, MODE, Tile32>(g, st);
-    if (bm == 16) return launch<D, MODE, Tile16>(g, st);
+    if (kind == TILE_16) return launch<D, MODE, Tile16>(g, st);
+  } else if constexpr (MODE != WGRAD) {
+    if (kind == TILE_16) return launch_skinny<D, MODE>(g, st);
   }
   return MOE_ERR_UNSUPPORTED;
 }
 
 template <class D>
-static int launch_mode(int mode, int bm, const GemmArgs &g, hipStream_t st) {
+static int launch_mode(int mode, int kind, const GemmArgs &g, hipStream_t st) {
   switch (mode) {
-    case GATED: return launch_bm<D, GATED>(bm, g, st);
-    case LINEAR: return launch_bm<D, LINEAR>(bm, g, st);
-    case DGRAD: return launch_bm<D, DGRAD>(bm, g, st);
-    case WGRAD: return launch_bm<D, WGRAD>(bm, g, st);
+    case GATED: return launch_kind<D, GATED>(kind, g, st);
+    case LINEAR: return launch_kind<D, LINEAR>(kind, g, st);
+    case DGRAD: return launch_kind<D, DGRAD>(kind, g, st);
+    case WGRAD: return launch_kind<D, WGRAD>(kind, g, st);
   }
   return MOE_ERR_UNSUPPORTED;
 }

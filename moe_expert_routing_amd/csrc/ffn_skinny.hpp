@@ -1,5 +1,5 @@
-// ffn_skinny.hpp - the forward products for few rows (decode): h or y for at
-// most 64 rows of one weight matrix, bound by reading that matrix once.
+// ffn_skinny.hpp - the forward products for few rows (decode): h or y of 16
+// rows of one weight matrix, bound by reading that matrix once.
 //
 // The weights go from global memory straight into MFMA operands, with no
 // LDS and no barrier in the loop: a wave takes 16 weight rows (GATED: 8 of
@@ -103,34 +103,53 @@ __global__ __launch_bounds__(64 * SKINNY_WAVES) void skinny_kernel(const GemmArg
     for (int x = 0; x < RX; ++x) *reinterpret_cast<f32x4 *>(&part[wave][x][fr][4 * fq]) = acc[x];
   }
   __syncthreads();
-  // one output a thread: consecutive threads, consecutive columns
-  for (int o = threadIdx.x; o < GW * BM * NC; o += 64 * SKINNY_WAVES) {
-    const int c = o % NC, r = o / NC % BM, gr = o / (NC * BM);
+  // eight columns of a row a thread
+  const bool vec_c = vec8(g.c0, g.ldc0), vec_p = vec8(g.pre, g.ldp);
+  const bool vec_u = vec8(g.pre, g.ldp, g.N), vec_r = vec8(g.res, g.ldr);
+  constexpr int RUNS = NC / 8;
+  for (int o = threadIdx.x; o < GW * BM * RUNS; o += 64 * SKINNY_WAVES) {
+    const int c = o % RUNS * 8, gr = o / RUNS % GW, r = o / (RUNS * GW);
     const int n = n0 + gr * NC + c;
     const int64_t m = m0 + r;
     if (n >= g.N || m >= g.M) continue;
     const bool real = live && (!grouped || g.r.m_indices[m] == e);
-    float z = 0.f, u = 0.f;
+    f32x8 z = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, u = z;
     if (real) {
 #pragma unroll
       for (int k = 0; k < KW; ++k) {
-        z += part[gr * KW + k][r >> 4][r & 15][c];
-        if (MODE == GATED) u += part[gr * KW + k][r >> 4][r & 15][8 + c];
+        const float *p = &part[gr * KW + k][r >> 4][r & 15][c];
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          z[v] += p[v];
+          if (MODE == GATED) u[v] += p[8 + v];
+        }
       }
     }
     if constexpr (MODE == GATED) {
-      g.c0[m * g.ldc0 + n] = real ? from_f<D>(act_value(z, g.act) * u) : 0;
       if (g.pre) {
-        g.pre[m * g.ldp + n] = from_f<D>(z);
-        g.pre[m * g.ldp + g.N + n] = from_f<D>(u);
+        store8<D>(g.pre + m * g.ldp, n, g.N, vec_p, z);
+        store8<D>(g.pre + m * g.ldp + g.N, n, g.N, vec_u, u);
       }
+#pragma unroll
+      for (int v = 0; v < 8; ++v) z[v] = real ? act_value(z[v], g.act) * u[v] : 0.f;
     } else {
-      if (real && g.bias) z += to_f<D>(g.bias[e * g.bias_stride + n]);
-      if (g.pre) g.pre[m * g.ldp + n] = from_f<D>(z);
-      if (real) z = act_value(z, g.act);
-      if (real && g.res) z += to_f<D>(g.res[m * g.ldr + n]);
-      g.c0[m * g.ldc0 + n] = real ? from_f<D>(z) : 0;
+      if (real && g.bias) {
+        const f32x8 b = load8<D>(g.bias + e * g.bias_stride, n, g.N, false);
+#pragma unroll
+        for (int v = 0; v < 8; ++v) z[v] += b[v];
+      }
+      if (g.pre) store8<D>(g.pre + m * g.ldp, n, g.N, vec_p, z);
+      if (real && g.act != MOE_ACT_NONE) {
+#pragma unroll
+        for (int v = 0; v < 8; ++v) z[v] = act_value(z[v], g.act);
+      }
+      if (real && g.res) {
+        const f32x8 b = load8<D>(g.res + m * g.ldr, n, g.N, vec_r);
+#pragma unroll
+        for (int v = 0; v < 8; ++v) z[v] += b[v];
+      }
     }
+    store8<D>(g.c0 + m * g.ldc0, n, g.N, vec_c, z);
   }
 #endif
 }
