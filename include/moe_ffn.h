@@ -66,7 +66,8 @@ typedef struct moe_matrix {
 } moe_matrix;
 
 typedef struct moe_expert_rows {
-  const int32_t *counts;         /* [>= num_experts] entries of each expert    */
+  const int32_t *counts;         /* [>= num_experts] entries of each expert;
+                                    read by the backward passes                */
   const int32_t *padded_offsets; /* [>= num_experts + 1] first row of each     */
   const int32_t *m_indices;      /* [rows] expert of each row, -1 on padding   */
   const int32_t *row_entry;      /* [rows] entry t * top_k + k of each row, -1;

@@ -110,8 +110,8 @@ static int check_common(int dtype, int act, int64_t tokens, int w0, int w1,
     if (r.num_experts > MOE_FFN_MAX_EXPERTS || r.rows > MAX_ROWS) return MOE_ERR_UNSUPPORTED;
     if (r.tile_m <= 0 || r.tile_m > MOE_GROUPED_MAX_TILE) return MOE_ERR_SHAPE;
     if (r.tile_m % 16 != 0) return MOE_ERR_UNSUPPORTED;
-    if (r.rows > 0 && !r.m_indices) return MOE_ERR_NULL;
-    if (backward && (!r.counts || !r.padded_offsets)) return MOE_ERR_NULL;
+    if (!r.padded_offsets || (r.rows > 0 && !r.m_indices)) return MOE_ERR_NULL;
+    if (backward && !r.counts) return MOE_ERR_NULL;
     if (r.row_entry && r.top_k <= 0) return MOE_ERR_SHAPE;
   }
   return MOE_OK;

@@ -111,15 +111,21 @@ __device__ __forceinline__ int swz(int k) {
   return R >= 128 ? ((k & 3) << 1) | (((k >> 3) & 1) << 3) : R >= 64 ? (k & 3) << 1 : (k & 1) << 1;
 }
 
-// Tile of this block. The hardware sends block b to XCD b % 8: each XCD takes
-// a contiguous run of tiles, and the run goes through the tiles in columns
-// of 8 m-tiles, so that the tiles in flight on one XCD share operand rows in
-// its L2.
-__device__ __forceinline__ void tile_of_block(int b, int total, int m_tiles, int n_tiles, int &mt,
-                                              int &nt) {
+// Number of this block's tile among `total`. The hardware sends block b to XCD
+// b % 8: each XCD takes a contiguous run of the first `live` tiles, and then
+// of the others, so that the live ones are spread evenly.
+__device__ __forceinline__ int tile_of_block(int b, int total, int live) {
+  const int x = b % 8, j = b / 8;
+  const int live_before = x * (live / 8) + min(x, live % 8);
+  const int live_here = live / 8 + (x < live % 8);
+  if (j < live_here) return live_before + j;
+  const int before = x * (total / 8) + min(x, total % 8);
+  return live + before - live_before + (j - live_here);
+}
+// Tiles go in columns of 8 m-tiles, so that those in flight on one XCD share
+// operand rows in its L2.
+__device__ __forceinline__ void tile_at(int t, int m_tiles, int n_tiles, int &mt, int &nt) {
   constexpr int GROUP = 8;
-  const int per = total / 8, rest = total % 8, x = b % 8;
-  int t = x * per + min(x, rest) + b / 8;
   const int full = GROUP * n_tiles;
   const int g = t / full, first = g * GROUP, size = min(GROUP, m_tiles - first);
   t -= g * full;
@@ -148,14 +154,25 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
     const int chunk = blockIdx.x / per;
     e = chunk / g.segs;
     seg0 = chunk % g.segs;
-    tile_of_block(blockIdx.x % per, per, g.m_tiles, g.n_tiles, mt, nt);
+    tile_at(tile_of_block(blockIdx.x % per, per, per), g.m_tiles, g.n_tiles, mt, nt);
     if (grouped) {
       const int64_t p0 = g.r.padded_offsets[e], cnt = g.r.counts[e];
       k_row0 = min(max(p0, (int64_t)0), g.r.rows);
       K = (int)min(max(cnt, (int64_t)0), g.r.rows - k_row0);
     }
   } else {
-    tile_of_block(blockIdx.x, gridDim.x, g.m_tiles, g.n_tiles, mt, nt);
+    int live = g.m_tiles;  // m-tiles with rows of the experts here
+    if (grouped) {
+      const int64_t end = g.r.padded_offsets[g.r.num_experts];
+      live = (int)min((int64_t)g.m_tiles, (max(end, (int64_t)0) + BM - 1) / BM);
+    }
+    const int t = tile_of_block(blockIdx.x, gridDim.x, live * g.n_tiles);
+    if (t < live * g.n_tiles) {
+      tile_at(t, live, g.n_tiles, mt, nt);
+    } else {
+      mt = t / g.n_tiles;
+      nt = t % g.n_tiles;
+    }
   }
   const int m0 = mt * BM;
   const int n0 = nt * (MODE == GATED ? BN / 2 : BN);  // column of C
@@ -164,16 +181,18 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
     if (grouped) {
       e = g.r.m_indices[m0];
       if (e < 0 || e >= g.r.num_experts || g.a_rows == 0) {  // no entry here: zeros
-        constexpr int W = MODE == GATED ? BN / 2 : BN;
-        const int width = min(W, g.N - n0), height = min(BM, g.M - m0);
-        for (int i = threadIdx.x; i < height * W; i += C::NTHREADS) {
-          const int r = i / W, c = i % W;
-          if (c < width) {
-            g.c0[(int64_t)(m0 + r) * g.ldc0 + n0 + c] = 0;
-            if (MODE <= LINEAR && g.pre) {
-              g.pre[(int64_t)(m0 + r) * g.ldp + n0 + c] = 0;
-              if (MODE == GATED) g.pre[(int64_t)(m0 + r) * g.ldp + g.N + n0 + c] = 0;
-            }
+        constexpr int RUNS = (MODE == GATED ? BN / 2 : BN) / 8;
+        const bool vec_c = vec8(g.c0, g.ldc0), vec_p = vec8(g.pre, g.ldp);
+        const bool vec_u = vec8(g.pre, g.ldp, g.N);
+        const s16x8 zero = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int i = threadIdx.x; i < BM * RUNS; i += C::NTHREADS) {
+          const int64_t m = m0 + i / RUNS;
+          const int n = n0 + i % RUNS * 8;
+          if (m >= g.M || n >= g.N) continue;
+          store8_raw(g.c0 + m * g.ldc0, n, g.N, vec_c, zero);
+          if (MODE <= LINEAR && g.pre) {
+            store8_raw(g.pre + m * g.ldp, n, g.N, vec_p, zero);
+            if (MODE == GATED) store8_raw(g.pre + m * g.ldp + g.N, n, g.N, vec_u, zero);
           }
         }
         return;
