@@ -24,6 +24,7 @@ row_entry may be cut to the rows that the caller's buffers have.
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Dict, Optional
 
 import torch
@@ -83,51 +84,78 @@ def _fail(msg: str):
     raise _pkg.MoeRouteError(msg)
 
 
-def _call(name: str, args, dev: torch.device, backward: Optional[int] = None,
-          ws: Optional[torch.Tensor] = None) -> None:
-    """Run a C entry on the current stream of `dev`, with a workspace of its
-    own where it needs one: a tensor of this call, so that a captured call
-    keeps it in its graph's memory."""
-    lib = _pkg.lib()
-    ref = ctypes.byref(args)
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return _call(name, args, dev, backward, ws)
-    if backward is None:
-        st = getattr(lib, name)(ref, _pkg._stream_handle(dev))
-    else:
-        need = getattr(lib, name.replace("_backward", "") + "_workspace_bytes")(ref, backward)
-        if ws is None and need > 0:
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        st = getattr(lib, name)(ref, None if ws is None else ws.data_ptr(),
-                                0 if ws is None else ws.numel(), _pkg._stream_handle(dev))
-    if st:
-        _pkg._check(st, name)
+# The structures above as bytes (native sizes and alignment): packing them is
+# several times faster than filling ctypes fields, which small calls notice.
+_MATRIX = "Pqq"
+_PACK_GATED = struct.Struct("@iiqii" + "PPPPqiii0q" + 9 * _MATRIX).pack
+_PACK_LINEAR = struct.Struct("@iiqii" + "PPPPqiii0q" + 10 * _MATRIX).pack
+_PACK_COMBINE = struct.Struct("@iiqqiii0q" + 7 * "P" + 5 * _MATRIX + "P").pack
+_NONE = (0, 0, 0)
+_ERR_WORKSPACE = -5
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _mat(t: Optional[torch.Tensor], name: str, shape, like: torch.Tensor) -> tuple:
+class _Entry:
+    """A C entry on the current stream of a device. One that needs a workspace
+    says so and gets one of this call alone, which a captured call keeps in its
+    graph's memory."""
+
+    def __init__(self, name: str, size: Optional[str] = None, backward: int = 0):
+        self.name, self.size, self.backward, self.fn = name, size, backward, None
+
+    def __call__(self, args: bytes, dev: torch.device, ws: Optional[torch.Tensor] = None) -> None:
+        if self.fn is None:
+            self.fn = getattr(_pkg.lib(), self.name)
+        if dev.index != _current_device():
+            with torch.cuda.device(dev):
+                return self(args, dev, ws)
+        stream = _pkg._stream_handle(dev)
+        if self.size is None:
+            st = self.fn(args, stream)
+        elif ws is not None:
+            st = self.fn(args, ws.data_ptr(), ws.numel(), stream)
+        else:
+            st = self.fn(args, None, 0, stream)
+            if st == _ERR_WORKSPACE:
+                need = getattr(_pkg.lib(), self.size)(args, self.backward)
+                ws = torch.empty(need, dtype=torch.uint8, device=dev)
+                st = self.fn(args, ws.data_ptr(), need, stream)
+        if st:
+            _pkg._check(st, self.name)
+
+
+_GATED = _Entry("moe_gated_ffn", "moe_gated_ffn_workspace_bytes")
+_GATED_BACKWARD = _Entry("moe_gated_ffn_backward", "moe_gated_ffn_workspace_bytes", 1)
+_LINEAR = _Entry("moe_linear", "moe_linear_workspace_bytes")
+_LINEAR_BACKWARD = _Entry("moe_linear_backward", "moe_linear_workspace_bytes", 1)
+_COMBINE = _Entry("moe_combine")
+_COMBINE_BACKWARD = _Entry("moe_combine_backward")
+
+
+def _mat(t: Optional[torch.Tensor], name: str, shape: tuple, like: torch.Tensor) -> tuple:
     """(pointer, ld, stride) of a matrix or a stack of them, checked."""
     if t is None:
-        return (None, 0, 0)
+        return _NONE
     if not isinstance(t, torch.Tensor) or t.dtype != like.dtype or t.device != like.device:
         _fail(f"{name} must be a {like.dtype} tensor on {like.device}")
     if t.shape != shape:
-        _fail(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+        _fail(f"{name} must have shape {shape}, not {tuple(t.shape)}")
     st = t.stride()
-    n = len(st)
-    if t.numel() == 0:
-        return (None, shape[-1], 0)
+    p = t.data_ptr()
+    if p == 0 or 0 in shape:
+        return (0, shape[-1], 0)
     if st[-1] != 1 and shape[-1] > 1:
         _fail(f"{name} must have contiguous columns")
+    n = len(st)
     if n == 1:
-        return (t.data_ptr(), shape[0], 0)
+        return (p, shape[0], 0)
     ld = st[-2] if shape[-2] > 1 else max(st[-2], shape[-1])
     if n == 2:
-        return (t.data_ptr(), ld, 0)
-    return (t.data_ptr(), ld, st[0] if shape[0] > 1 else ld * shape[1])
+        return (p, ld, 0)
+    return (p, ld, st[0] if shape[0] > 1 else ld * shape[1])
 
 
-def _vec(t: Optional[torch.Tensor], name: str, shape, like: torch.Tensor) -> tuple:
+def _vec(t: Optional[torch.Tensor], name: str, shape: tuple, like: torch.Tensor) -> tuple:
     """(pointer, ld, stride) of a vector, or of one vector for each expert."""
     if t is None or len(shape) == 1:
         return _mat(t, name, shape, like)
@@ -162,7 +190,7 @@ def _index(t, name: str, dev, least: int = 0) -> int:
     return t.data_ptr()
 
 
-_DENSE = (None, None, None, None, 0, 0, 0, 0)
+_DENSE = (0, 0, 0, 0, 0, 0, 0, 0)
 
 
 def _rows(lay, n_experts: int, tile_m: int, top_k: int, dev, gather: bool) -> tuple:
@@ -174,7 +202,7 @@ def _rows(lay, n_experts: int, tile_m: int, top_k: int, dev, gather: bool) -> tu
         _fail("row_entry must have as many elements as m_indices")
     return (_index(lay["counts"], "counts", dev, n_experts),
             _index(lay["padded_offsets"], "padded_offsets", dev, n_experts + 1),
-            p, None if entry is None else _index(entry, "row_entry", dev), rows, n_experts,
+            p, 0 if entry is None else _index(entry, "row_entry", dev), rows, n_experts,
             tile_m, top_k)
 
 
@@ -201,12 +229,11 @@ def _gated(x, w_gate, w_up, activation, save_pre, out, ws, lay, tile_m, top_k):
             if t is not None:
                 t.zero_()
         return out
-    a = GatedFfnArgs(d, act, tokens, hidden, inter, desc, _mat(x, "x", (tokens, hidden), x),
-                     _mat(w_gate, "w_gate", wshape, x), _mat(w_up, "w_up", wshape, x),
-                     _mat(out["h"], "h", (rows, inter), x),
-                     _mat(pre, "pre", (rows, 2 * inter), x))
-    if hidden and inter:
-        _call("moe_gated_ffn", a, x.device, 0, ws)
+    a = _PACK_GATED(d, act, tokens, hidden, inter, *desc, *_mat(x, "x", (tokens, hidden), x),
+                    *_mat(w_gate, "w_gate", wshape, x), *_mat(w_up, "w_up", wshape, x),
+                    *_mat(out["h"], "h", (rows, inter), x),
+                    *_mat(pre, "pre", (rows, 2 * inter), x), *_NONE * 4)
+    _GATED(a, x.device, ws)
     return out
 
 
@@ -253,15 +280,13 @@ def _gated_backward(dh, pre, x, w_gate, w_up, activation, out, ws, lay, tile_m, 
         if out.get("dx") is not None:
             out["dx"].zero_()
         return out
-    a = GatedFfnArgs(d, act, tokens, hidden, inter, desc, _mat(x, "x", (tokens, hidden), x),
-                     _mat(w_gate, "w_gate", wshape, x), _mat(w_up, "w_up", wshape, x),
-                     (None, 0, 0), _mat(pre, "pre", (rows, 2 * inter), x),
-                     _mat(dh, "dh", (rows, inter), x),
-                     _mat(out.get("dx"), "dx", (rows, hidden), x),
-                     _mat(out.get("dw_gate"), "dw_gate", wshape, x),
-                     _mat(out.get("dw_up"), "dw_up", wshape, x))
-    if hidden and inter:
-        _call("moe_gated_ffn_backward", a, x.device, 1, ws)
+    a = _PACK_GATED(d, act, tokens, hidden, inter, *desc, *_mat(x, "x", (tokens, hidden), x),
+                    *_mat(w_gate, "w_gate", wshape, x), *_mat(w_up, "w_up", wshape, x), *_NONE,
+                    *_mat(pre, "pre", (rows, 2 * inter), x), *_mat(dh, "dh", (rows, inter), x),
+                    *_mat(out.get("dx"), "dx", (rows, hidden), x),
+                    *_mat(out.get("dw_gate"), "dw_gate", wshape, x),
+                    *_mat(out.get("dw_up"), "dw_up", wshape, x))
+    _GATED_BACKWARD(a, x.device, ws)
     return out
 
 
@@ -310,12 +335,13 @@ def _linear(x, w, bias, activation, residual, save_pre, out, ws, lay, tile_m):
             if t is not None:
                 t.zero_()
         return out
-    a = LinearArgs(d, act, rows, n_in, n_out, desc, _mat(x, "x", (rows, n_in), x),
-                   _mat(w, "w", (*lead, n_out, n_in), x), _vec(bias, "bias", (*lead, n_out), x),
-                   _mat(residual, "residual", (rows, n_out), x),
-                   _mat(out["y"], "y", (rows, n_out), x), _mat(pre, "pre", (rows, n_out), x))
-    if n_out:
-        _call("moe_linear", a, x.device, 0, ws)
+    a = _PACK_LINEAR(d, act, rows, n_in, n_out, *desc, *_mat(x, "x", (rows, n_in), x),
+                     *_mat(w, "w", (*lead, n_out, n_in), x),
+                     *_vec(bias, "bias", (*lead, n_out), x),
+                     *_mat(residual, "residual", (rows, n_out), x),
+                     *_mat(out["y"], "y", (rows, n_out), x),
+                     *_mat(pre, "pre", (rows, n_out), x), *_NONE * 4)
+    _LINEAR(a, x.device, ws)
     return out
 
 
@@ -364,15 +390,14 @@ def _linear_backward(dy, x, w, pre, activation, bias_grad, out, ws, lay, tile_m)
         if out.get("dx") is not None:
             out["dx"].zero_()
         return out
-    a = LinearArgs(d, act, rows, n_in, n_out, desc, _mat(x, "x", (rows, n_in), x),
-                   _mat(w, "w", wshape, x), (None, 0, 0), (None, 0, 0), (None, 0, 0),
-                   _mat(pre, "pre", (rows, n_out), x) if act else (None, 0, 0),
-                   _mat(dy, "dy", (rows, n_out), x),
-                   _mat(out.get("dx"), "dx", (rows, n_in), x),
-                   _mat(out.get("dw"), "dw", wshape, x),
-                   _vec(out.get("dbias"), "dbias", (*lead, n_out), x))
-    if n_out:
-        _call("moe_linear_backward", a, x.device, 1, ws)
+    a = _PACK_LINEAR(d, act, rows, n_in, n_out, *desc, *_mat(x, "x", (rows, n_in), x),
+                     *_mat(w, "w", wshape, x), *_NONE * 3,
+                     *(_mat(pre, "pre", (rows, n_out), x) if act else _NONE),
+                     *_mat(dy, "dy", (rows, n_out), x),
+                     *_mat(out.get("dx"), "dx", (rows, n_in), x),
+                     *_mat(out.get("dw"), "dw", wshape, x),
+                     *_vec(out.get("dbias"), "dbias", (*lead, n_out), x))
+    _LINEAR_BACKWARD(a, x.device, ws)
     return out
 
 
@@ -400,7 +425,6 @@ def expert_linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
 def _combine_args(y_rows, width, d, lay, num_experts, weighted, like, backward, mats, dweights):
     packed = lay["packed"]
     dev = like.device
-    _index(packed, "packed", dev)
     if packed.dim() != 2:
         _fail("packed must have 2 dimensions")
     tokens, top_k = packed.shape
@@ -413,14 +437,14 @@ def _combine_args(y_rows, width, d, lay, num_experts, weighted, like, backward, 
     num_ids = offsets.numel() - 1
     if not 0 <= num_experts <= num_ids:
         _fail(f"num_experts must be between 0 and the {num_ids} ids of the layout")
-    rows = [None, None]
+    rows = (0, 0)
     if backward:
         rows = [_index(lay[k], k, dev, y_rows) for k in ("m_indices", "row_entry")]
-    return CombineArgs(d, width, tokens, y_rows, top_k, num_experts, num_ids,
-                       packed.data_ptr(), _index(lay["inv_perm"], "inv_perm", dev, n),
-                       _index(offsets, "offsets", dev, 1),
-                       _index(lay["padded_offsets"], "padded_offsets", dev, num_ids + 1),
-                       rows[0], rows[1], None if w is None else w.data_ptr(), *mats, dweights)
+    return _PACK_COMBINE(d, width, tokens, y_rows, top_k, num_experts, num_ids,
+                         _index(packed, "packed", dev), _index(lay["inv_perm"], "inv_perm", dev, n),
+                         _index(offsets, "offsets", dev, 1),
+                         _index(lay["padded_offsets"], "padded_offsets", dev, num_ids + 1),
+                         *rows, 0 if w is None else w.data_ptr(), *mats, dweights)
 
 
 def combine(y: torch.Tensor, lay: Dict[str, torch.Tensor], *, num_experts: int,
@@ -435,11 +459,10 @@ def combine(y: torch.Tensor, lay: Dict[str, torch.Tensor], *, num_experts: int,
     if out is None:
         out = torch.empty((tokens, width), dtype=y.dtype, device=y.device)
     a = _combine_args(rows, width, d, lay, num_experts, weighted, y, False,
-                      (_mat(y, "y", (rows, width), y),
-                       _mat(residual, "residual", (tokens, width), y),
-                       _mat(out, "out", (tokens, width), y), (None, 0, 0), (None, 0, 0)), None)
-    if width:
-        _call("moe_combine", a, y.device)
+                      (*_mat(y, "y", (rows, width), y),
+                       *_mat(residual, "residual", (tokens, width), y),
+                       *_mat(out, "out", (tokens, width), y), *_NONE * 2), 0)
+    _COMBINE(a, y.device)
     return out
 
 
@@ -468,10 +491,9 @@ def combine_backward(dout: torch.Tensor, y: Optional[torch.Tensor],
     if lay["packed"].shape[0] != tokens:
         _fail("dout must have one row for each token of the layout")
     a = _combine_args(rows, width, d, lay, num_experts, weighted, dout, True,
-                      (_mat(y, "y", (rows, width), dout), (None, 0, 0), (None, 0, 0),
-                       _mat(dout, "dout", (tokens, width), dout),
-                       _mat(out["dy"], "dy", (rows, width), dout)),
-                      None if dw is None else dw.data_ptr())
-    if width:
-        _call("moe_combine_backward", a, dout.device)
+                      (*_mat(y, "y", (rows, width), dout), *_NONE * 2,
+                       *_mat(dout, "dout", (tokens, width), dout),
+                       *_mat(out["dy"], "dy", (rows, width), dout)),
+                      0 if dw is None else dw.data_ptr())
+    _COMBINE_BACKWARD(a, dout.device)
     return out

@@ -32,6 +32,23 @@ def test_header_and_binding_agree(L):
         assert hasattr(L, n)
 
 
+def test_packed_arguments_have_the_structures_layout():
+    """The binding packs bytes; every field has to land where the structure has it."""
+    def numbers(n):
+        return list(range(1, n + 1))
+
+    def flat(v):
+        if isinstance(v, ctypes.Structure):
+            return [x for name, _ in v._fields_ for x in flat(getattr(v, name))]
+        return [v or 0]
+    for pack, cls, n in ((ffn._PACK_GATED, ffn.GatedFfnArgs, 13 + 27),
+                         (ffn._PACK_LINEAR, ffn.LinearArgs, 13 + 30),
+                         (ffn._PACK_COMBINE, ffn.CombineArgs, 7 + 7 + 15 + 1)):
+        raw = pack(*numbers(n))
+        assert len(raw) == ctypes.sizeof(cls)
+        assert flat(cls.from_buffer_copy(raw)) == numbers(n)
+
+
 def rows(**kw):
     d = dict(counts=P, padded_offsets=P, m_indices=P, row_entry=P, rows=64, num_experts=4,
              tile_m=16, top_k=2)
