@@ -86,7 +86,7 @@ struct Tile {
   static constexpr int A_BYTES = BM * TK * 2, STAGE_BYTES = (BM + BN) * TK * 2;
   static_assert(TK == 32 || TK == 64, "one or two MFMA k-steps in a stage");
   static_assert(A_INSTR * 512 == BM * TK && B_INSTR * 512 == BN * TK, "whole pieces");
-  static_assert((NS - 2) * LOADS_MIN <= 63, "vmcnt range");
+  static_assert((NS - 1) * LOADS_MIN <= 63, "vmcnt range");
   static_assert(BLOCKS * NS * STAGE_BYTES <= 160 * 1024, "LDS of a compute unit");
 };
 
@@ -302,15 +302,17 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
     if (!is_a(q) && B_TR) return lane / (BN / 8) >= left - number(q) * (512 / BN);
     return k_chunk * 8 >= left;
   };
-  // WGRAD with gathered x: the entries of the next stage's rows
+  // WGRAD with gathered x: the entry of the row that piece q of stage s reads,
+  // and those of the next stage to be issued
   int32_t entry[C::B_LOADS];
+  auto entry_of = [&](int s, int q) MOE_INLINE {
+    const int k = number(q) * (512 / BN) + lane / (BN / 8);
+    return g.r.row_entry[k_row0 + min(s * TK + k, K - 1)];
+  };
   auto fetch_entries = [&](int s) MOE_INLINE {
     if constexpr (MODE == WGRAD && GATHER) {
 #pragma unroll
-      for (int q = C::A_LOADS; q < C::LOADS; ++q) {
-        const int k = number(q) * (512 / BN) + lane / (BN / 8);
-        entry[q - C::A_LOADS] = g.r.row_entry[k_row0 + min(s * TK + k, K - 1)];
-      }
+      for (int q = C::A_LOADS; q < C::LOADS; ++q) entry[q - C::A_LOADS] = entry_of(s, q);
     }
   };
   // Stages are issued in order, each followed by next_stage.
@@ -326,7 +328,6 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
                                 number(q) * 1024);
   };
   auto next_stage = [&](int s) MOE_INLINE {  // after stage s
-    fetch_entries(s + 1);
     a_base += a_step;
     b_base += b_step;
     left -= TK;
@@ -397,6 +398,14 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
 #pragma unroll
     for (int j = 0; j < C::FN; ++j) asm volatile("" : "+v"(fb[set][j]));
   };
+  // The entries too: the compiler counts only the loads it knows, so it would
+  // wait for pieces issued after the entries before it uses them.
+  auto settle_entries = [&]() MOE_INLINE {
+    if constexpr (MODE == WGRAD && GATHER) {
+#pragma unroll
+      for (int q = 0; q < C::B_LOADS; ++q) asm volatile("" : "+v"(entry[q]));
+    }
+  };
   // One MFMA k-step on `set`. Between the MFMAs, one at a time, go the fragment
   // reads of k-step rks of stage rs (over the first three quarters) and, with
   // ISSUE, the pieces of stage `is`: an MFMA holds its pipe for 16 cycles, in
@@ -420,7 +429,10 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
       acc[i][j] = D::mfma(fb[set][j], fa[set][i], acc[i][j]);
       __builtin_amdgcn_sched_barrier(0);
     });
-    if constexpr (ISSUE) next_stage(is);
+    if constexpr (ISSUE) {
+      fetch_entries(is + 1);
+      next_stage(is);
+    }
   };
   // The oldest stage in flight has landed for every wave (NS - 2 younger ones
   // may not have), and every wave has read the buffer that is filled next.
@@ -435,19 +447,37 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
     if constexpr (C::KS == 2) step(0, s, 1, std::false_type(), 0);
     wait_stage();
     settle(set);
+    settle_entries();
     step(set, s + 1, 0, std::true_type(), s + NS);
   };
 
   if (nk > 0) {
     start();
-    fetch_entries(0);
-#pragma unroll 1
-    for (int s = 0; s < NS; ++s) {
-      if (s == NS - 1) wait_stage();
+    // all buffers are free: NS stages at once, their entries before them
+    int32_t first[NS][C::B_LOADS];
+    if constexpr (MODE == WGRAD && GATHER) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int q = C::A_LOADS; q < C::LOADS; ++q) first[s][q - C::A_LOADS] = entry_of(s, q);
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int q = 0; q < C::B_LOADS; ++q) asm volatile("" : "+v"(first[s][q]));
+    }
+    unrolled<NS>([&](auto sc) MOE_INLINE {
+      constexpr int s = decltype(sc)::value;
+      if constexpr (MODE == WGRAD && GATHER) {
+#pragma unroll
+        for (int q = 0; q < C::B_LOADS; ++q) entry[q] = first[s][q];
+      }
 #pragma unroll
       for (int q = 0; q < C::LOADS; ++q) issue_piece(s, q);
       next_stage(s);
-    }
+    });
+    fetch_entries(NS);
+    wait_vmcnt_imm<C::LOADS_MIN *(NS - 1)>();
+    asm volatile("s_barrier" ::: "memory");
 #pragma unroll
     for (int f = 0; f < C::FM + C::FN; ++f) read_frag(0, 0, 0, f);
     if constexpr (C::KS == 2) {
