@@ -338,35 +338,33 @@ static int run_linear_backward(const moe_linear_args *a, Arena &ws, hipStream_t 
   int status = MOE_OK;
   GemmArgs g = gemm_args(a->rows, rows, false);
   const uint16_t *dy = (const uint16_t *)a->dy.p, *pre = (const uint16_t *)a->pre.p;
+  // dz: dy itself without an activation, where its pieces are aligned
+  const bool products = a->dx.p || a->dw.p, none = a->activation == MOE_ACT_NONE;
+  Operand dz = {};
+  if (products && none) dz = operand(a->dy, rows, O, 1, ws, st, &status);
+  if (products && !none) dz = {ws.take((size_t)rows * Oa * 2), Oa, 0};
+  uint16_t *dz_out = products && !none ? const_cast<uint16_t *>(dz.p) : nullptr;
   if (a->dbias.p) {
     const int S = bias_splits(a->rows, rows);
     float *part = reinterpret_cast<float *>(ws.take((size_t)mats * S * O * 4));
-    if (!ws.dry) {
+    if (!ws.dry && status == MOE_OK) {
+      const dim3 grid((O + 63) / 64, S, mats), block(8, BIAS_ROWS);
       const auto sums = bf ? bias_grad_kernel<Bf16> : bias_grad_kernel<F16>;
-      sums<<<dim3((O + 63) / 64, S, mats), dim3(8, BIAS_ROWS), 0, st>>>(
-          dy, a->dy.ld, pre, a->pre.ld, rows, O, a->activation, g.r, S, part);
+      sums<<<grid, block, 0, st>>>(dy, a->dy.ld, pre, a->pre.ld, rows, O, a->activation, g.r, S,
+                                   part, dz_out);
       MOE_TRY(hip_status());
       const auto join = bf ? bias_sum_kernel<Bf16> : bias_sum_kernel<F16>;
-      join<<<dim3((O + 255) / 256, 1, mats), 256, 0, st>>>(part, S, O, (uint16_t *)a->dbias.p,
-                                                           a->dbias.stride);
+      join<<<dim3((O + 63) / 64, 1, mats), 256, 0, st>>>(part, S, O, (uint16_t *)a->dbias.p,
+                                                         a->dbias.stride);
       MOE_TRY(hip_status());
     }
+  } else if (dz_out && !ws.dry && rows > 0) {
+    const auto kernel = bf ? linear_dz_kernel<Bf16> : linear_dz_kernel<F16>;
+    kernel<<<row_grid(rows, Oa, 1), dim3(COL_THREADS, ROW_THREADS), 0, st>>>(
+        dy, a->dy.ld, pre, a->pre.ld, rows, O, a->activation, g.r, dz_out);
+    MOE_TRY(hip_status());
   }
-  if (!a->dx.p && !a->dw.p) return MOE_OK;
-  // dz: dy itself without an activation, where its pieces are aligned
-  Operand dz;
-  if (a->activation == MOE_ACT_NONE) {
-    dz = operand(a->dy, rows, O, 1, ws, st, &status);
-  } else {
-    uint16_t *p = ws.take((size_t)rows * Oa * 2);
-    dz = {p, Oa, 0};
-    if (!ws.dry && rows > 0) {
-      const auto kernel = bf ? linear_dz_kernel<Bf16> : linear_dz_kernel<F16>;
-      kernel<<<row_grid(rows, Oa, 1), dim3(COL_THREADS, ROW_THREADS), 0, st>>>(
-          dy, a->dy.ld, pre, a->pre.ld, rows, O, a->activation, g.r, p);
-      MOE_TRY(hip_status());
-    }
-  }
+  if (!products) return status;
   Operand x = {}, w = {};
   if (a->dw.p) x = operand(a->x, rows, I, 1, ws, st, &status);
   if (a->dx.p && rows > 0) w = operand(a->w, O, I, mats, ws, st, &status);

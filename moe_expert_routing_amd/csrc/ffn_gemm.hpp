@@ -182,17 +182,15 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
       e = g.r.m_indices[m0];
       if (e < 0 || e >= g.r.num_experts || g.a_rows == 0) {  // no entry here: zeros
         constexpr int RUNS = (MODE == GATED ? BN / 2 : BN) / 8;
-        const bool vec_c = vec8(g.c0, g.ldc0), vec_p = vec8(g.pre, g.ldp);
-        const bool vec_u = vec8(g.pre, g.ldp, g.N);
         const s16x8 zero = {0, 0, 0, 0, 0, 0, 0, 0};
         for (int i = threadIdx.x; i < BM * RUNS; i += C::NTHREADS) {
           const int64_t m = m0 + i / RUNS;
           const int n = n0 + i % RUNS * 8;
           if (m >= g.M || n >= g.N) continue;
-          store8_raw(g.c0 + m * g.ldc0, n, g.N, vec_c, zero);
+          store8_raw(g.c0 + m * g.ldc0, n, g.N, zero);
           if (MODE <= LINEAR && g.pre) {
-            store8_raw(g.pre + m * g.ldp, n, g.N, vec_p, zero);
-            if (MODE == GATED) store8_raw(g.pre + m * g.ldp + g.N, n, g.N, vec_u, zero);
+            store8_raw(g.pre + m * g.ldp, n, g.N, zero);
+            if (MODE == GATED) store8_raw(g.pre + m * g.ldp + g.N, n, g.N, zero);
           }
         }
         return;
@@ -533,11 +531,9 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
   const f32x8 zero8 = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   uint16_t *out = MODE == WGRAD ? (seg0 ? g.c1 + e * g.c_stride1 : g.c0 + e * g.c_stride0) : g.c0;
   const int64_t ldc = MODE == WGRAD && seg0 ? g.ldc1 : g.ldc0;
-  const bool vec_c = vec8(out, ldc), vec_p = vec8(g.pre, g.ldp), vec_u = vec8(g.pre, g.ldp, g.N);
-  const bool vec_r = vec8(g.res, g.ldr);
   if constexpr (MODE == GATED) {
     // what is turned: h, and with pre the two projections as well
-    auto rows_out = [&](int i, auto value, uint16_t *to, int64_t ld, int width, int col, bool vec)
+    auto rows_out = [&](int i, auto value, uint16_t *to, int64_t ld, int width, int col)
         MOE_INLINE {
       turn_order();
 #pragma unroll
@@ -548,7 +544,7 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
         const f32x8 v = turn_out(p);
         const int64_t m = row_of(i, p);
         if (cols && m < g.M)
-          store8<D>(to + m * ld, col, width, vec, is_real(m) ? v : zero8);
+          store8<D>(to + m * ld, col, width, is_real(m) ? v : zero8);
       }
     };
 #pragma unroll
@@ -558,16 +554,15 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
 #pragma unroll
         for (int v = 0; v < 4; ++v) h[v] = act_value(gt[v], g.act) * up4[v];
         return h;
-      }, out, ldc, g.N, n, vec_c);
+      }, out, ldc, g.N, n);
       if (g.pre) {
-        rows_out(i, [&](f32x4 gt, f32x4) MOE_INLINE { return gt; }, g.pre, g.ldp, g.N, n, vec_p);
-        rows_out(i, [&](f32x4, f32x4 up4) MOE_INLINE { return up4; }, g.pre + g.N, g.ldp, g.N, n,
-                 vec_u);
+        rows_out(i, [&](f32x4 gt, f32x4) MOE_INLINE { return gt; }, g.pre, g.ldp, g.N, n);
+        rows_out(i, [&](f32x4, f32x4 up4) MOE_INLINE { return up4; }, g.pre + g.N, g.ldp, g.N, n);
       }
     }
   } else {
     f32x8 bias = zero8;
-    if (MODE == LINEAR && g.bias && cols) bias = load8<D>(g.bias + e * g.bias_stride, n, g.N, false);
+    if (MODE == LINEAR && g.bias && cols) bias = load8<D>(g.bias + e * g.bias_stride, n, g.N);
 #pragma unroll
     for (int i = 0; i < C::FM; ++i) {
       turn_order();
@@ -583,18 +578,18 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
         if constexpr (MODE == LINEAR) {
 #pragma unroll
           for (int v = 0; v < 8; ++v) z[v] += bias[v];
-          if (g.pre) store8<D>(g.pre + m * g.ldp, n, g.N, vec_p, real ? z : zero8);
+          if (g.pre) store8<D>(g.pre + m * g.ldp, n, g.N, real ? z : zero8);
           if (g.act != MOE_ACT_NONE) {
 #pragma unroll
             for (int v = 0; v < 8; ++v) z[v] = act_value(z[v], g.act);
           }
           if (g.res && real) {
-            const f32x8 r = load8<D>(g.res + m * g.ldr, n, g.N, vec_r);
+            const f32x8 r = load8<D>(g.res + m * g.ldr, n, g.N);
 #pragma unroll
             for (int v = 0; v < 8; ++v) z[v] += r[v];
           }
         }
-        store8<D>(out + m * ldc, n, g.N, vec_c, real ? z : zero8);
+        store8<D>(out + m * ldc, n, g.N, real ? z : zero8);
       }
     }
   }

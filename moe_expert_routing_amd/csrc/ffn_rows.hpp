@@ -24,18 +24,9 @@ __global__ __launch_bounds__(COL_THREADS *ROW_THREADS) void pad_rows_kernel(
   if (c >= cols8) return;
   src += blockIdx.z * stride;
   dst += (int64_t)blockIdx.z * rows * cols8;
-  const bool vec = vec8(src, ld);
   for (int64_t r = blockIdx.y * ROW_THREADS + threadIdx.y; r < rows;
        r += (int64_t)gridDim.y * ROW_THREADS) {
-    s16x8 w = {0, 0, 0, 0, 0, 0, 0, 0};
-    const uint16_t *p = src + r * ld;
-    if (vec && c + 8 <= cols) {
-      w = *reinterpret_cast<const s16x8 *>(p + c);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < cols) w[i] = (short)p[c + i];
-    }
+    const s16x8 w = load8_raw(src + r * ld, c, cols);
     *reinterpret_cast<s16x8 *>(dst + r * cols8 + c) = w;
   }
 }
@@ -47,22 +38,12 @@ __global__ __launch_bounds__(COL_THREADS *ROW_THREADS) void gather_rows_kernel(
     uint16_t *__restrict__ dst, int cols8) {
   const int c = (blockIdx.x * COL_THREADS + threadIdx.x) * 8;
   if (c >= cols8) return;
-  const bool vec = vec8(x, ld);
   for (int64_t m = blockIdx.y * ROW_THREADS + threadIdx.y; m < rows;
        m += (int64_t)gridDim.y * ROW_THREADS) {
     s16x8 w = {0, 0, 0, 0, 0, 0, 0, 0};
     const int32_t entry = row_is_real(r, m) ? r.row_entry[m] : -1;
     const int64_t t = entry / r.top_k;
-    if (entry >= 0 && t < tokens) {
-      const uint16_t *p = x + t * ld;
-      if (vec && c + 8 <= cols) {
-        w = *reinterpret_cast<const s16x8 *>(p + c);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (c + i < cols) w[i] = (short)p[c + i];
-      }
-    }
+    if (entry >= 0 && t < tokens) w = load8_raw(x + t * ld, c, cols);
     *reinterpret_cast<s16x8 *>(dst + m * cols8 + c) = w;
   }
 }
@@ -78,13 +59,12 @@ __global__ __launch_bounds__(COL_THREADS *ROW_THREADS) void gated_dz_kernel(
   const int Fa = (F + 7) & ~7;
   const int c = (blockIdx.x * COL_THREADS + threadIdx.x) * 8;
   if (c >= Fa) return;
-  const bool vh = vec8(dh, ld_dh), vp = vec8(pre, ld_pre), vu = vec8(pre, ld_pre, F);
   for (int64_t m = blockIdx.y * ROW_THREADS + threadIdx.y; m < rows;
        m += (int64_t)gridDim.y * ROW_THREADS) {
     if (!row_is_real(r, m)) continue;
-    const f32x8 d = load8<D>(dh + m * ld_dh, c, F, vh);
-    const f32x8 gt = load8<D>(pre + m * ld_pre, c, F, vp);
-    const f32x8 up = load8<D>(pre + m * ld_pre + F, c, F, vu);
+    const f32x8 d = load8<D>(dh + m * ld_dh, c, F);
+    const f32x8 gt = load8<D>(pre + m * ld_pre, c, F);
+    const f32x8 up = load8<D>(pre + m * ld_pre + F, c, F);
     f32x8 dg, du;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -99,8 +79,7 @@ __global__ __launch_bounds__(COL_THREADS *ROW_THREADS) void gated_dz_kernel(
   }
 }
 
-// dz [rows, Oa] = dy act'(pre), rounded once; as above. Without an
-// activation pre is not read and this is a padded copy.
+// dz [rows, Oa] = dy act'(pre), rounded once; as above.
 template <class D>
 __global__ __launch_bounds__(COL_THREADS *ROW_THREADS) void linear_dz_kernel(
     const uint16_t *__restrict__ dy, int64_t ld_dy, const uint16_t *__restrict__ pre,
@@ -108,33 +87,32 @@ __global__ __launch_bounds__(COL_THREADS *ROW_THREADS) void linear_dz_kernel(
   const int Oa = (O + 7) & ~7;
   const int c = (blockIdx.x * COL_THREADS + threadIdx.x) * 8;
   if (c >= Oa) return;
-  const bool vd = vec8(dy, ld_dy), vp = vec8(pre, ld_pre);
   for (int64_t m = blockIdx.y * ROW_THREADS + threadIdx.y; m < rows;
        m += (int64_t)gridDim.y * ROW_THREADS) {
     if (!row_is_real(r, m)) continue;
-    f32x8 d = load8<D>(dy + m * ld_dy, c, O, vd);
-    if (act != MOE_ACT_NONE) {
-      const f32x8 z = load8<D>(pre + m * ld_pre, c, O, vp);
+    f32x8 d = load8<D>(dy + m * ld_dy, c, O);
+    const f32x8 z = load8<D>(pre + m * ld_pre, c, O);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float v, s;
-        act_value_slope(z[i], act, v, s);
-        d[i] *= s;
-      }
+    for (int i = 0; i < 8; ++i) {
+      float v, s;
+      act_value_slope(z[i], act, v, s);
+      d[i] *= s;
     }
     *reinterpret_cast<s16x8 *>(dz + m * (int64_t)Oa + c) = pack8<D>(d);
   }
 }
 
 // Column sums of dz = dy act'(pre) in fp32, from dy and pre themselves: the
-// bias gradient does not see dz's rounding. A block sums 64 columns of one of
-// S row ranges: 8 lanes across, 32 rows at a time, then the 32 partial
-// sums in a fixed order. part [mats][S][O].
+// bias gradient does not see dz's rounding; dz itself is written on the way
+// where it is wanted (not NULL). A block sums 64 columns of one of S row
+// ranges: 8 lanes across, 32 rows at a time, then the 32 partial sums in a
+// fixed order. part [mats][S][O].
 constexpr int BIAS_ROWS = 32;
 template <class D>
 __global__ __launch_bounds__(8 * BIAS_ROWS) void bias_grad_kernel(
     const uint16_t *__restrict__ dy, int64_t ld_dy, const uint16_t *__restrict__ pre,
-    int64_t ld_pre, int64_t rows, int O, int act, Rows r, int S, float *__restrict__ part) {
+    int64_t ld_pre, int64_t rows, int O, int act, Rows r, int S, float *__restrict__ part,
+    uint16_t *__restrict__ dz) {
   __shared__ float sum[BIAS_ROWS][65];
   const int c = blockIdx.x * 64 + threadIdx.x * 8;
   int64_t first = 0, n = rows;
@@ -143,23 +121,22 @@ __global__ __launch_bounds__(8 * BIAS_ROWS) void bias_grad_kernel(
     n = min(max((int64_t)r.counts[blockIdx.z], (int64_t)0), r.rows - first);
   }
   const int64_t per = (n + S - 1) / S, lo = min(n, blockIdx.y * per), hi = min(n, lo + per);
-  const bool vd = vec8(dy, ld_dy), vp = vec8(pre, ld_pre);
   f32x8 a = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (c < O) {
     for (int64_t m = first + lo + threadIdx.y; m < first + hi; m += BIAS_ROWS) {
-      const f32x8 d = load8<D>(dy + m * ld_dy, c, O, vd);
+      f32x8 d = load8<D>(dy + m * ld_dy, c, O);
       if (act != MOE_ACT_NONE) {
-        const f32x8 z = load8<D>(pre + m * ld_pre, c, O, vp);
+        const f32x8 z = load8<D>(pre + m * ld_pre, c, O);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float v, s;
           act_value_slope(z[i], act, v, s);
-          a[i] += d[i] * s;
+          d[i] *= s;
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] += d[i];
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a[i] += d[i];
+      if (dz) *reinterpret_cast<s16x8 *>(dz + m * ((O + 7) & ~7) + c) = pack8<D>(d);
     }
   }
 #pragma unroll
@@ -172,15 +149,23 @@ __global__ __launch_bounds__(8 * BIAS_ROWS) void bias_grad_kernel(
     part[((int64_t)blockIdx.z * S + blockIdx.y) * O + blockIdx.x * 64 + t] = v;
   }
 }
+// The S partial sums of 64 columns: four ranges of them, then the four.
 template <class D>
 __global__ __launch_bounds__(256) void bias_sum_kernel(const float *__restrict__ part, int S, int O,
                                                        uint16_t *__restrict__ db, int64_t stride) {
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= O) return;
-  const float *p = part + (int64_t)blockIdx.z * S * O + c;
+  __shared__ float sum[4][64];
+  const int c = blockIdx.x * 64 + threadIdx.x % 64, q = threadIdx.x / 64;
   float v = 0.f;
-  for (int s = 0; s < S; ++s) v += p[(int64_t)s * O];
-  db[blockIdx.z * stride + c] = from_f<D>(v);
+  if (c < O) {
+    const float *p = part + (int64_t)blockIdx.z * S * O + c;
+#pragma unroll 8
+    for (int s = S * q / 4; s < S * (q + 1) / 4; ++s) v += p[(int64_t)s * O];
+  }
+  sum[q][threadIdx.x % 64] = v;
+  __syncthreads();
+  if (q == 0 && c < O)
+    db[blockIdx.z * stride + c] = from_f<D>(((v + sum[1][threadIdx.x]) + sum[2][threadIdx.x]) +
+                                            sum[3][threadIdx.x]);
 }
 
 // ------------------------------------------------------------------ combine
@@ -233,19 +218,18 @@ __global__ __launch_bounds__(COMBINE_THREADS) void combine_kernel(const CombineA
   }
   __syncthreads();
   const int n = n_rows;
-  const bool vy = vec8(a.y, a.ld_y), vr = vec8(a.residual, a.ld_res), vo = vec8(a.out, a.ld_out);
   for (int c = (blockIdx.y * COMBINE_THREADS + threadIdx.x) * 8; c < a.width;
        c += gridDim.y * COMBINE_THREADS * 8) {
     f32x8 s = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (a.residual) s = load8<D>(a.residual + t * a.ld_res, c, a.width, vr);
+    if (a.residual) s = load8<D>(a.residual + t * a.ld_res, c, a.width);
 #pragma unroll 4
     for (int k = 0; k < n; ++k) {
-      const f32x8 v = load8<D>(a.y + rows[k] * a.ld_y, c, a.width, vy);
+      const f32x8 v = load8<D>(a.y + rows[k] * a.ld_y, c, a.width);
       const float w = ws[k];
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[i] = fmaf(w, v[i], s[i]);
     }
-    store8<D>(a.out + t * a.ld_out, c, a.width, vo, s);
+    store8<D>(a.out + t * a.ld_out, c, a.width, s);
   }
 }
 
@@ -265,21 +249,20 @@ __global__ __launch_bounds__(COMBINE_THREADS) void combine_backward_kernel(const
                     entry < a.tokens * a.top_k;
   const int64_t t = real ? entry / a.top_k : 0;
   const float w = real ? (a.weights ? a.weights[entry] : 1.f) : 0.f;
-  const bool vy = vec8(a.y, a.ld_y), vd = vec8(a.dout, a.ld_dout), vo = vec8(a.dy, a.ld_dy);
   float dot = 0.f;
   for (int c = threadIdx.x * 8; c < a.width; c += COMBINE_THREADS * 8) {
     f32x8 d = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (real) {
-      d = load8<D>(a.dout + t * a.ld_dout, c, a.width, vd);
+      d = load8<D>(a.dout + t * a.ld_dout, c, a.width);
       if (a.dweights) {
-        const f32x8 v = load8<D>(a.y + row * a.ld_y, c, a.width, vy);
+        const f32x8 v = load8<D>(a.y + row * a.ld_y, c, a.width);
 #pragma unroll
         for (int i = 0; i < 8; ++i) dot = fmaf(d[i], v[i], dot);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) d[i] *= w;
     }
-    store8<D>(a.dy + row * a.ld_dy, c, a.width, vo, d);
+    store8<D>(a.dy + row * a.ld_dy, c, a.width, d);
   }
   if (!real || !a.dweights) return;
 #pragma unroll

@@ -104,8 +104,6 @@ __global__ __launch_bounds__(64 * SKINNY_WAVES) void skinny_kernel(const GemmArg
   }
   __syncthreads();
   // eight columns of a row a thread
-  const bool vec_c = vec8(g.c0, g.ldc0), vec_p = vec8(g.pre, g.ldp);
-  const bool vec_u = vec8(g.pre, g.ldp, g.N), vec_r = vec8(g.res, g.ldr);
   constexpr int RUNS = NC / 8;
   for (int o = threadIdx.x; o < GW * BM * RUNS; o += 64 * SKINNY_WAVES) {
     const int c = o % RUNS * 8, gr = o / RUNS % GW, r = o / (RUNS * GW);
@@ -127,29 +125,29 @@ __global__ __launch_bounds__(64 * SKINNY_WAVES) void skinny_kernel(const GemmArg
     }
     if constexpr (MODE == GATED) {
       if (g.pre) {
-        store8<D>(g.pre + m * g.ldp, n, g.N, vec_p, z);
-        store8<D>(g.pre + m * g.ldp + g.N, n, g.N, vec_u, u);
+        store8<D>(g.pre + m * g.ldp, n, g.N, z);
+        store8<D>(g.pre + m * g.ldp + g.N, n, g.N, u);
       }
 #pragma unroll
       for (int v = 0; v < 8; ++v) z[v] = real ? act_value(z[v], g.act) * u[v] : 0.f;
     } else {
       if (real && g.bias) {
-        const f32x8 b = load8<D>(g.bias + e * g.bias_stride, n, g.N, false);
+        const f32x8 b = load8<D>(g.bias + e * g.bias_stride, n, g.N);
 #pragma unroll
         for (int v = 0; v < 8; ++v) z[v] += b[v];
       }
-      if (g.pre) store8<D>(g.pre + m * g.ldp, n, g.N, vec_p, z);
+      if (g.pre) store8<D>(g.pre + m * g.ldp, n, g.N, z);
       if (real && g.act != MOE_ACT_NONE) {
 #pragma unroll
         for (int v = 0; v < 8; ++v) z[v] = act_value(z[v], g.act);
       }
       if (real && g.res) {
-        const f32x8 b = load8<D>(g.res + m * g.ldr, n, g.N, vec_r);
+        const f32x8 b = load8<D>(g.res + m * g.ldr, n, g.N);
 #pragma unroll
         for (int v = 0; v < 8; ++v) z[v] += b[v];
       }
     }
-    store8<D>(g.c0 + m * g.ldc0, n, g.N, vec_c, z);
+    store8<D>(g.c0 + m * g.ldc0, n, g.N, z);
   }
 #endif
 }

@@ -101,22 +101,24 @@ __device__ __forceinline__ void act_value_slope(float z, int act, float &value, 
   }
 }
 
-// Eight elements at column c of a row that has n columns; zeros past n.
-template <class D>
-__device__ __forceinline__ f32x8 load8(const uint16_t *row, int c, int n, bool vec) {
+// Eight elements at column c of a row that has n columns; zeros past n. Global
+// memory takes 16-byte accesses at any element's address.
+typedef s16x8 s16x8_any __attribute__((aligned(2)));
+__device__ __forceinline__ s16x8 load8_raw(const uint16_t *row, int c, int n) {
+  if (c + 8 <= n) return *reinterpret_cast<const s16x8_any *>(row + c);
   s16x8 w = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (vec && c + 8 <= n) {
-    w = *reinterpret_cast<const s16x8 *>(row + c);
-  } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < n) w[i] = (short)row[c + i];
-  }
-  return unpack8<D>(w);
+  for (int i = 0; i < 8; ++i)
+    if (c + i < n) w[i] = (short)row[c + i];
+  return w;
 }
-__device__ __forceinline__ void store8_raw(uint16_t *row, int c, int n, bool vec, s16x8 w) {
-  if (vec && c + 8 <= n) {
-    *reinterpret_cast<s16x8 *>(row + c) = w;
+template <class D>
+__device__ __forceinline__ f32x8 load8(const uint16_t *row, int c, int n) {
+  return unpack8<D>(load8_raw(row, c, n));
+}
+__device__ __forceinline__ void store8_raw(uint16_t *row, int c, int n, s16x8 w) {
+  if (c + 8 <= n) {
+    *reinterpret_cast<s16x8_any *>(row + c) = w;
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -124,12 +126,8 @@ __device__ __forceinline__ void store8_raw(uint16_t *row, int c, int n, bool vec
   }
 }
 template <class D>
-__device__ __forceinline__ void store8(uint16_t *row, int c, int n, bool vec, f32x8 v) {
-  store8_raw(row, c, n, vec, pack8<D>(v));
-}
-// whether 8 consecutive elements at a multiple-of-8 column are one aligned load
-__device__ __forceinline__ bool vec8(const void *p, int64_t ld, int64_t off = 0) {
-  return (((uintptr_t)p & 15) | (uintptr_t)((ld | off) & 7)) == 0;
+__device__ __forceinline__ void store8(uint16_t *row, int c, int n, f32x8 v) {
+  store8_raw(row, c, n, pack8<D>(v));
 }
 
 // The expert of a row's tile and whether one row holds an entry of it.
