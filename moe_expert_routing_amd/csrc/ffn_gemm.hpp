@@ -19,10 +19,10 @@
 // lanes); chunk c of k-row k sits at c ^ swz(k), which puts the 4 rows and the
 // two 16-lane groups of a pass on different banks.
 //
-// Both operands go from global memory straight into LDS
-// (global_load_lds_dwordx4). NS stage buffers: NS - 1 stages are in flight
-// while one is consumed. The fragments of one MFMA k-step are read from LDS
-// while the previous step's MFMAs run.
+// Both operands go from global memory straight into LDS, NS stages of 64 k
+// deep: stage s + NS is issued as soon as every wave has read stage s. The
+// fragments of one MFMA k-step are read from LDS while the previous step's
+// MFMAs run.
 //
 // The weights are the MFMA's first operand: a lane then holds 4 consecutive n
 // of one row m, so the epilogue stores 8 bytes and the two projections of a
@@ -71,20 +71,21 @@ __device__ __forceinline__ void lds_piece(const uint8_t *p, uint32_t o, uint8_t 
 }
 #endif
 
-template <int BM_, int BN_, int WM_, int WN_, int TK_, int NS_, int BLOCKS_>
+constexpr int TK = 64;  // k of a stage: two MFMA k-steps
+
+template <int BM_, int BN_, int WM_, int WN_, int NS_, int BLOCKS_>
 struct Tile {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, TK = TK_, NS = NS_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_;
   static constexpr int BLOCKS = BLOCKS_;  // blocks per compute unit
   static constexpr int WAVES_N = BN / WN, NW = (BM / WM) * WAVES_N;
   static constexpr int NTHREADS = 64 * NW;
-  static constexpr int FM = WM / 16, FN = WN / 16, KS = TK / 32;
+  static constexpr int FM = WM / 16, FN = WN / 16;
   static constexpr int A_INSTR = BM * TK / 512, B_INSTR = BN * TK / 512;  // 1 KB pieces
   // pieces of one wave, where they do not come out even the most; and what
   // every wave has at least
   static constexpr int A_LOADS = (A_INSTR + NW - 1) / NW, B_LOADS = (B_INSTR + NW - 1) / NW;
   static constexpr int LOADS = A_LOADS + B_LOADS, LOADS_MIN = A_INSTR / NW + B_INSTR / NW;
   static constexpr int A_BYTES = BM * TK * 2, STAGE_BYTES = (BM + BN) * TK * 2;
-  static_assert(TK == 32 || TK == 64, "one or two MFMA k-steps in a stage");
   static_assert(A_INSTR * 512 == BM * TK && B_INSTR * 512 == BN * TK, "whole pieces");
   static_assert((NS - 1) * LOADS_MIN <= 63, "vmcnt range");
   static_assert(BLOCKS * NS * STAGE_BYTES <= 160 * 1024, "LDS of a compute unit");
@@ -104,6 +105,7 @@ template <int N>
 __device__ __forceinline__ void wait_vmcnt_imm() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
+
 // Position of 16-byte chunk c in k-row k of an operand staged as it lies in
 // memory, R columns wide.
 template <int R>
@@ -137,7 +139,7 @@ template <class D, int MODE, class C, bool GATHER>
 __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm_kernel(
     const GemmArgs g) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  constexpr int BM = C::BM, BN = C::BN, NS = C::NS, TK = C::TK;
+  constexpr int BM = C::BM, BN = C::BN, NS = C::NS;
   constexpr bool A_TR = MODE == WGRAD, B_TR = MODE == DGRAD || MODE == WGRAD;
   static_assert((!A_TR || BM >= 32) && (!B_TR || BN >= 32), "chunks for swz to permute");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * C::STAGE_BYTES];
@@ -152,9 +154,9 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
     // one expert and projection after the other, all its tiles together
     const int per = g.m_tiles * g.n_tiles;
     const int chunk = blockIdx.x / per;
+    tile_at(tile_of_block(blockIdx.x % per, per, per), g.m_tiles, g.n_tiles, mt, nt);
     e = chunk / g.segs;
     seg0 = chunk % g.segs;
-    tile_at(tile_of_block(blockIdx.x % per, per, per), g.m_tiles, g.n_tiles, mt, nt);
     if (grouped) {
       const int64_t p0 = g.r.padded_offsets[e], cnt = g.r.counts[e];
       k_row0 = min(max(p0, (int64_t)0), g.r.rows);
@@ -226,9 +228,8 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
   };
   // GATED: B rows alternate, 16 of the gate's and 16 of the other's. A wave's
   // pieces are all of one projection.
-  constexpr int PIECE_ROWS = 512 / TK;
-  static_assert(MODE != GATED || C::NW * PIECE_ROWS % 32 == 0, "one projection for a wave");
-  const bool up = MODE == GATED && ((wave * PIECE_ROWS) >> 4 & 1);
+  static_assert(MODE != GATED || C::NW * 8 % 32 == 0, "one projection for a wave");
+  const bool up = MODE == GATED && ((wave * 8) >> 4 & 1);
   const int64_t ldb = up ? g.ldb1 : g.ldb0;
   const uint8_t *a_base, *b_base, *b_next = nullptr;
   int64_t a_step, b_step;
@@ -250,19 +251,9 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
     b_base = reinterpret_cast<const uint8_t *>((up ? b1 : b0) + n0 * ldb);
     b_step = TK * 2;
   }
-  // (row, 8-element chunk) of a lane in piece `id` of an operand with
-  // contiguous k. 64 k: 128-byte rows, chunk c at c ^ (row & 7). 32 k: two
-  // rows in a 128-byte line, the line's chunk c at c ^ (line & 7).
-  auto row_chunk = [&](int id, int &row, int &c) MOE_INLINE {
-    if constexpr (TK == 64) {
-      row = id * 8 + (lane >> 3);
-      c = (lane & 7) ^ (lane >> 3);
-    } else {
-      const int line = lane >> 3, c8 = (lane & 7) ^ line;
-      row = id * 16 + line * 2 + (c8 >> 2);
-      c = c8 & 3;
-    }
-  };
+  // a lane's row and 8-element chunk in a piece of an operand with contiguous
+  // k: 128-byte rows, chunk c at c ^ (row & 7)
+  const int piece_row = lane >> 3, piece_chunk = (lane & 7) ^ (lane >> 3);
   uint32_t off[C::LOADS];
   auto start = [&]() MOE_INLINE {
 #pragma unroll
@@ -273,32 +264,27 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
         const int k = (id * 64 + lane) / PER, c = (lane % PER) ^ swz<BM>(k);
         off[q] = (uint32_t)(k * g.lda + min(m0 + c * 8, m_last)) * 2;
       } else if (is_a(q)) {
-        int r, c;
-        row_chunk(id, r, c);
-        const int row = min(m0 + r, g.M - 1);
+        const int row = min(m0 + id * 8 + piece_row, g.M - 1);
         const int64_t at = GATHER ? gathered_row(g.r.row_entry[row]) : row - m0;
-        off[q] = (uint32_t)(at * g.lda + c * 8) * 2;
+        off[q] = (uint32_t)(at * g.lda + piece_chunk * 8) * 2;
       } else if (B_TR) {
         constexpr int PER = BN / 8;
         const int k = (id * 64 + lane) / PER, c = (lane % PER) ^ swz<BN>(k);
         // gathered: the row is added when its entry is known
         off[q] = (uint32_t)((MODE == WGRAD && GATHER ? 0 : k * ldb) + min(n0 + c * 8, n_last)) * 2;
       } else {
-        int j, c;
-        row_chunk(id, j, c);
+        int j = id * 8 + piece_row;
         if (MODE == GATED) j = (j >> 5) * 16 + (j & 15);
-        off[q] = (uint32_t)(min(j, g.N - 1 - n0) * ldb + c * 8) * 2;
+        off[q] = (uint32_t)(min(j, g.N - 1 - n0) * ldb + piece_chunk * 8) * 2;
       }
     }
   };
   // Whether piece q of a stage with `left` k from its start on lies past them:
   // such pieces, a stage's tail or stages after the last, load zeros.
-  int k_chunk, c_row;
-  row_chunk(0, c_row, k_chunk);
   auto past = [&](int q, int left) MOE_INLINE {
     if (is_a(q) && A_TR) return lane / (BM / 8) >= left - number(q) * (512 / BM);
     if (!is_a(q) && B_TR) return lane / (BN / 8) >= left - number(q) * (512 / BN);
-    return k_chunk * 8 >= left;
+    return piece_chunk * 8 >= left;
   };
   // WGRAD with gathered x: the entry of the row that piece q of stage s reads,
   // and those of the next stage to be issued
@@ -348,12 +334,8 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
 
   s16x8 fa[2][C::FM], fb[2][C::FN];
   auto frag_k = [&](const uint8_t *t, int row, int ks) MOE_INLINE {
-    if constexpr (TK == 64)
-      return *reinterpret_cast<const s16x8 *>(t + (row + fr) * 128 +
-                                              (((ks * 4 + fq) ^ (fr & 7)) * 16));
-    else
-      return *reinterpret_cast<const s16x8 *>(
-          t + (row + fr) * 64 - (fr & 1) * 64 + ((((fr & 1) * 4 + fq) ^ ((fr >> 1) & 7)) * 16));
+    return *reinterpret_cast<const s16x8 *>(t + (row + fr) * 128 +
+                                            (((ks * 4 + fq) ^ (fr & 7)) * 16));
   };
   auto frag_tr = [&](const uint8_t *t, uint32_t lane_off, int f, int ks, auto width) MOE_INLINE {
     constexpr int R = decltype(width)::value;
@@ -438,17 +420,6 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
     wait_vmcnt_imm<C::LOADS_MIN *(NS - 2)>();
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   };
-  // A stage's k-steps; the last one reads the next stage's first fragments and
-  // issues the stage NS ahead. After the last stage both go on with zeros,
-  // so that the loop has no branches.
-  auto stage = [&](int s, int set) MOE_INLINE {
-    if constexpr (C::KS == 2) step(0, s, 1, std::false_type(), 0);
-    wait_stage();
-    settle(set);
-    settle_entries();
-    step(set, s + 1, 0, std::true_type(), s + NS);
-  };
-
   if (nk > 0) {
     start();
     // all buffers are free: NS stages at once, their entries before them
@@ -478,15 +449,16 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
     asm volatile("s_barrier" ::: "memory");
 #pragma unroll
     for (int f = 0; f < C::FM + C::FN; ++f) read_frag(0, 0, 0, f);
-    if constexpr (C::KS == 2) {
+    // The second k-step of a stage reads the next stage's first fragments and
+    // issues the stage NS ahead. After the last stage both go on with zeros,
+    // so that the loop has no branches.
 #pragma unroll 1
-      for (int s = 0; s < nk; ++s) stage(s, 1);
-    } else {  // the register sets alternate by stage
-#pragma unroll 1
-      for (int s = 0; s < nk; s += 2) {
-        stage(s, 0);
-        stage(s + 1, 1);
-      }
+    for (int s = 0; s < nk; ++s) {
+      step(0, s, 1, std::false_type(), 0);
+      wait_stage();
+      settle(1);
+      settle_entries();
+      step(1, s + 1, 0, std::true_type(), s + NS);
     }
   }
 
@@ -494,9 +466,8 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
   // tile. Each wave turns 16 rows at a time through LDS of its own (fp32, 16-byte
   // chunk c of row r at c ^ r) so that a lane gets 8 consecutive columns of
   // a row: 16-byte loads and stores that fill whole lines, and the epilogue's
-  // column vectors stay the same for all rows.
-  wait_vmcnt_imm<0>();  // the zeros still on their way to LDS
-  __syncthreads();
+  // column vectors stay the same for all rows. What it reads for its rows is
+  // loaded before the first of them: one latency, not one for each run of rows.
   constexpr int OUT = MODE == GATED ? C::WN / 2 : C::WN;  // columns of a wave
   constexpr int CH = OUT / 4, LPR = OUT / 8;               // chunks, lanes in a row
   constexpr int PASSES = LPR > 4 ? LPR / 4 : 1, ROWS = 16 / PASSES;
@@ -525,9 +496,28 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
   auto row_of = [&](int i, int p) MOE_INLINE {
     return (int64_t)m0 + wm + 16 * i + p * ROWS + tr;
   };
-  auto is_real = [&](int64_t m) MOE_INLINE {
-    return !grouped || MODE == WGRAD || g.r.m_indices[m] == e;
-  };
+  uint32_t real = 0xffffffffu;  // a bit a run: the row holds an entry
+  if (MODE != WGRAD && grouped) {
+    real = 0;
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p)
+        if (row_of(i, p) < g.M && g.r.m_indices[row_of(i, p)] == e) real |= 1u << (i * PASSES + p);
+  }
+  auto is_real = [&](int i, int p) MOE_INLINE { return (real >> (i * PASSES + p) & 1) != 0; };
+  static_assert(C::FM * PASSES <= 32, "a bit a run");
+  s16x8 residual[MODE == LINEAR ? C::FM * PASSES : 1];
+  if (MODE == LINEAR && g.res) {
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p)
+        if (cols && row_of(i, p) < g.M)
+          residual[i * PASSES + p] = load8_raw(g.res + row_of(i, p) * g.ldr, n, g.N);
+  }
+  wait_vmcnt_imm<0>();  // with them the zeros still on their way to LDS
+  __syncthreads();
   const f32x8 zero8 = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   uint16_t *out = MODE == WGRAD ? (seg0 ? g.c1 + e * g.c_stride1 : g.c0 + e * g.c_stride0) : g.c0;
   const int64_t ldc = MODE == WGRAD && seg0 ? g.ldc1 : g.ldc0;
@@ -544,7 +534,7 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
         const f32x8 v = turn_out(p);
         const int64_t m = row_of(i, p);
         if (cols && m < g.M)
-          store8<D>(to + m * ld, col, width, is_real(m) ? v : zero8);
+          store8<D>(to + m * ld, col, width, is_real(i, p) ? v : zero8);
       }
     };
 #pragma unroll
@@ -574,22 +564,21 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
         f32x8 z = turn_out(p);
         const int64_t m = row_of(i, p);
         if (!cols || m >= g.M) continue;
-        const bool real = is_real(m);
         if constexpr (MODE == LINEAR) {
 #pragma unroll
           for (int v = 0; v < 8; ++v) z[v] += bias[v];
-          if (g.pre) store8<D>(g.pre + m * g.ldp, n, g.N, real ? z : zero8);
+          if (g.pre) store8<D>(g.pre + m * g.ldp, n, g.N, is_real(i, p) ? z : zero8);
           if (g.act != MOE_ACT_NONE) {
 #pragma unroll
             for (int v = 0; v < 8; ++v) z[v] = act_value(z[v], g.act);
           }
-          if (g.res && real) {
-            const f32x8 r = load8<D>(g.res + m * g.ldr, n, g.N);
+          if (g.res) {
+            const f32x8 r = unpack8<D>(residual[i * PASSES + p]);
 #pragma unroll
             for (int v = 0; v < 8; ++v) z[v] += r[v];
           }
         }
-        store8<D>(out + m * ldc, n, g.N, real ? z : zero8);
+        store8<D>(out + m * ldc, n, g.N, is_real(i, p) ? z : zero8);
       }
     }
   }

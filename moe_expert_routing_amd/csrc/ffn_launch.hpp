@@ -7,13 +7,13 @@
 
 namespace moe_ffn {
 
-//           BM   BN   WM  WN TK NS blocks/CU
-typedef Tile<256, 256, 128, 64, 64, 2, 1> Tile256;
-typedef Tile<128, 256, 64, 64, 64, 3, 1> Tile128w;
-typedef Tile<128, 128, 64, 32, 64, 4, 1> Tile128;
-typedef Tile<64, 64, 32, 32, 64, 4, 2> Tile64;
-typedef Tile<32, 64, 16, 32, 64, 4, 2> Tile32;
-typedef Tile<16, 128, 16, 32, 64, 4, 2> Tile16;
+//           BM   BN   WM  WN NS blocks/CU
+typedef Tile<256, 256, 128, 64, 2, 1> Tile256;
+typedef Tile<128, 256, 64, 64, 3, 1> Tile128w;
+typedef Tile<128, 128, 64, 32, 4, 1> Tile128;
+typedef Tile<64, 64, 32, 32, 4, 2> Tile64;
+typedef Tile<32, 64, 16, 32, 4, 2> Tile32;
+typedef Tile<16, 128, 16, 32, 4, 2> Tile16;
 
 template <class D, int MODE, class C>
 static int launch(GemmArgs g, hipStream_t st) {
