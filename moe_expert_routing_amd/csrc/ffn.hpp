@@ -6,7 +6,7 @@
 namespace moe_ffn {
 
 // Tile shapes of the products, named by their rows of M.
-enum TileKind { TILE_16, TILE_32, TILE_64, TILE_128, TILE_128W, TILE_256 };
+enum TileKind { TILE_16, TILE_32, TILE_64, TILE_64W, TILE_128, TILE_128W, TILE_256 };
 
 // Launches a product of the given mode (Mode); compiled for each element type.
 int launch_gemm_bf16(int mode, int kind, const GemmArgs &g, hipStream_t st);

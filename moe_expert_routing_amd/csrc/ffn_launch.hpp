@@ -11,6 +11,7 @@ namespace moe_ffn {
 typedef Tile<256, 256, 128, 64, 2, 1> Tile256;
 typedef Tile<128, 256, 64, 64, 3, 1> Tile128w;
 typedef Tile<128, 128, 64, 32, 4, 1> Tile128;
+typedef Tile<64, 256, 32, 64, 2, 2> Tile64w;
 typedef Tile<64, 64, 32, 32, 4, 2> Tile64;
 typedef Tile<32, 64, 16, 32, 4, 2> Tile32;
 typedef Tile<16, 128, 16, 32, 4, 2> Tile16;
@@ -76,8 +77,10 @@ static int launch_kind(int kind, const GemmArgs &g, hipStream_t st) {
     case TILE_64: return launch<D, MODE, Tile64>(g, st);
     case TILE_32: return launch<D, MODE, Tile32>(g, st);
   }
-  if constexpr (MODE != WGRAD)
+  if constexpr (MODE != WGRAD) {
     if (kind == TILE_128W) return launch<D, MODE, Tile128w>(g, st);
+    if (kind == TILE_64W) return launch<D, MODE, Tile64w>(g, st);
+  }
   if constexpr (MODE == DGRAD) {
     if (kind == TILE_16) return launch<D, MODE, Tile16>(g, st);
   } else if constexpr (MODE != WGRAD) {
