@@ -87,6 +87,33 @@ def local_layout(T, tile, *, e=128, top_k=8, off=0, cnt=0, seed=0, scale=1.0):
     return lay, (cnt if cnt and lay["num_experts_out"] != e else e)
 
 
+def hand_layout(ids, n_ids, tile, rows=None):
+    """The grouped layout of ids [T, K] (int64, 0 .. n_ids-1, one entry each), with
+    uniform weights; rows beyond the entries are padding."""
+    dev = "cuda"
+    T, k = ids.shape
+    flat = ids.reshape(-1).to(dev)
+    perm = torch.argsort(flat, stable=True)
+    inv = torch.empty_like(perm)
+    inv[perm] = torch.arange(T * k, device=dev)
+    counts = torch.bincount(flat, minlength=n_ids)
+    zero = torch.zeros(1, dtype=torch.long, device=dev)
+    offsets = torch.cat([zero, counts.cumsum(0)])
+    padded = torch.cat([zero, ((counts + tile - 1) // tile * tile).cumsum(0)])
+    rows = int(padded[-1]) if rows is None else rows
+    row = inv - offsets[flat] + padded[flat]
+    m = torch.full((rows,), -1, dtype=torch.int32, device=dev)
+    entry = torch.full((rows,), -1, dtype=torch.int32, device=dev)
+    here = row < rows
+    m[row[here]] = flat[here].int()
+    entry[row[here]] = torch.nonzero(here).reshape(-1).int()
+    i = torch.int32
+    return dict(counts=counts.to(i), offsets=offsets.to(i), padded_offsets=padded.to(i),
+                m_indices=m, row_entry=entry, inv_perm=inv.to(i),
+                packed=(flat.view(T, k) << 16).to(i),
+                topk_weights=torch.full((T, k), 1.0 / k, device=dev))
+
+
 def normal(seed, *shape, dt, scale=1.0):
     g = torch.Generator(device="cuda")
     g.manual_seed(seed)

@@ -8,7 +8,7 @@ import torch
 
 import moe_expert_routing_amd as M
 from ffn_util import (F32, TINY, act, assert_close, gated_grads, gated_oracle, groups,
-                      half_step, linear_grads, linear_oracle, local_layout, normal)
+                      half_step, hand_layout, linear_grads, linear_oracle, local_layout, normal)
 
 pytestmark = [
     pytest.mark.gpu,
@@ -405,3 +405,151 @@ def test_gradients_against_differences():
         # like random signs in the mean: 6 half steps of the gradient's norm
         scale = float(grad[key].double().norm()) * float(dirn.norm()) / dirn.numel() ** 0.5
         assert abs(num - ana) <= 6 * half_step(dt) * scale * 10 + 1e-6 * abs(num), (key, num, ana)
+
+
+def check_expert_gated(lay, n, k, x, F, tile, dt, name="silu", backward=True):
+    H, rows = x.shape[1], lay["m_indices"].numel()
+    wg, wu = normal(2, n, F, H, dt=dt, scale=H ** -0.5), normal(3, n, F, H, dt=dt, scale=H ** -0.5)
+    kw = dict(tile_m=tile, top_k=k, activation=name)
+    r = M.expert_gated_ffn(x, wg, wu, lay, save_pre=True, **kw)
+    pre, dh = normal(4, rows, 2 * F, dt=dt), normal(5, rows, F, dt=dt)
+    b = M.expert_gated_ffn_backward(dh, pre, x, wg, wu, lay, **kw) if backward else None
+    for e, at, tok in groups(lay, n, rows, k):
+        at, tok = at.cuda(), tok.cuda()
+        h, bh, ref, bp = gated_oracle(x[tok], wg[e], wu[e], name, dt)
+        assert_close(r["h"][at], h, bh, f"h of {e}")
+        assert_close(r["pre"][at], ref, bp, f"pre of {e}")
+        if b is not None:
+            for key, (ref, bd) in gated_grads(dh[at], pre[at], x[tok], wg[e], wu[e], name, dt).items():
+                assert_close(b[key][at] if key == "dx" else b[key][e], ref, bd, f"{key} of {e}")
+
+
+@pytest.mark.parametrize("k", [1, 3, 6])
+def test_entries_per_token_need_not_be_a_power_of_two(k):
+    T, n = 90, 7
+    g = torch.Generator().manual_seed(k)
+    ids = torch.stack([torch.randperm(n, generator=g)[:k] for _ in range(T)])
+    lay = hand_layout(ids, n, 32)
+    check_expert_gated(lay, n, k, normal(1, T, 136, dt=BF), 72, 32, BF)
+
+
+def test_many_rows_an_expert():
+    """Experts with thousands of rows, one with a single row and one with none."""
+    T, n = 5200, 4
+    ids = torch.randint(0, 2, (T, 1), generator=torch.Generator().manual_seed(1))
+    ids[77] = 3
+    lay = hand_layout(ids, n, 256, rows=9216)
+    check_expert_gated(lay, n, 1, normal(1, T, 264, dt=FP), 136, 256, FP, "gelu")
+
+
+def test_one_expert_gets_everything():
+    lay = hand_layout(torch.full((300, 1), 5), 8, 64)
+    check_expert_gated(lay, 8, 1, normal(1, 300, 128, dt=BF), 256, 64, BF)
+
+
+def test_gathered_rows_beyond_32_bits():
+    """x of more than 4 GB: rows at its end are the ones that are gathered."""
+    T, H, F, n = 300_032, 7168, 64, 2
+    x = torch.zeros((T, H), dtype=BF, device="cuda")
+    far = T - 1 - torch.arange(40) * 3
+    x[far.cuda()] = normal(1, 40, H, dt=BF)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    m = torch.full((64,), -1, **i32)
+    entry = torch.full((64,), -1, **i32)
+    m[:25], m[32:47] = 0, 1
+    entry[:25], entry[32:47] = far[:25].int().cuda(), far[25:].int().cuda()
+    lay = dict(m_indices=m, row_entry=entry, counts=torch.tensor([25, 15], **i32),
+               padded_offsets=torch.tensor([0, 32, 64], **i32))
+    check_expert_gated(lay, n, 1, x, F, 32, BF)
+
+
+def test_outputs_beyond_32_bits():
+    """Outputs of more than 4 GB, by the last rows."""
+    T, I, O = 300_032, 8, 8192
+    x, w = normal(1, T, I, dt=BF), normal(2, O, I, dt=BF)
+    res = torch.zeros((1, O), dtype=BF, device="cuda").expand(T, O)
+    with pytest.raises(M.MoeRouteError):
+        M.linear(x, w, residual=res)  # rows that overlap
+    y = M.linear(x, w)["y"]
+    ref, b, _, _ = linear_oracle(x[-300:], w, None, "none", None, BF)
+    assert_close(y[-300:], ref, b, "y")
+    lay = hand_layout(torch.zeros((T, 1), dtype=torch.long), 1, 16)
+    out = M.combine(y, lay, num_experts=1)
+    assert torch.equal(out[-300:], y[-300:])
+    dy = M.combine_backward(out, y, lay, num_experts=1)
+    assert torch.equal(dy["dy"][-300:], y[-300:])
+    d = y[-300:].double()
+    assert_close(dy["dweights"][-300:, 0], (d * d).sum(1), (O + 8) * F32 * (d * d).sum(1), "dw")
+
+
+@pytest.mark.parametrize("T,I,O", [(40, 4480, 384), (64, 7168, 256), (100, 512, 4096), (1000, 2560, 384),
+                                   (3000, 1024, 1024), (2100, 2048, 4096)])
+def test_linear_tiles(T, I, O):
+    """Shapes that lie on each side of the tile choice, forward and backward."""
+    x, w = normal(1, T, I, dt=BF), normal(2, O, I, dt=BF, scale=I ** -0.5)
+    dy, pre = normal(3, T, O, dt=BF), normal(4, T, O, dt=BF)
+    y, by, z, bz = linear_oracle(x, w, None, "silu", None, BF)
+    r = M.linear(x, w, activation="silu", save_pre=True)
+    assert_close(r["y"], y, by, "y")
+    assert_close(r["pre"], z, bz, "pre")
+    r = M.linear_backward(dy, x, w, pre=pre, activation="silu", bias_grad=True)
+    for k, (ref, b) in linear_grads(dy, pre, x, w, "silu", BF).items():
+        assert_close(r[k], ref, b, k)
+
+
+def test_two_streams_at_once():
+    """Calls on two streams with nothing between them give what each gives alone."""
+    xs = [normal(i, 700, 512, dt=BF) for i in range(2)]
+    ws = [normal(5 + i, 1024, 512, dt=BF) for i in range(2)]
+    dys = [normal(9 + i, 700, 1024, dt=BF) for i in range(2)]
+    pre = normal(20, 700, 1024, dt=BF)
+    want = [M.linear_backward(dys[i], xs[i], ws[i], pre=pre, activation="gelu", bias_grad=True)
+            for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(M.linear_backward(dys[i], xs[i], ws[i], pre=pre, activation="gelu",
+                                                bias_grad=True))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r in got[i]:
+            assert all(torch.equal(r[k], want[i][k]) for k in want[i])
+
+
+def test_refusals_on_the_gpu():
+    x, w = normal(1, 8, 64, dt=BF), normal(2, 32, 64, dt=BF)
+    bad = [
+        lambda: M.gated_ffn(x, w, w.to(FP)),                       # another type
+        lambda: M.gated_ffn(x.float(), w.float(), w.float()),      # no such type
+        lambda: M.gated_ffn(x, w, w[:, :32]),                      # another shape
+        lambda: M.gated_ffn(x.t(), w, w),                          # columns not contiguous
+        lambda: M.gated_ffn(x, w, w, activation="tanh"),
+        lambda: M.gated_ffn(x, w, w, out={"h": x}),                # output of another shape
+        lambda: M.linear(x, w.unsqueeze(0)),
+        lambda: M.linear(x, w, bias=x[0]),
+        lambda: M.linear_backward(normal(3, 8, 32, dt=BF), x, w, activation="silu"),  # no pre
+        lambda: M.linear(x, w, residual=normal(4, 9, 32, dt=BF)),
+        lambda: M.linear(x, w.cpu()),
+    ]
+    lay, n = local_layout(20, 16, top_k=4, off=0, cnt=16)
+    rows = lay["m_indices"].numel()
+    we = normal(5, n, 32, 64, dt=BF)
+    xt = normal(6, 20, 64, dt=BF)
+    bad += [
+        lambda: M.expert_gated_ffn(xt, we, we, lay, tile_m=24, top_k=4),   # no multiple of 16
+        lambda: M.expert_gated_ffn(xt, we, we, lay, tile_m=16, top_k=0),
+        lambda: M.expert_gated_ffn(xt, we[0], we[0], lay, tile_m=16, top_k=4),
+        lambda: M.expert_linear(xt, we, lay, tile_m=16),                   # rows, not tokens
+        lambda: M.expert_gated_ffn(xt, we, we, {**lay, "m_indices": lay["m_indices"].long()},
+                                   tile_m=16, top_k=4),
+        lambda: M.combine(normal(7, rows, 64, dt=BF), lay, num_experts=1000),
+        lambda: M.combine(normal(7, rows, 64, dt=BF), lay, num_experts=n, residual=xt[:, :32]),
+        lambda: M.combine_backward(xt[:10], None, lay, num_experts=n, weighted=False),
+        lambda: M.combine_backward(xt, None, lay, num_experts=n),          # dweights need y
+    ]
+    for f in bad:
+        with pytest.raises(M.MoeRouteError):
+            f()
