@@ -57,14 +57,24 @@ static Operand operand(const moe_matrix &m, int64_t rows, int cols, int mats, Ar
   return {dst, c8, rows * c8};
 }
 
-// Tile of `mats` products of M x N over K: the one with the least estimated
-// time, its rounds over the 256 compute units times (64-k stages times a stage's
+// How a product runs: its tile, and the ranges that its k is split into.
+struct Plan {
+  int kind, splits;
+};
+// Plan of `mats` products of M x N over K: the one with the least estimated time,
+// its rounds over the 256 compute units times (64-k stages times a stage's
 // time, plus a fixed part). The stage times, in microseconds, are measured
 // with one tile on a compute unit, and with two where two fit. What
 // the choice does, in us, for 256 / 128 / 64 / 32-row tiles:
 //   1024 x 1024 x 2816     60 / 22 / 14 / 14    8192 x 7168 x 2048  265 / 295 / - / -
 //   2048 x 2048 x 2048     49 / 21 / 31 / -     64 x 7168 x 2048    - / - / 11 / 8.7
-static int dense_tile(int64_t mats, int64_t M, int64_t N, int64_t K) {
+// Where few tiles have a long way through k (may_split), up to 16 ranges of at
+// least 6 stages each are summed apart, which costs the partial sums' way through
+// memory, a workspace and a launch that joins them: 12 us fixed, so that calls
+// bound by the host's side stay as they are. Measured, one range / split: 64 x
+// 7168 -> 2048 gated 30 / 19 us, 64 x 7168 -> 1024 18 / 15, dW of 16384 x 1024 ->
+// 512 53 / 36; with 9 us instead of 12, 64 x 4096 -> 1024 gated went 12 / 16.
+static Plan dense_plan(int64_t mats, int64_t M, int64_t N, int64_t K, bool may_split) {
   static const struct {
     int kind, bm, bn, blocks;
     float one, full, fixed;
@@ -72,29 +82,66 @@ static int dense_tile(int64_t mats, int64_t M, int64_t N, int64_t K) {
                {TILE_128, 128, 128, 1, 0.46f, 0.46f, 4.f},
                {TILE_64, 64, 64, 2, 0.30f, 0.48f, 2.5f},
                {TILE_32, 32, 64, 2, 0.26f, 0.36f, 2.5f}};
-  const float stages = (float)((K + 63) / 64);
-  int best = TILE_256;
+  const int64_t stages = (K + 63) / 64;
+  Plan best = {TILE_256, 1};
   float least = 0.f;
-  for (const auto &t : tiles) {
-    const int64_t n = mats * ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
-    const int64_t rounds = (n + 256 * t.blocks - 1) / (256 * t.blocks);
-    const float time = (float)rounds * (stages * (n <= 256 ? t.one : t.full) + t.fixed);
-    if (least == 0.f || time < least) least = time, best = t.kind;
+  for (int splits = 1; splits == 1 || (may_split && splits <= 16 && stages / splits >= 6);
+       splits *= 2) {
+    const float join =
+        splits == 1 ? 0.f : 12.f + (float)(splits * mats * M * N) * 8.f / 4e6f;  // at 4 TB/s
+    for (const auto &t : tiles) {
+      const int64_t n = splits * mats * ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
+      const int64_t rounds = (n + 256 * t.blocks - 1) / (256 * t.blocks);
+      const float stage = n <= 256 ? t.one : t.full;
+      const float time =
+          (float)rounds * ((float)((stages + splits - 1) / splits) * stage + t.fixed) + join;
+      if (least == 0.f || time < least) least = time, best = {t.kind, splits};
+    }
   }
   return best;
 }
-// Tile of the products whose M is the call's rows. Over experts a tile
+// Plan of the products whose M is the call's rows. Over experts a tile
 // holds rows of one expert, so it divides the layout's alignment; 256 rows only
 // where experts have that many by far, as shorter tiles that hold padding
 // alone are skipped. (112 experts with about 146 rows padded to 128, 2048 ->
 // 1024 gated: 128 x 256 tiles 252 us, 128 x 128 301, 64 x 256 306, 64 x 128 337.)
-static int row_tile(const moe_expert_rows &r, int64_t M, int N, int64_t K) {
+static Plan row_plan(const moe_expert_rows &r, int64_t M, int64_t N, int64_t K) {
   if (r.num_experts > 0) {
-    if (r.tile_m % 256 == 0 && M / r.num_experts >= 2048) return TILE_256;
-    return r.tile_m % 128 == 0 ? TILE_128W
-           : r.tile_m % 64 == 0 ? TILE_64W : r.tile_m % 32 == 0 ? TILE_32 : TILE_16;
+    if (r.tile_m % 256 == 0 && M / r.num_experts >= 2048) return {TILE_256, 1};
+    return {r.tile_m % 128 == 0  ? TILE_128W
+            : r.tile_m % 64 == 0 ? TILE_64W
+            : r.tile_m % 32 == 0 ? TILE_32
+                                 : TILE_16,
+            1};
   }
-  return M <= 16 ? TILE_16 : dense_tile(1, M, N, K);
+  if (M <= 16) return {TILE_16, 1};
+  return dense_plan(1, M, N, K, true);
+}
+static Plan weight_plan(const moe_expert_rows &r, int64_t segs, int64_t M, int64_t N,
+                        int64_t rows) {
+  if (r.num_experts > 0) return dense_plan(segs * r.num_experts, M, N, rows / r.num_experts, false);
+  return dense_plan(segs, M, N, rows, true);
+}
+
+// Runs a product by its plan, with the partial sums of a split one in the
+// workspace. `width`: the partial sums of a row of C.
+static int run_product(int dtype, int mode, const Plan &plan, GemmArgs &g, int width, Arena &ws,
+                       hipStream_t st) {
+  const int64_t stages = (g.K + 63) / 64;
+  if (plan.splits > 1) {
+    g.k_split = (int)((stages + plan.splits - 1) / plan.splits) * 64;
+    g.splits = (g.K + g.k_split - 1) / g.k_split;  // none of them empty
+    const int segs = mode == WGRAD ? g.segs : 1;
+    g.partial = reinterpret_cast<float *>(
+        ws.take((size_t)g.splits * segs * g.M * width * sizeof(float)));
+    if (ws.dry) return MOE_OK;
+    const int got = launch_gemm(dtype, mode, plan.kind, g, st);
+    if (got != MOE_OK) return got;
+    const auto kernel = dtype == MOE_BF16 ? join_kernel<Bf16> : join_kernel<F16>;
+    kernel<<<row_grid(g.M, round8(g.N), segs), dim3(COL_THREADS, ROW_THREADS), 0, st>>>(g, mode);
+    return hip_status();
+  }
+  return ws.dry ? MOE_OK : launch_gemm(dtype, mode, plan.kind, g, st);
 }
 
 static int check_common(int dtype, int act, int64_t tokens, int w0, int w1,
@@ -223,14 +270,14 @@ static int run_gated(const moe_gated_ffn_args *a, Arena &ws, hipStream_t st) {
   }
   const Operand wg = operand(a->w_gate, F, H, mats, ws, st, &status);
   const Operand wu = operand(a->w_up, F, H, mats, ws, st, &status);
-  if (ws.dry || status != MOE_OK) return status;
+  if (status != MOE_OK) return status;
   g.a = x.p, g.lda = x.ld;
   set_b0(g, wg);
   set_b1(g, wu);
   set_c0(g, a->h);
   g.pre = (uint16_t *)a->pre.p, g.ldp = a->pre.ld;
   g.M = (int)rows, g.N = F, g.K = H, g.act = a->activation;
-  return launch_gemm(a->dtype, GATED, row_tile(a->rows, rows, 2 * F, H), g, st);
+  return run_product(a->dtype, GATED, row_plan(a->rows, rows, 2 * F, H), g, 2 * F, ws, st);
 }
 
 static int run_gated_backward(const moe_gated_ffn_args *a, Arena &ws, hipStream_t st) {
@@ -251,8 +298,8 @@ static int run_gated_backward(const moe_gated_ffn_args *a, Arena &ws, hipStream_
     wg = operand(a->w_gate, F, H, mats, ws, st, &status, copy);
     wu = operand(a->w_up, F, H, mats, ws, st, &status, copy);
   }
-  if (ws.dry || status != MOE_OK) return status;
-  if (rows > 0) {
+  if (status != MOE_OK) return status;
+  if (rows > 0 && !ws.dry) {
     const dim3 grid = row_grid(rows, Fa, 1), block(COL_THREADS, ROW_THREADS);
     const auto kernel = a->dtype == MOE_BF16 ? gated_dz_kernel<Bf16> : gated_dz_kernel<F16>;
     kernel<<<grid, block, 0, st>>>((const uint16_t *)a->dh.p, a->dh.ld,
@@ -269,7 +316,7 @@ static int run_gated_backward(const moe_gated_ffn_args *a, Arena &ws, hipStream_
     set_b1(d, wu);
     set_c0(d, a->dx);
     d.M = (int)rows, d.N = H, d.K = F;
-    MOE_TRY(launch_gemm(a->dtype, DGRAD, row_tile(a->rows, rows, H, 2 * F), d, st));
+    MOE_TRY(run_product(a->dtype, DGRAD, row_plan(a->rows, rows, H, 2 * F), d, H, ws, st));
   }
   if (a->dw_gate.p) {
     set_b0(g, x);
@@ -278,7 +325,7 @@ static int run_gated_backward(const moe_gated_ffn_args *a, Arena &ws, hipStream_
     set_c0(g, a->dw_gate);
     set_c1(g, a->dw_up);
     g.M = F, g.N = H, g.K = (int)rows;
-    MOE_TRY(launch_gemm(a->dtype, WGRAD, dense_tile(2 * mats, F, H, rows / mats), g, st));
+    MOE_TRY(run_product(a->dtype, WGRAD, weight_plan(a->rows, 2, F, H, rows), g, H, ws, st));
   }
   return MOE_OK;
 }
@@ -311,7 +358,7 @@ static int run_linear(const moe_linear_args *a, Arena &ws, hipStream_t st) {
   if (rows == 0) return MOE_OK;
   const Operand x = operand(a->x, rows, I, 1, ws, st, &status);
   const Operand w = operand(a->w, O, I, mats, ws, st, &status);
-  if (ws.dry || status != MOE_OK) return status;
+  if (status != MOE_OK) return status;
   GemmArgs g = gemm_args(a->rows, rows, false);
   g.a = x.p, g.lda = x.ld, g.a_rows = rows;
   set_b0(g, w);
@@ -320,7 +367,7 @@ static int run_linear(const moe_linear_args *a, Arena &ws, hipStream_t st) {
   g.bias = (const uint16_t *)a->bias.p, g.bias_stride = a->bias.stride;
   g.res = (const uint16_t *)a->residual.p, g.ldr = a->residual.ld;
   g.M = (int)rows, g.N = O, g.K = I, g.act = a->activation;
-  return launch_gemm(a->dtype, LINEAR, row_tile(a->rows, rows, O, I), g, st);
+  return run_product(a->dtype, LINEAR, row_plan(a->rows, rows, O, I), g, O, ws, st);
 }
 
 // Row ranges of the bias gradient's partial sums: dense, one for every 256
@@ -368,20 +415,20 @@ static int run_linear_backward(const moe_linear_args *a, Arena &ws, hipStream_t 
   Operand x = {}, w = {};
   if (a->dw.p) x = operand(a->x, rows, I, 1, ws, st, &status);
   if (a->dx.p && rows > 0) w = operand(a->w, O, I, mats, ws, st, &status);
-  if (ws.dry || status != MOE_OK) return status;
+  if (status != MOE_OK) return status;
   g.a = dz.p, g.lda = dz.ld, g.a_rows = rows;
   if (a->dx.p && rows > 0) {
     GemmArgs d = g;
     set_b0(d, w);
     set_c0(d, a->dx);
     d.M = (int)rows, d.N = I, d.K = O;
-    MOE_TRY(launch_gemm(a->dtype, DGRAD, row_tile(a->rows, rows, I, O), d, st));
+    MOE_TRY(run_product(a->dtype, DGRAD, row_plan(a->rows, rows, I, O), d, I, ws, st));
   }
   if (a->dw.p) {
     set_b0(g, x);
     set_c0(g, a->dw);
     g.M = O, g.N = I, g.K = (int)rows;
-    MOE_TRY(launch_gemm(a->dtype, WGRAD, dense_tile(mats, O, I, rows / mats), g, st));
+    MOE_TRY(run_product(a->dtype, WGRAD, weight_plan(a->rows, 1, O, I, rows), g, I, ws, st));
   }
   return MOE_OK;
 }

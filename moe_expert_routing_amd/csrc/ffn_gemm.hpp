@@ -148,12 +148,14 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
   const bool grouped = g.r.num_experts > 0;
 
   int mt, nt, e = 0, seg0 = 0;
-  int64_t k_row0 = 0;  // WGRAD: first row of the expert
+  int64_t k_row0 = 0;  // WGRAD: first row of the expert, or of the k range
+  int split = 0, k0 = 0;  // the others: first k of the range
   int K = g.K;
   if constexpr (MODE == WGRAD) {
     // one expert and projection after the other, all its tiles together
     const int per = g.m_tiles * g.n_tiles;
-    const int chunk = blockIdx.x / per;
+    const int chunk = blockIdx.x / per % (g.segs * max(1, g.r.num_experts));
+    split = blockIdx.x / per / (g.segs * max(1, g.r.num_experts));
     tile_at(tile_of_block(blockIdx.x % per, per, per), g.m_tiles, g.n_tiles, mt, nt);
     e = chunk / g.segs;
     seg0 = chunk % g.segs;
@@ -168,7 +170,9 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
       const int64_t end = g.r.padded_offsets[g.r.num_experts];
       live = (int)min((int64_t)g.m_tiles, (max(end, (int64_t)0) + BM - 1) / BM);
     }
-    const int t = tile_of_block(blockIdx.x, gridDim.x, live * g.n_tiles);
+    const int per = g.m_tiles * g.n_tiles;  // split: all tiles of one k range together
+    split = blockIdx.x / per;
+    const int t = tile_of_block(blockIdx.x % per, per, live * g.n_tiles);
     if (t < live * g.n_tiles) {
       tile_at(t, live, g.n_tiles, mt, nt);
     } else {
@@ -198,6 +202,10 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
         return;
       }
     }
+  }
+  if (g.partial) {
+    if (MODE == WGRAD) k_row0 = split * (int64_t)g.k_split; else k0 = split * g.k_split;
+    K = min(g.k_split, K - split * g.k_split);
   }
   const uint16_t *b0 = g.b0, *b1 = g.b1;
   if (MODE != WGRAD) {
@@ -237,18 +245,18 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
     a_base = reinterpret_cast<const uint8_t *>(g.a + k_row0 * g.lda + seg0 * g.a_seg);
     a_step = TK * g.lda * 2;
   } else {
-    a_base = reinterpret_cast<const uint8_t *>(g.a + (GATHER ? 0 : m0 * g.lda));
+    a_base = reinterpret_cast<const uint8_t *>(g.a + (GATHER ? 0 : m0 * g.lda) + k0);
     a_step = TK * 2;
   }
   if constexpr (MODE == WGRAD) {
     b_base = reinterpret_cast<const uint8_t *>(b0 + (GATHER ? 0 : k_row0 * ldb));
     b_step = GATHER ? 0 : TK * ldb * 2;
   } else if constexpr (MODE == DGRAD) {
-    b_base = reinterpret_cast<const uint8_t *>(b0);
-    b_next = reinterpret_cast<const uint8_t *>(b1);
+    b_base = reinterpret_cast<const uint8_t *>(b0 + k0 * ldb);
+    b_next = reinterpret_cast<const uint8_t *>(b1 + k0 * ldb);
     b_step = TK * ldb * 2;
   } else {
-    b_base = reinterpret_cast<const uint8_t *>((up ? b1 : b0) + n0 * ldb);
+    b_base = reinterpret_cast<const uint8_t *>((up ? b1 : b0) + n0 * ldb + k0);
     b_step = TK * 2;
   }
   // a lane's row and 8-element chunk in a piece of an operand with contiguous
@@ -317,7 +325,8 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
     left -= TK;
     if (MODE == DGRAD) {
       const bool second = g.segs > 1 && s + 1 == seg_stages;
-      a_base = second ? reinterpret_cast<const uint8_t *>(g.a + m0 * g.lda + g.a_seg) : a_base;
+      a_base = second ? reinterpret_cast<const uint8_t *>(g.a + m0 * g.lda + k0 + g.a_seg)
+                      : a_base;
       b_base = second ? b_next : b_base;
       left = second ? K : left;
     }
@@ -508,7 +517,7 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
   auto is_real = [&](int i, int p) MOE_INLINE { return (real >> (i * PASSES + p) & 1) != 0; };
   static_assert(C::FM * PASSES <= 32, "a bit a run");
   s16x8 residual[MODE == LINEAR ? C::FM * PASSES : 1];
-  if (MODE == LINEAR && g.res) {
+  if (MODE == LINEAR && g.res && !g.partial) {
 #pragma unroll
     for (int i = 0; i < C::FM; ++i)
 #pragma unroll
@@ -521,6 +530,27 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
   const f32x8 zero8 = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   uint16_t *out = MODE == WGRAD ? (seg0 ? g.c1 + e * g.c_stride1 : g.c0 + e * g.c_stride0) : g.c0;
   const int64_t ldc = MODE == WGRAD && seg0 ? g.ldc1 : g.ldc0;
+  if (g.partial) {  // a range's sums as they are; join_kernel does the rest
+    const int width = MODE == GATED ? 2 * g.N : g.N;
+    float *part = g.partial + (split * (int64_t)(MODE == WGRAD ? g.segs : 1) + seg0) * g.M * width;
+    constexpr int SIDES = MODE == GATED ? 2 : 1;
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+      for (int side = 0; side < SIDES; ++side) {
+        turn_order();
+#pragma unroll
+        for (int j = 0; j < C::FN / SIDES; ++j) turn_in(j, acc[i][SIDES * j + side]);
+        turn_order();
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p) {
+          const f32x8 v = turn_out(p);
+          if (cols && row_of(i, p) < g.M)
+            store8_f32(part + row_of(i, p) * width + side * g.N, n, g.N, v);
+        }
+      }
+    return;
+  }
   if constexpr (MODE == GATED) {
     // what is turned: h, and with pre the two projections as well
     auto rows_out = [&](int i, auto value, uint16_t *to, int64_t ld, int width, int col)

@@ -23,6 +23,7 @@ static int launch(GemmArgs g, hipStream_t st) {
   g.n_tiles = (g.N + bn - 1) / bn;
   int64_t blocks = (int64_t)g.m_tiles * g.n_tiles;
   if (MODE == WGRAD) blocks *= (int64_t)(g.r.num_experts > 0 ? g.r.num_experts : 1) * g.segs;
+  if (g.partial) blocks *= g.splits;
   if (blocks == 0) return MOE_OK;
   if (blocks > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
   const dim3 grid((uint32_t)blocks), block(C::NTHREADS);

@@ -168,6 +168,59 @@ __global__ __launch_bounds__(256) void bias_sum_kernel(const float *__restrict__
                                             sum[3][threadIdx.x]);
 }
 
+// The partial sums of a product that was split over k, added in the order of
+// the ranges, and its epilogue. blockIdx.z: WGRAD's segment.
+template <class D>
+__global__ __launch_bounds__(COL_THREADS *ROW_THREADS) void join_kernel(const GemmArgs g, int mode) {
+  const int c = (blockIdx.x * COL_THREADS + threadIdx.x) * 8;
+  if (c >= g.N) return;
+  const int width = mode == GATED ? 2 * g.N : g.N, segs = mode == WGRAD ? g.segs : 1;
+  const int64_t range = (int64_t)segs * g.M * width;
+  uint16_t *out = mode == WGRAD && blockIdx.z ? g.c1 : g.c0;
+  const int64_t ldc = mode == WGRAD && blockIdx.z ? g.ldc1 : g.ldc0;
+  for (int64_t m = blockIdx.y * ROW_THREADS + threadIdx.y; m < g.M;
+       m += (int64_t)gridDim.y * ROW_THREADS) {
+    const float *p = g.partial + (blockIdx.z * (int64_t)g.M + m) * width;
+    f32x8 z = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, u = z;
+#pragma unroll 4
+    for (int s = 0; s < g.splits; ++s) {
+      const f32x8 a = load8_f32(p + s * range, c, g.N);
+#pragma unroll
+      for (int v = 0; v < 8; ++v) z[v] += a[v];
+      if (mode == GATED) {
+        const f32x8 b = load8_f32(p + s * range + g.N, c, g.N);
+#pragma unroll
+        for (int v = 0; v < 8; ++v) u[v] += b[v];
+      }
+    }
+    if (mode == GATED) {
+      if (g.pre) {
+        store8<D>(g.pre + m * g.ldp, c, g.N, z);
+        store8<D>(g.pre + m * g.ldp + g.N, c, g.N, u);
+      }
+#pragma unroll
+      for (int v = 0; v < 8; ++v) z[v] = act_value(z[v], g.act) * u[v];
+    } else if (mode == LINEAR) {
+      if (g.bias) {
+        const f32x8 b = load8<D>(g.bias, c, g.N);
+#pragma unroll
+        for (int v = 0; v < 8; ++v) z[v] += b[v];
+      }
+      if (g.pre) store8<D>(g.pre + m * g.ldp, c, g.N, z);
+      if (g.act != MOE_ACT_NONE) {
+#pragma unroll
+        for (int v = 0; v < 8; ++v) z[v] = act_value(z[v], g.act);
+      }
+      if (g.res) {
+        const f32x8 r = load8<D>(g.res + m * g.ldr, c, g.N);
+#pragma unroll
+        for (int v = 0; v < 8; ++v) z[v] += r[v];
+      }
+    }
+    store8<D>(out + m * ldc, c, g.N, z);
+  }
+}
+
 // ------------------------------------------------------------------ combine
 
 struct CombineArgs {

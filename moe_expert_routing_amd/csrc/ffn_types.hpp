@@ -130,6 +130,25 @@ __device__ __forceinline__ void store8(uint16_t *row, int c, int n, f32x8 v) {
   store8_raw(row, c, n, pack8<D>(v));
 }
 
+typedef f32x8 f32x8_any __attribute__((aligned(4)));
+__device__ __forceinline__ void store8_f32(float *row, int c, int n, f32x8 v) {
+  if (c + 8 <= n) {
+    *reinterpret_cast<f32x8_any *>(row + c) = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < n) row[c + i] = v[i];
+  }
+}
+__device__ __forceinline__ f32x8 load8_f32(const float *row, int c, int n) {
+  if (c + 8 <= n) return *reinterpret_cast<const f32x8_any *>(row + c);
+  f32x8 v = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c + i < n) v[i] = row[c + i];
+  return v;
+}
+
 // The expert of a row's tile and whether one row holds an entry of it.
 struct Rows {
   const int32_t *counts, *padded_offsets, *m_indices, *row_entry;
@@ -161,6 +180,10 @@ struct GemmArgs {
   int32_t segs;            // 1, or 2 for the two projections of a gated block
   int32_t act;
   int32_t m_tiles, n_tiles;
+  // dense only: K in `splits` ranges of k_split (a multiple of 64), each summed
+  // into its own partial [splits][WGRAD: segs][M][N, GATED: 2 N]; NULL: one range
+  int32_t splits, k_split;
+  float *partial;
   uint32_t top_k_magic, top_k_shift; // entry / top_k as a product; magic 0: top_k is 1
 };
 
