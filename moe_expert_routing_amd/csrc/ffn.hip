@@ -70,10 +70,10 @@ struct Plan {
 //   2048 x 2048 x 2048     49 / 21 / 31 / -     64 x 7168 x 2048    - / - / 11 / 8.7
 // Where few tiles have a long way through k (may_split), up to 16 ranges of at
 // least 6 stages each are summed apart, which costs the partial sums' way through
-// memory, a workspace and a launch that joins them: 12 us fixed, so that calls
+// memory, a workspace and a launch that joins them: 14 us fixed, so that calls
 // bound by the host's side stay as they are. Measured, one range / split: 64 x
 // 7168 -> 2048 gated 30 / 19 us, 64 x 7168 -> 1024 18 / 15, dW of 16384 x 1024 ->
-// 512 53 / 36; with 9 us instead of 12, 64 x 4096 -> 1024 gated went 12 / 16.
+// 512 53 / 36; with 12 us instead of 14, 64 x 4096 -> 1024 gated went 12 / 16.
 static Plan dense_plan(int64_t mats, int64_t M, int64_t N, int64_t K, bool may_split) {
   static const struct {
     int kind, bm, bn, blocks;
@@ -88,7 +88,7 @@ static Plan dense_plan(int64_t mats, int64_t M, int64_t N, int64_t K, bool may_s
   for (int splits = 1; splits == 1 || (may_split && splits <= 16 && stages / splits >= 6);
        splits *= 2) {
     const float join =
-        splits == 1 ? 0.f : 12.f + (float)(splits * mats * M * N) * 8.f / 4e6f;  // at 4 TB/s
+        splits == 1 ? 0.f : 14.f + (float)(splits * mats * M * N) * 8.f / 4e6f;  // at 4 TB/s
     for (const auto &t : tiles) {
       const int64_t n = splits * mats * ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
       const int64_t rounds = (n + 256 * t.blocks - 1) / (256 * t.blocks);

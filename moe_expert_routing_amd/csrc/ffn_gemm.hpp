@@ -570,9 +570,9 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
 #pragma unroll
     for (int i = 0; i < C::FM; ++i) {
       rows_out(i, [&](f32x4 gt, f32x4 up4) MOE_INLINE {
-        f32x4 h;
+        f32x4 h = act_value(gt, g.act);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) h[v] = act_value(gt[v], g.act) * up4[v];
+        for (int v = 0; v < 4; ++v) h[v] *= up4[v];
         return h;
       }, out, ldc, g.N, n);
       if (g.pre) {
@@ -598,10 +598,7 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
 #pragma unroll
           for (int v = 0; v < 8; ++v) z[v] += bias[v];
           if (g.pre) store8<D>(g.pre + m * g.ldp, n, g.N, is_real(i, p) ? z : zero8);
-          if (g.act != MOE_ACT_NONE) {
-#pragma unroll
-            for (int v = 0; v < 8; ++v) z[v] = act_value(z[v], g.act);
-          }
+          z = act_value(z, g.act);
           if (g.res) {
             const f32x8 r = unpack8<D>(residual[i * PASSES + p]);
 #pragma unroll

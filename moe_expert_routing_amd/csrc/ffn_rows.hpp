@@ -65,13 +65,12 @@ __global__ __launch_bounds__(COL_THREADS *ROW_THREADS) void gated_dz_kernel(
     const f32x8 d = load8<D>(dh + m * ld_dh, c, F);
     const f32x8 gt = load8<D>(pre + m * ld_pre, c, F);
     const f32x8 up = load8<D>(pre + m * ld_pre + F, c, F);
-    f32x8 dg, du;
+    f32x8 dg, du, v, s;
+    act_value_slope(gt, act, v, s);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float v, s;
-      act_value_slope(gt[i], act, v, s);
-      dg[i] = d[i] * up[i] * s;
-      du[i] = d[i] * v;
+      dg[i] = d[i] * up[i] * s[i];
+      du[i] = d[i] * v[i];
     }
     uint16_t *o = dz + m * (2 * (int64_t)Fa);
     *reinterpret_cast<s16x8 *>(o + c) = pack8<D>(dg);
@@ -91,13 +90,10 @@ __global__ __launch_bounds__(COL_THREADS *ROW_THREADS) void linear_dz_kernel(
        m += (int64_t)gridDim.y * ROW_THREADS) {
     if (!row_is_real(r, m)) continue;
     f32x8 d = load8<D>(dy + m * ld_dy, c, O);
-    const f32x8 z = load8<D>(pre + m * ld_pre, c, O);
+    f32x8 v, s;
+    act_value_slope(load8<D>(pre + m * ld_pre, c, O), act, v, s);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float v, s;
-      act_value_slope(z[i], act, v, s);
-      d[i] *= s;
-    }
+    for (int i = 0; i < 8; ++i) d[i] *= s[i];
     *reinterpret_cast<s16x8 *>(dz + m * (int64_t)Oa + c) = pack8<D>(d);
   }
 }
@@ -126,13 +122,10 @@ __global__ __launch_bounds__(8 * BIAS_ROWS) void bias_grad_kernel(
     for (int64_t m = first + lo + threadIdx.y; m < first + hi; m += BIAS_ROWS) {
       f32x8 d = load8<D>(dy + m * ld_dy, c, O);
       if (act != MOE_ACT_NONE) {
-        const f32x8 z = load8<D>(pre + m * ld_pre, c, O);
+        f32x8 v, s;
+        act_value_slope(load8<D>(pre + m * ld_pre, c, O), act, v, s);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float v, s;
-          act_value_slope(z[i], act, v, s);
-          d[i] *= s;
-        }
+        for (int i = 0; i < 8; ++i) d[i] *= s[i];
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) a[i] += d[i];
@@ -198,8 +191,9 @@ __global__ __launch_bounds__(COL_THREADS *ROW_THREADS) void join_kernel(const Ge
         store8<D>(g.pre + m * g.ldp, c, g.N, z);
         store8<D>(g.pre + m * g.ldp + g.N, c, g.N, u);
       }
+      z = act_value(z, g.act);
 #pragma unroll
-      for (int v = 0; v < 8; ++v) z[v] = act_value(z[v], g.act) * u[v];
+      for (int v = 0; v < 8; ++v) z[v] *= u[v];
     } else if (mode == LINEAR) {
       if (g.bias) {
         const f32x8 b = load8<D>(g.bias, c, g.N);
@@ -207,10 +201,7 @@ __global__ __launch_bounds__(COL_THREADS *ROW_THREADS) void join_kernel(const Ge
         for (int v = 0; v < 8; ++v) z[v] += b[v];
       }
       if (g.pre) store8<D>(g.pre + m * g.ldp, c, g.N, z);
-      if (g.act != MOE_ACT_NONE) {
-#pragma unroll
-        for (int v = 0; v < 8; ++v) z[v] = act_value(z[v], g.act);
-      }
+      z = act_value(z, g.act);
       if (g.res) {
         const f32x8 r = load8<D>(g.res + m * g.ldr, c, g.N);
 #pragma unroll

@@ -128,8 +128,9 @@ __global__ __launch_bounds__(64 * SKINNY_WAVES) void skinny_kernel(const GemmArg
         store8<D>(g.pre + m * g.ldp, n, g.N, z);
         store8<D>(g.pre + m * g.ldp + g.N, n, g.N, u);
       }
+      z = act_value(z, g.act);
 #pragma unroll
-      for (int v = 0; v < 8; ++v) z[v] = real ? act_value(z[v], g.act) * u[v] : 0.f;
+      for (int v = 0; v < 8; ++v) z[v] = real ? z[v] * u[v] : 0.f;
     } else {
       if (real && g.bias) {
         const f32x8 b = load8<D>(g.bias + e * g.bias_stride, n, g.N);
@@ -137,10 +138,7 @@ __global__ __launch_bounds__(64 * SKINNY_WAVES) void skinny_kernel(const GemmArg
         for (int v = 0; v < 8; ++v) z[v] += b[v];
       }
       if (g.pre) store8<D>(g.pre + m * g.ldp, n, g.N, z);
-      if (real && g.act != MOE_ACT_NONE) {
-#pragma unroll
-        for (int v = 0; v < 8; ++v) z[v] = act_value(z[v], g.act);
-      }
+      z = act_value(z, g.act);  // 0 stays 0
       if (real && g.res) {
         const f32x8 b = load8<D>(g.res + m * g.ldr, n, g.N);
 #pragma unroll

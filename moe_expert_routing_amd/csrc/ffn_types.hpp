@@ -81,23 +81,40 @@ __device__ __forceinline__ float phi_cdf(float z, float e) {
   const float tail = e * t * q;
   return z < 0.f ? tail : 1.f - tail;
 }
-__device__ __forceinline__ float act_value(float z, int act) {
-  if (act == MOE_ACT_SILU) return z * sigmoid_f(z);
-  if (act == MOE_ACT_GELU) return z * phi_cdf(z, __expf(-0.5f * z * z));
+// Whole vectors, so that the branch on the activation is taken once and their
+// elements' long chains of dependent operations run beside each other.
+template <class V>
+__device__ __forceinline__ V act_value(V z, int act) {
+  constexpr int N = sizeof(V) / sizeof(float);
+  if (act == MOE_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = z[i] * sigmoid_f(z[i]);
+  } else if (act == MOE_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = z[i] * phi_cdf(z[i], __expf(-0.5f * z[i] * z[i]));
+  }
   return z;
 }
-__device__ __forceinline__ void act_value_slope(float z, int act, float &value, float &slope) {
+template <class V>
+__device__ __forceinline__ void act_value_slope(V z, int act, V &value, V &slope) {
+  constexpr int N = sizeof(V) / sizeof(float);
   if (act == MOE_ACT_SILU) {
-    const float s = sigmoid_f(z);
-    value = z * s;
-    slope = s * (1.f + z * (1.f - s));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float s = sigmoid_f(z[i]);
+      value[i] = z[i] * s;
+      slope[i] = s * (1.f + z[i] * (1.f - s));
+    }
   } else if (act == MOE_ACT_GELU) {
-    const float e = __expf(-0.5f * z * z), c = phi_cdf(z, e);
-    value = z * c;
-    slope = c + z * 0.39894228040143268f * e;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float e = __expf(-0.5f * z[i] * z[i]), c = phi_cdf(z[i], e);
+      value[i] = z[i] * c;
+      slope[i] = c + z[i] * 0.39894228040143268f * e;
+    }
   } else {
-    value = z;
-    slope = 1.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) value[i] = z[i], slope[i] = 1.f;
   }
 }
 
