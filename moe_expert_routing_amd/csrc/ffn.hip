@@ -100,22 +100,33 @@ static Plan dense_plan(int64_t mats, int64_t M, int64_t N, int64_t K, bool may_s
   }
   return best;
 }
-// Plan of the products whose M is the call's rows. Over experts a tile
-// holds rows of one expert, so it divides the layout's alignment; 256 rows only
-// where experts have that many by far, as shorter tiles that hold padding
-// alone are skipped. (112 experts with about 146 rows padded to 128, 2048 ->
-// 1024 gated: 128 x 256 tiles 252 us, 128 x 128 301, 64 x 256 306, 64 x 128 337.)
+// Plan of the products whose M is the call's rows. Over experts a tile holds
+// rows of one, and its rows go by how many an expert has on average, without
+// the padding. Where the tile does not divide the layout's alignment a launch
+// finds the tiles first (about 5 us), for 64 rows an expert and more. (112 experts with about 146 rows padded to 128, 2048 -> 1024 gated:
+// 128 x 256 tiles 252 us, 128 x 128 301, 64 x 256 306, 64 x 128 337; with about 277
+// rows in buffers for 400, 512 -> 4096: 256 x 256 tiles 302 us, 128 x 256 343, 512 ->
+// 2048 gated 261 and 289.)
 static Plan row_plan(const moe_expert_rows &r, int64_t M, int64_t N, int64_t K) {
   if (r.num_experts > 0) {
-    if (r.tile_m % 256 == 0 && M / r.num_experts >= 2048) return {TILE_256, 1};
-    return {r.tile_m % 128 == 0  ? TILE_128W
-            : r.tile_m % 64 == 0 ? TILE_64W
-            : r.tile_m % 32 == 0 ? TILE_32
-                                 : TILE_16,
-            1};
+    const int64_t mean = M / r.num_experts - r.tile_m / 2;
+    if (mean >= 320) return {TILE_256, 1};
+    if (mean >= 80) return {TILE_128W, 1};
+    if (mean >= 40 && (mean >= 64 || r.tile_m % 64 == 0)) return {TILE_64W, 1};
+    return {mean >= 20 && r.tile_m % 32 == 0 ? TILE_32 : TILE_16, 1};
   }
   if (M <= 16) return {TILE_16, 1};
   return dense_plan(1, M, N, K, true);
+}
+static int rows_of_tile(int kind) {
+  switch (kind) {
+    case TILE_16: return 16;
+    case TILE_32: return 32;
+    case TILE_64:
+    case TILE_64W: return 64;
+    case TILE_256: return 256;
+  }
+  return 128;
 }
 static Plan weight_plan(const moe_expert_rows &r, int64_t segs, int64_t M, int64_t N,
                         int64_t rows) {
@@ -124,10 +135,23 @@ static Plan weight_plan(const moe_expert_rows &r, int64_t segs, int64_t M, int64
 }
 
 // Runs a product by its plan, with the partial sums of a split one in the
-// workspace. `width`: the partial sums of a row of C.
-static int run_product(int dtype, int mode, const Plan &plan, GemmArgs &g, int width, Arena &ws,
-                       hipStream_t st) {
+// workspace. `width`: the partial sums of a row of C. `tile_m`: the alignment of
+// the layout, 0 for a dense product.
+static int run_product(int dtype, int mode, const Plan &plan, GemmArgs &g, int width, int tile_m,
+                       Arena &ws, hipStream_t st) {
   const int64_t stages = (g.K + 63) / 64;
+  const int bm = rows_of_tile(plan.kind);
+  if (mode != WGRAD && tile_m % bm != 0) {
+    // tiles that follow the experts' rows instead of the layout's alignment
+    g.m_tiles = (int)((g.M + bm - 1) / bm + g.r.num_experts);
+    int4 *map = reinterpret_cast<int4 *>(ws.take((size_t)(g.m_tiles + 1) * sizeof(int4)));
+    g.tile_map = map;
+    if (!ws.dry) {
+      tile_map_kernel<<<1, MAP_THREADS, 0, st>>>(g.r, bm, g.m_tiles, map);
+      const int got = hip_status();
+      if (got != MOE_OK) return got;
+    }
+  }
   if (plan.splits > 1) {
     g.k_split = (int)((stages + plan.splits - 1) / plan.splits) * 64;
     g.splits = (g.K + g.k_split - 1) / g.k_split;  // none of them empty
@@ -184,6 +208,7 @@ static int check_matrix(const moe_matrix &m, int64_t rows, int cols, int mats, b
 static int64_t call_rows(const moe_expert_rows &r, int64_t tokens) {
   return r.num_experts > 0 ? r.rows : tokens;
 }
+static int align_of(const moe_expert_rows &r) { return r.num_experts > 0 ? r.tile_m : 0; }
 static int mats_of(const moe_expert_rows &r) { return r.num_experts > 0 ? r.num_experts : 1; }
 
 // ---------------------------------------------------------------- gated block
@@ -254,7 +279,7 @@ static void set_c1(GemmArgs &g, const moe_matrix &c) {
 
 static int run_gated(const moe_gated_ffn_args *a, Arena &ws, hipStream_t st) {
   const int64_t rows = call_rows(a->rows, a->tokens);
-  const int mats = mats_of(a->rows), H = a->hidden, F = a->inter;
+  const int mats = mats_of(a->rows), align = align_of(a->rows), H = a->hidden, F = a->inter;
   int status = MOE_OK;
   if (rows == 0) return MOE_OK;
   const bool gather = a->rows.num_experts > 0 && a->rows.row_entry;
@@ -277,12 +302,13 @@ static int run_gated(const moe_gated_ffn_args *a, Arena &ws, hipStream_t st) {
   set_c0(g, a->h);
   g.pre = (uint16_t *)a->pre.p, g.ldp = a->pre.ld;
   g.M = (int)rows, g.N = F, g.K = H, g.act = a->activation;
-  return run_product(a->dtype, GATED, row_plan(a->rows, rows, 2 * F, H), g, 2 * F, ws, st);
+  return run_product(a->dtype, GATED, row_plan(a->rows, rows, 2 * F, H), g, 2 * F, align, ws, st);
 }
 
 static int run_gated_backward(const moe_gated_ffn_args *a, Arena &ws, hipStream_t st) {
   const int64_t rows = call_rows(a->rows, a->tokens);
-  const int mats = mats_of(a->rows), H = a->hidden, F = a->inter, Fa = round8(F);
+  const int mats = mats_of(a->rows), align = align_of(a->rows);
+  const int H = a->hidden, F = a->inter, Fa = round8(F);
   const bool gather = a->rows.num_experts > 0 && a->rows.row_entry;
   int status = MOE_OK;
   uint16_t *dz = ws.take((size_t)rows * 2 * Fa * 2);
@@ -316,7 +342,7 @@ static int run_gated_backward(const moe_gated_ffn_args *a, Arena &ws, hipStream_
     set_b1(d, wu);
     set_c0(d, a->dx);
     d.M = (int)rows, d.N = H, d.K = F;
-    MOE_TRY(run_product(a->dtype, DGRAD, row_plan(a->rows, rows, H, 2 * F), d, H, ws, st));
+    MOE_TRY(run_product(a->dtype, DGRAD, row_plan(a->rows, rows, H, 2 * F), d, H, align, ws, st));
   }
   if (a->dw_gate.p) {
     set_b0(g, x);
@@ -325,7 +351,7 @@ static int run_gated_backward(const moe_gated_ffn_args *a, Arena &ws, hipStream_
     set_c0(g, a->dw_gate);
     set_c1(g, a->dw_up);
     g.M = F, g.N = H, g.K = (int)rows;
-    MOE_TRY(run_product(a->dtype, WGRAD, weight_plan(a->rows, 2, F, H, rows), g, H, ws, st));
+    MOE_TRY(run_product(a->dtype, WGRAD, weight_plan(a->rows, 2, F, H, rows), g, H, align, ws, st));
   }
   return MOE_OK;
 }
@@ -353,7 +379,7 @@ static int check_linear(const moe_linear_args *a, bool backward) {
 
 static int run_linear(const moe_linear_args *a, Arena &ws, hipStream_t st) {
   const int64_t rows = call_rows(a->rows, a->tokens);
-  const int mats = mats_of(a->rows), I = a->in, O = a->out;
+  const int mats = mats_of(a->rows), align = align_of(a->rows), I = a->in, O = a->out;
   int status = MOE_OK;
   if (rows == 0) return MOE_OK;
   const Operand x = operand(a->x, rows, I, 1, ws, st, &status);
@@ -367,7 +393,7 @@ static int run_linear(const moe_linear_args *a, Arena &ws, hipStream_t st) {
   g.bias = (const uint16_t *)a->bias.p, g.bias_stride = a->bias.stride;
   g.res = (const uint16_t *)a->residual.p, g.ldr = a->residual.ld;
   g.M = (int)rows, g.N = O, g.K = I, g.act = a->activation;
-  return run_product(a->dtype, LINEAR, row_plan(a->rows, rows, O, I), g, O, ws, st);
+  return run_product(a->dtype, LINEAR, row_plan(a->rows, rows, O, I), g, O, align, ws, st);
 }
 
 // Row ranges of the bias gradient's partial sums: dense, one for every 256
@@ -380,7 +406,8 @@ static int bias_splits(const moe_expert_rows &r, int64_t rows) {
 
 static int run_linear_backward(const moe_linear_args *a, Arena &ws, hipStream_t st) {
   const int64_t rows = call_rows(a->rows, a->tokens);
-  const int mats = mats_of(a->rows), I = a->in, O = a->out, Oa = round8(O);
+  const int mats = mats_of(a->rows), align = align_of(a->rows);
+  const int I = a->in, O = a->out, Oa = round8(O);
   const bool bf = a->dtype == MOE_BF16;
   int status = MOE_OK;
   GemmArgs g = gemm_args(a->rows, rows, false);
@@ -422,13 +449,13 @@ static int run_linear_backward(const moe_linear_args *a, Arena &ws, hipStream_t 
     set_b0(d, w);
     set_c0(d, a->dx);
     d.M = (int)rows, d.N = I, d.K = O;
-    MOE_TRY(run_product(a->dtype, DGRAD, row_plan(a->rows, rows, I, O), d, I, ws, st));
+    MOE_TRY(run_product(a->dtype, DGRAD, row_plan(a->rows, rows, I, O), d, I, align, ws, st));
   }
   if (a->dw.p) {
     set_b0(g, x);
     set_c0(g, a->dw);
     g.M = O, g.N = I, g.K = (int)rows;
-    MOE_TRY(run_product(a->dtype, WGRAD, weight_plan(a->rows, 1, O, I, rows), g, I, ws, st));
+    MOE_TRY(run_product(a->dtype, WGRAD, weight_plan(a->rows, 1, O, I, rows), g, I, align, ws, st));
   }
   return MOE_OK;
 }

@@ -190,7 +190,9 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
     }
   } else {
     int live = g.m_tiles;  // m-tiles with rows of the experts here
-    if (grouped) {
+    if (g.tile_map) {
+      live = g.tile_map[g.m_tiles].x;
+    } else if (grouped) {
       const int64_t end = g.r.padded_offsets[g.r.num_experts];
       live = (int)min((int64_t)g.m_tiles, (max(end, (int64_t)0) + BM - 1) / BM);
     }
@@ -204,7 +206,13 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
       nt = t % g.n_tiles;
     }
   }
-  const int m0 = mt * BM;
+  int m0 = mt * BM, m_end = g.M;  // rows of the tile that are its own: below m_end
+  if (MODE != WGRAD && g.tile_map) {
+    const int4 tile = g.tile_map[mt];
+    m0 = tile.x;
+    m_end = tile.y;
+    if (m0 >= m_end) return;
+  }
   const int n0 = nt * (MODE == GATED ? BN / 2 : BN);  // column of C
 
   if constexpr (MODE != WGRAD) {
@@ -216,7 +224,7 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
         for (int i = threadIdx.x; i < BM * RUNS; i += C::NTHREADS) {
           const int64_t m = m0 + i / RUNS;
           const int n = n0 + i % RUNS * 8;
-          if (m >= g.M || n >= g.N) continue;
+          if (m >= m_end || n >= g.N) continue;
           store8_raw(g.c0 + m * g.ldc0, n, g.N, zero);
           if (MODE <= LINEAR && g.pre) {
             store8_raw(g.pre + m * g.ldp, n, g.N, zero);
@@ -536,7 +544,7 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
     for (int i = 0; i < C::FM; ++i)
 #pragma unroll
       for (int p = 0; p < PASSES; ++p)
-        if (row_of(i, p) < g.M && g.r.m_indices[row_of(i, p)] == e) real |= 1u << (i * PASSES + p);
+        if (row_of(i, p) < m_end && g.r.m_indices[row_of(i, p)] == e) real |= 1u << (i * PASSES + p);
   }
   auto is_real = [&](int i, int p) MOE_INLINE { return (real >> (i * PASSES + p) & 1) != 0; };
   static_assert(C::FM * PASSES <= 32, "a bit a run");
@@ -546,7 +554,7 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
     for (int i = 0; i < C::FM; ++i)
 #pragma unroll
       for (int p = 0; p < PASSES; ++p)
-        if (cols && row_of(i, p) < g.M)
+        if (cols && row_of(i, p) < m_end)
           residual[i * PASSES + p] = load8_raw(g.res + row_of(i, p) * g.ldr, n, g.N);
   }
   wait_vmcnt_imm<0>();  // with them the zeros still on their way to LDS
@@ -569,7 +577,7 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
 #pragma unroll
         for (int p = 0; p < PASSES; ++p) {
           const f32x8 v = turn_out(p);
-          if (cols && row_of(i, p) < g.M)
+          if (cols && row_of(i, p) < m_end)
             store8_f32(part + row_of(i, p) * width + side * g.N, n, g.N, v);
         }
       }
@@ -587,7 +595,7 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
       for (int p = 0; p < PASSES; ++p) {
         const f32x8 v = turn_out(p);
         const int64_t m = row_of(i, p);
-        if (cols && m < g.M)
+        if (cols && m < m_end)
           store8<D>(to + m * ld, col, width, is_real(i, p) ? v : zero8);
       }
     };
@@ -617,7 +625,7 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
       for (int p = 0; p < PASSES; ++p) {
         f32x8 z = turn_out(p);
         const int64_t m = row_of(i, p);
-        if (!cols || m >= g.M) continue;
+        if (!cols || m >= m_end) continue;
         if constexpr (MODE == LINEAR) {
 #pragma unroll
           for (int v = 0; v < 8; ++v) z[v] += bias[v];

@@ -19,7 +19,7 @@ typedef Tile<16, 128, 16, 32, 4, 2> Tile16;
 template <class D, int MODE, class C>
 static int launch(GemmArgs g, hipStream_t st) {
   const int bn = MODE == GATED ? C::BN / 2 : C::BN;
-  g.m_tiles = (g.M + C::BM - 1) / C::BM;
+  if (!g.tile_map) g.m_tiles = (g.M + C::BM - 1) / C::BM;
   g.n_tiles = (g.N + bn - 1) / bn;
   int64_t blocks = (int64_t)g.m_tiles * g.n_tiles;
   if (MODE == WGRAD) blocks *= (int64_t)(g.r.num_experts > 0 ? g.r.num_experts : 1) * g.segs;

@@ -52,6 +52,47 @@ __global__ __launch_bounds__(COL_THREADS *ROW_THREADS) void gather_rows_kernel(
   }
 }
 
+// The m-tiles of bm rows over a layout, each within one expert's rows: rows
+// [x, y) of tile i in map[i], the experts' first and in order, then the rows past
+// them, then empty ones up to m_tiles; map[m_tiles].x: how many the experts have.
+constexpr int MAP_THREADS = 1024;
+__global__ __launch_bounds__(MAP_THREADS) void tile_map_kernel(Rows r, int bm, int m_tiles,
+                                                               int4 *__restrict__ map) {
+  __shared__ int sums[MAP_THREADS];
+  constexpr int EACH = MOE_FFN_MAX_EXPERTS / MAP_THREADS;
+  const int t = threadIdx.x, rows = (int)r.rows;
+  auto first_row = [&](int e) { return min(max(r.padded_offsets[min(e, r.num_experts)], 0), rows); };
+  int tiles[EACH], mine = 0;
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    const int e = t * EACH + i;
+    tiles[i] = e < r.num_experts ? (max(first_row(e + 1) - first_row(e), 0) + bm - 1) / bm : 0;
+    mine += tiles[i];
+  }
+  sums[t] = mine;
+  __syncthreads();
+  for (int d = 1; d < MAP_THREADS; d *= 2) {  // inclusive sums
+    const int v = t >= d ? sums[t - d] : 0;
+    __syncthreads();
+    sums[t] += v;
+    __syncthreads();
+  }
+  int at = sums[t] - mine;
+  const int live = min(sums[MAP_THREADS - 1], m_tiles), end = first_row(r.num_experts);
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    const int e = t * EACH + i;
+    const int lo = first_row(e), hi = first_row(e + 1);
+    for (int k = 0; k < tiles[i]; ++k, ++at)
+      if (at < m_tiles) map[at] = make_int4(lo + k * bm, min(lo + (k + 1) * bm, hi), 0, 0);
+  }
+  for (int i = live + t; i < m_tiles; i += MAP_THREADS) {
+    const int64_t lo = end + (int64_t)(i - live) * bm;
+    map[i] = make_int4((int)min(lo, (int64_t)rows), (int)min(lo + bm, (int64_t)rows), 0, 0);
+  }
+  if (t == 0) map[m_tiles] = make_int4(live, 0, 0, 0);
+}
+
 // Gradient of a gated block's pre-activations, rounded once: dz [rows, 2 Fa]
 // with dg = dh u act'(g) in the first Fa = round_up(F, 8) columns and
 // du = dh act(g) in the others, zeros in the padding. Rows without an entry

@@ -197,6 +197,10 @@ struct GemmArgs {
   int32_t segs;            // 1, or 2 for the two projections of a gated block
   int32_t act;
   int32_t m_tiles, n_tiles;
+  // over experts, where the tile does not divide the layout's alignment: rows
+  // [x, y) of each m-tile, then in element m_tiles the number of those with an
+  // expert; else NULL
+  const int4 *tile_map;
   // dense only: K in `splits` ranges of k_split (a multiple of 64), each summed
   // into its own partial [splits][WGRAD: segs][M][N, GATED: 2 N]; NULL: one range
   int32_t splits, k_split;

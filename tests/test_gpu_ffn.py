@@ -576,3 +576,29 @@ def test_moe_block_example(tokens):
         assert E.off(grads[k], ref[k]) <= 6 * half_step(BF), k
     plain, _ = block.forward(x)
     assert torch.equal(plain, out)
+
+
+@pytest.mark.parametrize("T,n,k,tile,extra", [(60, 8, 4, 16, 0), (130, 8, 4, 16, 100), (400, 8, 3, 16, 0),
+                                              (400, 8, 3, 48, 200), (3000, 2, 1, 16, 70), (3000, 3, 1, 80, 0),
+                                              (900, 20, 4, 64, 33)])
+def test_tiles_that_follow_the_experts(T, n, k, tile, extra):
+    """More rows an expert than the layout's alignment: tiles that do not divide
+    it, with rows past the experts' to be cleared."""
+    g = torch.Generator().manual_seed(T)
+    ids = torch.stack([torch.randperm(n, generator=g)[:k] for _ in range(T)])
+    ids = torch.where(ids == 1, 0, ids) if k == 1 else ids  # an expert without rows
+    full = hand_layout(ids, n, tile)
+    lay = hand_layout(ids, n, tile, rows=full["m_indices"].numel() + extra)
+    check_expert_gated(lay, n, k, normal(1, T, 200, dt=BF), 136, tile, BF)
+    rows = lay["m_indices"].numel()
+    w, b = normal(6, n, 264, 136, dt=BF, scale=136 ** -0.5), normal(7, n, 264, dt=BF)
+    x, res = normal(8, rows, 136, dt=BF), normal(9, rows, 264, dt=BF)
+    r = M.expert_linear(x, w, lay, tile_m=tile, bias=b, activation="gelu", residual=res,
+                        save_pre=True, out={"y": torch.full((rows, 264), 9.0, dtype=BF, device="cuda")})
+    rest = torch.ones(rows, dtype=torch.bool)
+    for e, at, _ in groups(lay, n, rows, k):
+        rest[at] = False
+        ref, bd, z, bz = linear_oracle(x[at], w[e], b[e], "gelu", res[at], BF)
+        assert_close(r["y"][at], ref, bd, f"y of {e}")
+        assert_close(r["pre"][at], z, bz, f"z of {e}")
+    assert not bool(r["y"][rest].any()) and not bool(r["pre"][rest].any())
