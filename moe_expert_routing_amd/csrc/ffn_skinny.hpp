@@ -71,10 +71,10 @@ __global__ __launch_bounds__(64 * SKINNY_WAVES) void skinny_kernel(const GemmArg
     auto load = [&](int set, int s) MOE_INLINE {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        fw[set][u] = *reinterpret_cast<const s16x8 *>(w + (s + u) * 32);
+        fw[set][u] = *reinterpret_cast<const s16x8_any *>(w + (s + u) * 32);
 #pragma unroll
         for (int x = 0; x < RX; ++x)
-          fx[set][u][x] = *reinterpret_cast<const s16x8 *>(xr[x] + (s + u) * 32);
+          fx[set][u][x] = *reinterpret_cast<const s16x8_any *>(xr[x] + (s + u) * 32);
       }
     };
     auto multiply = [&](int set) MOE_INLINE {
@@ -95,14 +95,11 @@ __global__ __launch_bounds__(64 * SKINNY_WAVES) void skinny_kernel(const GemmArg
     }
     if (b < whole) multiply(0);
     for (int s = whole * U; s < s1 - s0; ++s) {  // the rest, and K's own tail
-      s16x8 a = {0, 0, 0, 0, 0, 0, 0, 0}, c[RX];
-      const bool in = (s0 + s) * 32 + fq * 8 < K;
-      if (in) a = *reinterpret_cast<const s16x8 *>(w + s * 32);
+      const int in = K - (s0 + s) * 32 - fq * 8;  // elements left in this lane's piece
+      const s16x8 a = load8_raw(w + s * 32, 0, in);
+      s16x8 c[RX];
 #pragma unroll
-      for (int x = 0; x < RX; ++x) {
-        c[x] = s16x8{0, 0, 0, 0, 0, 0, 0, 0};
-        if (in) c[x] = *reinterpret_cast<const s16x8 *>(xr[x] + s * 32);
-      }
+      for (int x = 0; x < RX; ++x) c[x] = load8_raw(xr[x] + s * 32, 0, in);
 #pragma unroll
       for (int x = 0; x < RX; ++x) acc[x] = D::mfma(a, c[x], acc[x]);
     }
