@@ -287,6 +287,35 @@ static bool reads_directly(const moe_expert_rows &r, const Plan &plan) {
 }
 static Operand as_is(const moe_matrix &m) { return {(const uint16_t *)m.p, m.ld, m.stride}; }
 
+// Whether the weight gradients go by few_rows_dw_kernel. Both gradients of a gated
+// block, few rows and matrix cores: 7168 -> 2048 of 1 row 14 and 21 us, 8 rows 17 and
+// 21, 16 rows 23 and 22; 64 experts of 2048 -> 512 with 1 row each 49 and 63, 8 rows 74
+// and 78, 16 rows 102 and 79.
+constexpr int FEW_DW_ROWS = 8;
+static bool few_rows(const moe_expert_rows &r, int64_t rows) {
+  const int64_t mean = r.num_experts > 0 ? rows / r.num_experts - r.tile_m / 2 : rows;
+  return mean <= FEW_DW_ROWS;
+}
+static int run_few_rows(int dtype, bool gated, const moe_matrix &d,
+                        const moe_matrix &pre, const moe_matrix &x, int64_t x_rows,
+                        const moe_matrix &dw0, const moe_matrix &dw1, int64_t rows, int F, int H,
+                        int act, int mats, const Rows &r, hipStream_t st) {
+  FewRowsArgs a = {};
+  a.d = (const uint16_t *)d.p, a.ld_d = d.ld;
+  if (gated || act != MOE_ACT_NONE) a.pre = (const uint16_t *)pre.p, a.ld_pre = pre.ld;
+  a.x = (const uint16_t *)x.p, a.ld_x = x.ld, a.x_rows = x_rows;
+  a.dw0 = (uint16_t *)dw0.p, a.ld0 = dw0.ld, a.stride0 = dw0.stride;
+  a.dw1 = (uint16_t *)dw1.p, a.ld1 = dw1.ld, a.stride1 = dw1.stride;
+  a.rows = rows, a.F = F, a.H = H, a.act = act, a.r = r;
+  a.f_blocks = (F + FEW_F * FEW_WAVES - 1) / (FEW_F * FEW_WAVES);
+  const dim3 grid((H + 511) / 512, a.f_blocks * (gated ? 2 : 1), mats);
+  const bool bf = dtype == MOE_BF16;
+  const auto kernel = gated ? (bf ? few_rows_dw_kernel<Bf16, true> : few_rows_dw_kernel<F16, true>)
+                            : (bf ? few_rows_dw_kernel<Bf16, false> : few_rows_dw_kernel<F16, false>);
+  kernel<<<grid, 64 * FEW_WAVES, 0, st>>>(a);
+  return hip_status();
+}
+
 static int run_gated(const moe_gated_ffn_args *a, Arena &ws, hipStream_t st) {
   const int64_t rows = call_rows(a->rows, a->tokens);
   const int mats = mats_of(a->rows), align = align_of(a->rows), H = a->hidden, F = a->inter;
@@ -328,9 +357,10 @@ static int run_gated_backward(const moe_gated_ffn_args *a, Arena &ws, hipStream_
   uint16_t *dz = ws.take((size_t)rows * 2 * Fa * 2);
   Operand x = {}, wg = {}, wu = {};
   GemmArgs g = gemm_args(a->rows, rows, gather);
+  const bool few = a->dw_gate.p && few_rows(a->rows, rows);
   const bool wide = gather && is_wide(a->x, a->tokens);
-  if (a->dw_gate.p && wide) x = gathered(a->x, a->tokens, H, g.r, rows, ws, st, &status);
-  if (a->dw_gate.p && !wide) x = operand(a->x, a->tokens, H, 1, ws, st, &status);
+  if (a->dw_gate.p && !few && wide) x = gathered(a->x, a->tokens, H, g.r, rows, ws, st, &status);
+  if (a->dw_gate.p && !few && !wide) x = operand(a->x, a->tokens, H, 1, ws, st, &status);
   if (a->dx.p && rows > 0) {
     // the product goes from one weight to the other with the same offsets
     const bool copy = !is_aligned(a->w_gate, H, mats) || !is_aligned(a->w_up, H, mats) ||
@@ -339,7 +369,7 @@ static int run_gated_backward(const moe_gated_ffn_args *a, Arena &ws, hipStream_
     wu = operand(a->w_up, F, H, mats, ws, st, &status, copy);
   }
   if (status != MOE_OK) return status;
-  if (rows > 0 && !ws.dry) {
+  if (rows > 0 && (a->dx.p || !few) && !ws.dry) {
     const dim3 grid = row_grid(rows, Fa, 1), block(COL_THREADS, ROW_THREADS);
     const auto kernel = a->dtype == MOE_BF16 ? gated_dz_kernel<Bf16> : gated_dz_kernel<F16>;
     kernel<<<grid, block, 0, st>>>((const uint16_t *)a->dh.p, a->dh.ld,
@@ -358,6 +388,10 @@ static int run_gated_backward(const moe_gated_ffn_args *a, Arena &ws, hipStream_
     d.M = (int)rows, d.N = H, d.K = F;
     MOE_TRY(run_product(a->dtype, DGRAD, row_plan(a->rows, rows, H, 2 * F), d, H, align, ws, st));
   }
+  if (few)
+    return ws.dry ? MOE_OK
+                  : run_few_rows(a->dtype, true, a->dh, a->pre, a->x, a->tokens, a->dw_gate,
+                                 a->dw_up, rows, F, H, a->activation, mats, g.r, st);
   if (a->dw_gate.p) {
     set_b0(g, x);
     g.a_rows = wide ? rows : a->tokens;
@@ -429,7 +463,8 @@ static int run_linear_backward(const moe_linear_args *a, Arena &ws, hipStream_t 
   GemmArgs g = gemm_args(a->rows, rows, false);
   const uint16_t *dy = (const uint16_t *)a->dy.p, *pre = (const uint16_t *)a->pre.p;
   // dz: dy itself without an activation, where its pieces are aligned
-  const bool products = a->dx.p || a->dw.p, none = a->activation == MOE_ACT_NONE;
+  const bool few = a->dw.p && few_rows(a->rows, rows);
+  const bool products = a->dx.p || (a->dw.p && !few), none = a->activation == MOE_ACT_NONE;
   Operand dz = {};
   if (products && none) dz = operand(a->dy, rows, O, 1, ws, st, &status);
   if (products && !none) dz = {ws.take((size_t)rows * Oa * 2), Oa, 0};
@@ -454,9 +489,8 @@ static int run_linear_backward(const moe_linear_args *a, Arena &ws, hipStream_t 
         dy, a->dy.ld, pre, a->pre.ld, rows, O, a->activation, g.r, dz_out);
     MOE_TRY(hip_status());
   }
-  if (!products) return status;
   Operand x = {}, w = {};
-  if (a->dw.p) x = operand(a->x, rows, I, 1, ws, st, &status);
+  if (a->dw.p && !few) x = operand(a->x, rows, I, 1, ws, st, &status);
   if (a->dx.p && rows > 0) w = operand(a->w, O, I, mats, ws, st, &status);
   if (status != MOE_OK) return status;
   g.a = dz.p, g.lda = dz.ld, g.a_rows = rows;
@@ -467,6 +501,10 @@ static int run_linear_backward(const moe_linear_args *a, Arena &ws, hipStream_t 
     d.M = (int)rows, d.N = I, d.K = O;
     MOE_TRY(run_product(a->dtype, DGRAD, row_plan(a->rows, rows, I, O), d, I, align, ws, st));
   }
+  if (few)
+    return ws.dry ? MOE_OK
+                  : run_few_rows(a->dtype, false, a->dy, a->pre, a->x, rows, a->dw, a->dw, rows, O, I,
+                                 a->activation, mats, g.r, st);
   if (a->dw.p) {
     set_b0(g, x);
     set_c0(g, a->dw);

@@ -206,6 +206,75 @@ __global__ __launch_bounds__(256) void bias_sum_kernel(const float *__restrict__
                                             sum[3][threadIdx.x]);
 }
 
+// Weight gradients of few rows, dW[f, h] = sum over the rows of dz[row, f]
+// x[row, h], in fp32 and with dz unrounded: over a handful of rows dz's rounding
+// would not average out, and the matrix cores' 64-row stages are mostly
+// empty. Bound by writing dW. A block takes 32 f and 512 h; the dz of its f are
+// formed in LDS from dh or dy, 16 rows at a time, and a wave multiplies 8 f by 8
+// consecutive h a lane, 64 sums.
+constexpr int FEW_F = 8, FEW_WAVES = 4, FEW_ROWS = 16;
+struct FewRowsArgs {
+  const uint16_t *d, *pre, *x;  // d: dh or dy; pre: NULL without an activation
+  int64_t ld_d, ld_pre, ld_x, x_rows, rows;
+  uint16_t *dw0, *dw1;  // dw1: gated, of the second projection
+  int64_t ld0, ld1, stride0, stride1;
+  int F, H, f_blocks, act;
+  Rows r;
+};
+template <class D, bool GATED_DZ>
+__global__ __launch_bounds__(64 * FEW_WAVES) void few_rows_dw_kernel(const FewRowsArgs a) {
+  __shared__ __attribute__((aligned(32))) float dz[FEW_ROWS][FEW_F * FEW_WAVES];
+  __shared__ int64_t at[FEW_ROWS];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int seg = blockIdx.y / a.f_blocks, e = blockIdx.z;
+  const int fb = blockIdx.y % a.f_blocks * FEW_F * FEW_WAVES, f0 = fb + wave * FEW_F;
+  const int c = (blockIdx.x * 64 + lane) * 8;
+  int64_t first = 0, n = a.rows;
+  if (a.r.num_experts > 0) {
+    first = min(max((int64_t)a.r.padded_offsets[e], (int64_t)0), a.rows);
+    n = min(max((int64_t)a.r.counts[e], (int64_t)0), a.rows - first);
+  }
+  f32x8 acc[FEW_F];
+#pragma unroll
+  for (int i = 0; i < FEW_F; ++i) acc[i] = f32x8{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int64_t m0 = first; m0 < first + n; m0 += FEW_ROWS) {
+    const int rows = (int)min(first + n - m0, (int64_t)FEW_ROWS);
+    __syncthreads();
+    if (lane < rows) {  // each wave its own 8 f, a row a lane
+      const int64_t m = m0 + lane;
+      f32x8 v = load8<D>(a.d + m * a.ld_d, f0, a.F);
+      if (a.pre) {
+        f32x8 value, slope;
+        act_value_slope(load8<D>(a.pre + m * a.ld_pre, f0, a.F), a.act, value, slope);
+        if (GATED_DZ && seg == 0) v *= load8<D>(a.pre + m * a.ld_pre + a.F, f0, a.F);
+        v *= GATED_DZ && seg == 1 ? value : slope;
+      }
+      *reinterpret_cast<f32x8 *>(&dz[lane][wave * FEW_F]) = v;
+      int64_t row = m;
+      if (a.r.row_entry) {
+        const uint32_t t = (uint32_t)a.r.row_entry[m] / (uint32_t)a.r.top_k;
+        row = t < (uint64_t)a.x_rows ? t : 0;
+      }
+      if (wave == 0) at[lane] = row * a.ld_x;
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int i = 0; i < rows; ++i) {
+      const f32x8 x = load8<D>(a.x + at[i], c, a.H);
+      const f32x8 d = *reinterpret_cast<const f32x8 *>(&dz[i][wave * FEW_F]);
+#pragma unroll
+      for (int f = 0; f < FEW_F; ++f)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[f][j] = fmaf(d[f], x[j], acc[f][j]);
+    }
+  }
+  uint16_t *dw = seg ? a.dw1 + e * a.stride1 : a.dw0 + e * a.stride0;
+  const int64_t ld = seg ? a.ld1 : a.ld0;
+#pragma unroll
+  for (int i = 0; i < FEW_F; ++i)
+    if (f0 + i < a.F) store8<D>(dw + (f0 + i) * ld, c, a.H, acc[i]);
+}
+
 // The partial sums of a product that was split over k, added in the order of
 // the ranges, and its epilogue. blockIdx.z: WGRAD's segment.
 template <class D>

@@ -7,8 +7,9 @@ import pytest
 import torch
 
 import moe_expert_routing_amd as M
-from ffn_util import (F32, TINY, act, assert_close, gated_grads, gated_oracle, groups,
-                      half_step, hand_layout, linear_grads, linear_oracle, local_layout, normal)
+from ffn_util import (ACT_ULP, F32, TINY, act, assert_close, gated_grads, gated_oracle, groups,
+                      half_step, hand_layout, linear_grads, linear_oracle, local_layout, normal,
+                      slope)
 
 pytestmark = [
     pytest.mark.gpu,
@@ -602,3 +603,22 @@ def test_tiles_that_follow_the_experts(T, n, k, tile, extra):
         assert_close(r["y"][at], ref, bd, f"y of {e}")
         assert_close(r["pre"][at], z, bz, f"z of {e}")
     assert not bool(r["y"][rest].any()) and not bool(r["pre"][rest].any())
+
+
+@pytest.mark.parametrize("T,H,F", [(1, 2112, 322), (3, 513, 33), (8, 1088, 448), (5, 7, 1500)])
+@pytest.mark.parametrize("dt,name", [(BF, "silu"), (FP, "gelu"), (FP, "none")])
+def test_weight_gradients_of_few_rows_are_rounded_once(T, H, F, dt, name):
+    """Up to 8 rows: fp32 up to the result, so half a step of it, the fp32 sum
+    and the activation's own error are all there is."""
+    x, dh, pre = normal(1, T, H, dt=dt), normal(2, T, F, dt=dt), normal(3, T, 2 * F, dt=dt)
+    wg, wu = normal(4, F, H, dt=dt), normal(5, F, H, dt=dt)
+    d, g, u, xd = dh.double(), pre[:, :F].double(), pre[:, F:].double(), x.double()
+    out = {"dw_gate": torch.empty_like(wg), "dw_up": torch.empty_like(wu)}
+    r = M.gated_ffn_backward(dh, pre, x, wg, wu, activation=name, out=out)
+    y = M.linear_backward(dh, x, wg, pre=pre[:, :F], activation=name, out={"dw": torch.empty_like(wg)})
+    for got, f, size in ((r["dw_gate"], slope(g, name) * u, (1 + g.abs()) * u.abs()),
+                         (r["dw_up"], act(g, name), g.abs()), (y["dw"], slope(g, name), 1 + g.abs())):
+        dz = d * f
+        S = (dz.abs() * (T + 8) + 2 * ACT_ULP * d.abs() * size).T @ xd.abs()
+        ref = dz.T @ xd
+        assert_close(got, ref, half_step(dt) * 1.01 * ref.abs() + F32 * S * 1.01 + TINY[dt], name)
