@@ -476,12 +476,13 @@ static int run_linear_backward(const moe_linear_args *a, Arena &ws, hipStream_t 
       const dim3 grid((O + 63) / 64, S, mats), block(8, BIAS_ROWS);
       const auto sums = bf ? bias_grad_kernel<Bf16> : bias_grad_kernel<F16>;
       sums<<<grid, block, 0, st>>>(dy, a->dy.ld, pre, a->pre.ld, rows, O, a->activation, g.r, S,
-                                   part, dz_out);
+                                   part, dz_out, (uint16_t *)a->dbias.p, a->dbias.stride);
       MOE_TRY(hip_status());
-      const auto join = bf ? bias_sum_kernel<Bf16> : bias_sum_kernel<F16>;
-      join<<<dim3((O + 63) / 64, 1, mats), 256, 0, st>>>(part, S, O, (uint16_t *)a->dbias.p,
-                                                         a->dbias.stride);
-      MOE_TRY(hip_status());
+      if (S > 1) {
+        const auto join = bf ? bias_sum_kernel<Bf16> : bias_sum_kernel<F16>;
+        join<<<dim3((O + 63) / 64), 256, 0, st>>>(part, S, O, (uint16_t *)a->dbias.p);
+        MOE_TRY(hip_status());
+      }
     }
   } else if (dz_out && !ws.dry && rows > 0) {
     const auto kernel = bf ? linear_dz_kernel<Bf16> : linear_dz_kernel<F16>;
