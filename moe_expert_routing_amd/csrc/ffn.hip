@@ -103,11 +103,14 @@ static Plan dense_plan(int64_t mats, int64_t M, int64_t N, int64_t K, bool may_s
 // Plan of the products whose M is the call's rows. Over experts a tile holds
 // rows of one, and its rows go by how many an expert has on average, without
 // the padding. Where the tile does not divide the layout's alignment a launch
-// finds the tiles first (about 5 us), for 64 rows an expert and more. (112 experts with about 146 rows padded to 128, 2048 -> 1024 gated:
-// 128 x 256 tiles 252 us, 128 x 128 301, 64 x 256 306, 64 x 128 337; with about 277
-// rows in buffers for 400, 512 -> 4096: 256 x 256 tiles 302 us, 128 x 256 343, 512 ->
-// 2048 gated 261 and 289.)
-static Plan row_plan(const moe_expert_rows &r, int64_t M, int64_t N, int64_t K) {
+// finds the tiles first (about 5 us), for 64 rows an expert and more. (112 experts
+// with about 146 rows padded to 128, 2048 -> 1024 gated: 128 x 256 tiles 252 us, 128 x
+// 128 301, 64 x 256 306, 64 x 128 337; with about 277 rows in buffers for 400, 512 ->
+// 4096: 256 x 256 tiles 302 us, 128 x 256 343, 512 -> 2048 gated 261 and 289.) A dense
+// forward product of up to 16 rows goes by the skinny kernel; dx of as few, whose
+// weights are read transposed, by the plan (16-row tiles and the plan: 8 rows of 7168
+// from 7168 48 and 26 us, 12 rows of 4096 from 14336 87 and 31).
+static Plan row_plan(const moe_expert_rows &r, bool forward, int64_t M, int64_t N, int64_t K) {
   if (r.num_experts > 0) {
     const int64_t mean = M / r.num_experts - r.tile_m / 2;
     if (mean >= 320) return {TILE_256, 1};
@@ -115,7 +118,7 @@ static Plan row_plan(const moe_expert_rows &r, int64_t M, int64_t N, int64_t K) 
     if (mean >= 40 && (mean >= 64 || r.tile_m % 64 == 0)) return {TILE_64W, 1};
     return {mean >= 20 && r.tile_m % 32 == 0 ? TILE_32 : TILE_16, 1};
   }
-  if (M <= 16) return {TILE_16, 1};
+  if (forward && M <= 16) return {TILE_16, 1};
   return dense_plan(1, M, N, K, true);
 }
 static int rows_of_tile(int kind) {
@@ -324,7 +327,7 @@ static int run_gated(const moe_gated_ffn_args *a, Arena &ws, hipStream_t st) {
   const bool gather = a->rows.num_experts > 0 && a->rows.row_entry;
   GemmArgs g = gemm_args(a->rows, rows, gather);
   g.a_rows = a->tokens;
-  const Plan plan = row_plan(a->rows, rows, 2 * F, H);
+  const Plan plan = row_plan(a->rows, true, rows, 2 * F, H);
   const bool direct = reads_directly(a->rows, plan);
   Operand x;
   if (direct) {
@@ -386,7 +389,7 @@ static int run_gated_backward(const moe_gated_ffn_args *a, Arena &ws, hipStream_
     set_b1(d, wu);
     set_c0(d, a->dx);
     d.M = (int)rows, d.N = H, d.K = F;
-    MOE_TRY(run_product(a->dtype, DGRAD, row_plan(a->rows, rows, H, 2 * F), d, H, align, ws, st));
+    MOE_TRY(run_product(a->dtype, DGRAD, row_plan(a->rows, false, rows, H, 2 * F), d, H, align, ws, st));
   }
   if (few)
     return ws.dry ? MOE_OK
@@ -430,7 +433,7 @@ static int run_linear(const moe_linear_args *a, Arena &ws, hipStream_t st) {
   const int mats = mats_of(a->rows), align = align_of(a->rows), I = a->in, O = a->out;
   int status = MOE_OK;
   if (rows == 0) return MOE_OK;
-  const Plan plan = row_plan(a->rows, rows, O, I);
+  const Plan plan = row_plan(a->rows, true, rows, O, I);
   const bool direct = reads_directly(a->rows, plan);
   const Operand x = direct ? as_is(a->x) : operand(a->x, rows, I, 1, ws, st, &status);
   const Operand w = direct ? as_is(a->w) : operand(a->w, O, I, mats, ws, st, &status);
@@ -500,7 +503,7 @@ static int run_linear_backward(const moe_linear_args *a, Arena &ws, hipStream_t 
     set_b0(d, w);
     set_c0(d, a->dx);
     d.M = (int)rows, d.N = I, d.K = O;
-    MOE_TRY(run_product(a->dtype, DGRAD, row_plan(a->rows, rows, I, O), d, I, align, ws, st));
+    MOE_TRY(run_product(a->dtype, DGRAD, row_plan(a->rows, false, rows, I, O), d, I, align, ws, st));
   }
   if (few)
     return ws.dry ? MOE_OK
