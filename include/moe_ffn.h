@@ -16,13 +16,15 @@
  *  - Matrices hold bf16 or fp16 (moe_dtype), all of a call the same; sums are
  *    fp32 and each output is rounded once. Inside moe_gated_ffn_backward and
  *    moe_linear_backward the gradient of the pre-activations is rounded once
- *    to the matrices' type before the two products that take it.
+ *    to the matrices' type before the two products that take it (weight
+ *    gradients of up to 8 rows, or rows an expert, take it unrounded).
  *  - A moe_matrix has contiguous columns and rows `ld` elements apart; a
  *    stack of one matrix per expert has them `stride` elements apart. Any ld
  *    of at least the columns, any stride and any element alignment works.
  *    The matrix cores read 16-byte pieces: an operand of a product whose
  *    pointer, ld, stride or columns are no multiple of 8 elements is first
- *    copied into the workspace with its rows padded.
+ *    copied into the workspace with its rows padded (but for forward
+ *    products over experts with few rows, which read them in place).
  *  - Dense form: rows.num_experts = 0, the rows are the tokens.
  *  - Expert form: rows.num_experts = n experts with weights, ids 0 .. n-1 of
  *    a grouped layout (moe_grouped_layout, moe_route_local_grouped). A row r
