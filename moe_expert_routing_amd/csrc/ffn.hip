@@ -251,10 +251,13 @@ static GemmArgs gemm_args(const moe_expert_rows &r, int64_t rows, bool gather) {
   }
   return g;
 }
-// Gathered rows are addressed by 32-bit offsets from x. Where x is larger
-// than that its rows are gathered into the workspace first.
-static bool is_wide(const moe_matrix &x, int64_t tokens) {
-  return tokens * x.ld * 2 >= 0xfffff000ll;
+// Gathered rows are addressed by 32-bit offsets from what the product reads: x,
+// or the padded copy that operand() makes of it, whose rows may be longer than
+// x's own. Where that is larger than they reach, the rows are gathered into the
+// workspace first.
+static bool is_wide(const moe_matrix &x, int64_t tokens, int cols) {
+  const int64_t copy_ld = is_aligned(x, cols, 1) ? 0 : round8(cols);
+  return tokens * (x.ld > copy_ld ? x.ld : copy_ld) * 2 >= 0xfffff000ll;
 }
 static Operand gathered(const moe_matrix &x, int64_t tokens, int cols, const Rows &r,
                         int64_t rows, Arena &a, hipStream_t st, int *status) {
@@ -332,7 +335,7 @@ static int run_gated(const moe_gated_ffn_args *a, Arena &ws, hipStream_t st) {
   Operand x;
   if (direct) {
     x = as_is(a->x);
-  } else if (gather && is_wide(a->x, a->tokens)) {
+  } else if (gather && is_wide(a->x, a->tokens, H)) {
     x = gathered(a->x, a->tokens, H, g.r, rows, ws, st, &status);
     g.r.row_entry = nullptr;
     g.a_rows = rows;
@@ -361,7 +364,7 @@ static int run_gated_backward(const moe_gated_ffn_args *a, Arena &ws, hipStream_
   Operand x = {}, wg = {}, wu = {};
   GemmArgs g = gemm_args(a->rows, rows, gather);
   const bool few = a->dw_gate.p && few_rows(a->rows, rows);
-  const bool wide = gather && is_wide(a->x, a->tokens);
+  const bool wide = gather && is_wide(a->x, a->tokens, H);
   if (a->dw_gate.p && !few && wide) x = gathered(a->x, a->tokens, H, g.r, rows, ws, st, &status);
   if (a->dw_gate.p && !few && !wide) x = operand(a->x, a->tokens, H, 1, ws, st, &status);
   if (a->dx.p && rows > 0) {

@@ -1,0 +1,83 @@
+"""Host-side decisions of the feed-forward operators at unusual sizes, with no
+GPU: seen through the workspace sizes, which differ between the ways that a
+call may take."""
+import ctypes
+import os
+
+import pytest
+
+import moe_expert_routing_amd as M
+from moe_expert_routing_amd import ffn
+
+P = 0x10000  # a pointer that nothing here dereferences
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(M.LIB_PATH):
+        pytest.skip("library not built")
+    return M.lib()
+
+
+def mat(rows, cols, mats=1, p=P, ld=None):
+    ld = cols if ld is None else ld
+    return ffn.Matrix(p, ld, rows * ld if mats > 1 else 0)
+
+
+def rows_of(rows, experts, tile, top_k=2, entry=P):
+    return ffn.ExpertRows(P, P, P, entry, rows, experts, tile, top_k)
+
+
+def a256(nbytes):
+    return (nbytes + 255) // 256 * 256
+
+
+def up8(n):
+    return (n + 7) // 8 * 8
+
+
+def expert_gated(tokens, hidden, inter, rows, experts, tile, backward=False, grads=("dx", "dw"),
+                 x=None):
+    w = mat(inter, hidden, experts)
+    none = ffn.Matrix()
+    return ffn.GatedFfnArgs(
+        0, 1, tokens, hidden, inter, rows_of(rows, experts, tile),
+        x or mat(tokens, hidden), w, w, mat(rows, inter), mat(rows, 2 * inter),
+        mat(rows, inter) if backward else none,
+        mat(rows, hidden) if backward and "dx" in grads else none,
+        *([w, w] if backward and "dw" in grads else [none, none]))
+
+
+# tokens, hidden, where the row of a token can lie past 4 GB in what the product reads:
+# x itself, or the copy of it with its rows padded to 8 elements
+WIDE = [
+    (2_130_000, 1001, False), (2_131_000, 1001, True), (2_140_000, 1001, True),
+    (2_146_000, 1001, True), (1_048_000, 2047, False), (1_049_000, 2047, True),
+    (30_000_000, 65, True), (299_500, 7161, False), (299_700, 7161, True), (299_700, 7160, False),
+]
+
+
+@pytest.mark.parametrize("tokens,hidden,wide", WIDE)
+def test_gathered_rows_of_a_copy_beyond_32_bits(L, tokens, hidden, wide):
+    """Where a padded copy of x would be past what 32-bit offsets reach, the rows
+    are gathered first: rows x width of workspace, not tokens x width."""
+    rows, n, inter, tile = 4096, 8, 64, 256
+    h8 = up8(hidden)
+    weights = 0 if hidden == h8 else 2 * a256(n * inter * h8 * 2)
+    x = a256((rows if wide else tokens) * h8 * 2) if wide or hidden != h8 else 0
+    a = expert_gated(tokens, hidden, inter, rows, n, tile)
+    assert L.moe_gated_ffn_workspace_bytes(ctypes.byref(a), 0) == x + weights
+    dz = a256(rows * 2 * inter * 2)
+    a = expert_gated(tokens, hidden, inter, rows, n, tile, True, ("dw",))
+    assert L.moe_gated_ffn_workspace_bytes(ctypes.byref(a), 1) == dz + x
+
+
+def test_misaligned_x_counts_as_its_copy(L):
+    """x a few elements off the 16-byte grid, contiguous: 4 GB is its copy's size."""
+    tokens, rows, n = 2_131_000, 4096, 8
+    for hidden, wide in ((1004, True), (1001, True), (992, False)):
+        h8 = up8(hidden)
+        a = expert_gated(tokens, hidden, 64, rows, n, 256, x=mat(tokens, hidden, p=P + 2))
+        weights = 0 if hidden == h8 else 2 * a256(n * 64 * h8 * 2)
+        assert L.moe_gated_ffn_workspace_bytes(ctypes.byref(a), 0) == \
+            a256((rows if wide else tokens) * h8 * 2) + weights
