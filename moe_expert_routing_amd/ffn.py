@@ -19,7 +19,9 @@ of their own; nothing is kept between calls.
 
 ``lay`` is what ``route_local_grouped`` returns (or a dict with the same
 names from ``route_local`` and ``grouped_layout``). Its m_indices and
-row_entry may be cut to the rows that the caller's buffers have.
+row_entry may be cut to the rows that the caller's buffers have. ``ws``, a
+contiguous tensor on the operands' device, is a workspace of the caller's own;
+without it a call that needs one takes one for itself.
 """
 from __future__ import annotations
 
@@ -113,7 +115,9 @@ class _Entry:
         if self.size is None:
             st = self.fn(args, stream)
         elif ws is not None:
-            st = self.fn(args, ws.data_ptr(), ws.numel(), stream)
+            if not isinstance(ws, torch.Tensor) or ws.device != dev or not ws.is_contiguous():
+                _fail(f"ws must be a contiguous tensor on {dev}")
+            st = self.fn(args, ws.data_ptr(), ws.numel() * ws.element_size(), stream)
         else:
             st = self.fn(args, None, 0, stream)
             if st == _ERR_WORKSPACE:
