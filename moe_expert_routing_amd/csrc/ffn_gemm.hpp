@@ -187,6 +187,7 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
       const int64_t p0 = g.r.padded_offsets[e], cnt = g.r.counts[e];
       k_row0 = min(max(p0, (int64_t)0), g.r.rows);
       K = (int)min(max(cnt, (int64_t)0), g.r.rows - k_row0);
+      if (GATHER && g.a_rows == 0) K = 0;  // not even a row 0 to gather
     }
   } else {
     int live = g.m_tiles;  // m-tiles with rows of the experts here

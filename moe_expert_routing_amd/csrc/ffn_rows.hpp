@@ -237,6 +237,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void few_rows_dw_kernel(const FewRo
   if (a.r.num_experts > 0) {
     first = min(max((int64_t)a.r.padded_offsets[e], (int64_t)0), a.rows);
     n = min(max((int64_t)a.r.counts[e], (int64_t)0), a.rows - first);
+    if (a.r.row_entry && a.x_rows == 0) n = 0;  // not even a row 0 to gather
   }
   f32x8 acc[FEW_F];
 #pragma unroll

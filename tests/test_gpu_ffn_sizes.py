@@ -3,7 +3,8 @@ or an even spread of the rows would allow."""
 import pytest
 import torch
 
-from ffn_util import normal
+import moe_expert_routing_amd as M
+from ffn_util import assert_close, gated_grads, groups, hand_layout, normal
 from test_gpu_ffn import check_expert_gated
 
 pytestmark = [
@@ -33,3 +34,25 @@ def test_gathered_tiles_beyond_32_bits(T, H):
     lay = dict(m_indices=m, row_entry=entry, counts=torch.tensor([104, 96], **i32),
                padded_offsets=torch.tensor([0, 128, 256], **i32))
     check_expert_gated(lay, n, 1, x, 64, tile, BF)
+
+
+@pytest.mark.parametrize("T", [12, 400])  # weight gradients of few rows, and on the matrix cores
+def test_layout_of_tokens_that_x_does_not_have(T):
+    """x of no rows with a layout of entries: nothing to gather, so h and the weight
+    gradients are zeros; dx is made of the rows alone and is whole."""
+    n, H, F, tile = 3, 72, 40, 16
+    ids = torch.randint(0, n, (T, 1), generator=torch.Generator().manual_seed(T))
+    lay = hand_layout(ids, n, tile)
+    rows = lay["m_indices"].numel()
+    x, dt = normal(1, 0, H, dt=BF), BF
+    wg, wu = normal(2, n, F, H, dt=dt), normal(3, n, F, H, dt=dt)
+    pre, dh = normal(4, rows, 2 * F, dt=dt), normal(5, rows, F, dt=dt)
+    kw = dict(tile_m=tile, top_k=1)
+    r = M.expert_gated_ffn(x, wg, wu, lay, save_pre=True, **kw)
+    assert not bool(r["h"].any()) and not bool(r["pre"].any())
+    b = M.expert_gated_ffn_backward(dh, pre, x, wg, wu, lay, **kw)
+    assert not bool(b["dw_gate"].any()) and not bool(b["dw_up"].any())
+    some = normal(6, T, H, dt=dt)
+    for e, at, tok in groups(lay, n, rows, 1):
+        ref, bd = gated_grads(dh[at], pre[at], some[tok], wg[e], wu[e], "silu", dt)["dx"]
+        assert_close(b["dx"][at], ref, bd, f"dx of {e}")
