@@ -54,10 +54,11 @@ typedef enum moe_dtype { MOE_BF16 = 0, MOE_F16 = 1 } moe_dtype;
 /* silu: z / (1 + e^-z). gelu: z (1 + erf(z / sqrt 2)) / 2. */
 typedef enum moe_activation { MOE_ACT_NONE = 0, MOE_ACT_SILU = 1, MOE_ACT_GELU = 2 } moe_activation;
 
-/* Envelope: widths (hidden, inter, out) 1 .. 2^20, tokens and rows up to
- * 2^31 - 1, ld up to 2^22 elements, at most 4096 experts, tile_m a multiple of 16
- * up to MOE_GROUPED_MAX_TILE. */
+/* Envelope: widths (hidden, inter, out) 1 .. 2^20, tokens and rows up to 2^30,
+ * ld up to 2^22 elements, at most 4096 experts, tile_m a multiple of 16 up to
+ * MOE_GROUPED_MAX_TILE. What lies beyond is refused with MOE_ERR_UNSUPPORTED. */
 #define MOE_FFN_MAX_WIDTH (1 << 20)
+#define MOE_FFN_MAX_ROWS (1 << 30)
 #define MOE_FFN_MAX_LD (1 << 22)
 #define MOE_FFN_MAX_EXPERTS 4096
 

@@ -5,7 +5,7 @@
 
 namespace moe_ffn {
 
-static const int64_t MAX_ROWS = (int64_t)1 << 30;
+static const int64_t MAX_ROWS = MOE_FFN_MAX_ROWS;
 
 static int round8(int v) { return (v + 7) & ~7; }
 static size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -618,25 +618,29 @@ int moe_linear_backward(const moe_linear_args *a, void *workspace, size_t worksp
 int moe_combine(const moe_combine_args *a, void *stream) {
   using namespace moe_ffn;
   MOE_TRY(check_combine(a, false));
-  if (a->tokens == 0) return MOE_OK;
-  const CombineArgs c = combine_args(a);
+  CombineArgs c = combine_args(a);
   const int y = (round8(a->width) / 8 + COMBINE_THREADS - 1) / COMBINE_THREADS;
   const auto kernel = a->dtype == MOE_BF16 ? combine_kernel<Bf16> : combine_kernel<F16>;
-  kernel<<<dim3((uint32_t)a->tokens, y), COMBINE_THREADS, 0, (hipStream_t)stream>>>(c);
-  return hip_status();
+  return in_parts(a->tokens, COMBINE_THREADS, [&](int64_t first, uint32_t n) {
+    c.block0 = first;
+    kernel<<<dim3(n, y), COMBINE_THREADS, 0, (hipStream_t)stream>>>(c);
+    return hip_status();
+  });
 }
 int moe_combine_backward(const moe_combine_args *a, void *stream) {
   using namespace moe_ffn;
   MOE_TRY(check_combine(a, true));
-  const CombineArgs c = combine_args(a);
+  CombineArgs c = combine_args(a);
   int64_t blocks = a->rows;
   if (a->dweights)
     blocks += (a->tokens * a->top_k + COMBINE_THREADS - 1) / COMBINE_THREADS;
-  if (blocks == 0) return MOE_OK;
   const auto kernel =
       a->dtype == MOE_BF16 ? combine_backward_kernel<Bf16> : combine_backward_kernel<F16>;
-  kernel<<<dim3((uint32_t)blocks), COMBINE_THREADS, 0, (hipStream_t)stream>>>(c);
-  return hip_status();
+  return in_parts(blocks, COMBINE_THREADS, [&](int64_t first, uint32_t n) {
+    c.block0 = first;
+    kernel<<<n, COMBINE_THREADS, 0, (hipStream_t)stream>>>(c);
+    return hip_status();
+  });
 }
 
 }  // extern "C"

@@ -171,6 +171,7 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const bool grouped = g.r.num_experts > 0;
 
+  const uint32_t block = blockIdx.x + g.block0;
   int mt, nt, e = 0, seg0 = 0;
   int64_t k_row0 = 0;  // WGRAD: first row of the expert, or of the k range
   int split = 0, k0 = 0;  // the others: first k of the range
@@ -178,9 +179,9 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
   if constexpr (MODE == WGRAD) {
     // one expert and projection after the other, all its tiles together
     const int per = g.m_tiles * g.n_tiles;
-    const int chunk = blockIdx.x / per % (g.segs * max(1, g.r.num_experts));
-    split = blockIdx.x / per / (g.segs * max(1, g.r.num_experts));
-    tile_at(tile_of_block(blockIdx.x % per, per, per), g.m_tiles, g.n_tiles, mt, nt);
+    const int chunk = block / per % (g.segs * max(1, g.r.num_experts));
+    split = block / per / (g.segs * max(1, g.r.num_experts));
+    tile_at(tile_of_block(block % per, per, per), g.m_tiles, g.n_tiles, mt, nt);
     e = chunk / g.segs;
     seg0 = chunk % g.segs;
     if (grouped) {
@@ -198,8 +199,8 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
       live = (int)min((int64_t)g.m_tiles, (max(end, (int64_t)0) + BM - 1) / BM);
     }
     const int per = g.m_tiles * g.n_tiles;  // split: all tiles of one k range together
-    split = blockIdx.x / per;
-    const int t = tile_of_block(blockIdx.x % per, per, live * g.n_tiles);
+    split = block / per;
+    const int t = tile_of_block(block % per, per, live * g.n_tiles);
     if (t < live * g.n_tiles) {
       tile_at(t, live, g.n_tiles, mt, nt);
     } else {

@@ -24,17 +24,15 @@ static int launch(GemmArgs g, hipStream_t st) {
   int64_t blocks = (int64_t)g.m_tiles * g.n_tiles;
   if (MODE == WGRAD) blocks *= (int64_t)(g.r.num_experts > 0 ? g.r.num_experts : 1) * g.segs;
   if (g.partial) blocks *= g.splits;
-  if (blocks == 0) return MOE_OK;
   if (blocks > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
-  const dim3 grid((uint32_t)blocks), block(C::NTHREADS);
-  if constexpr (MODE == GATED || MODE == WGRAD) {
-    if (g.r.row_entry) {
-      gemm_kernel<D, MODE, C, true><<<grid, block, 0, st>>>(g);
-      return hip_status();
-    }
-  }
-  gemm_kernel<D, MODE, C, false><<<grid, block, 0, st>>>(g);
-  return hip_status();
+  auto kernel = gemm_kernel<D, MODE, C, false>;
+  if constexpr (MODE == GATED || MODE == WGRAD)
+    if (g.r.row_entry) kernel = gemm_kernel<D, MODE, C, true>;
+  return in_parts(blocks, C::NTHREADS, [&](int64_t first, uint32_t n) {
+    g.block0 = (uint32_t)first;
+    kernel<<<n, C::NTHREADS, 0, st>>>(g);
+    return hip_status();
+  });
 }
 
 template <class D, int MODE, int KW>
@@ -43,14 +41,14 @@ static int launch_skinny_kw(GemmArgs g, hipStream_t st) {
   g.m_tiles = (g.M + 15) / 16;
   g.n_tiles = (g.N + COLS - 1) / COLS;
   const int64_t blocks = (int64_t)g.m_tiles * g.n_tiles;
-  if (blocks == 0) return MOE_OK;
   if (blocks > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
-  const dim3 grid((uint32_t)blocks), block(64 * SKINNY_WAVES);
-  if (MODE == GATED && g.r.row_entry)
-    skinny_kernel<D, MODE, 1, KW, 4, MODE == GATED><<<grid, block, 0, st>>>(g);
-  else
-    skinny_kernel<D, MODE, 1, KW, 4, false><<<grid, block, 0, st>>>(g);
-  return hip_status();
+  const auto kernel = MODE == GATED && g.r.row_entry ? skinny_kernel<D, MODE, 1, KW, 4, MODE == GATED>
+                                                     : skinny_kernel<D, MODE, 1, KW, 4, false>;
+  return in_parts(blocks, 64 * SKINNY_WAVES, [&](int64_t first, uint32_t n) {
+    g.block0 = (uint32_t)first;
+    kernel<<<n, 64 * SKINNY_WAVES, 0, st>>>(g);
+    return hip_status();
+  });
 }
 // Waves that share weight rows. Dense calls have few blocks: all 8, or 4 where
 // that already gives more than one block and a half for each compute unit

@@ -342,6 +342,7 @@ struct CombineArgs {
   uint16_t *out, *dy;
   int64_t ld_y, ld_res, ld_out, ld_dout, ld_dy;
   float *dweights;
+  int64_t block0;  // number of the launch's first block
 };
 
 // Row of an entry, or -1 where it is left out.
@@ -362,7 +363,7 @@ __global__ __launch_bounds__(COMBINE_THREADS) void combine_kernel(const CombineA
   __shared__ int64_t rows[COMBINE_MAX_TOPK];
   __shared__ float ws[COMBINE_MAX_TOPK];
   __shared__ int n_rows;
-  const int64_t t = blockIdx.x;
+  const int64_t t = a.block0 + blockIdx.x;
   if (threadIdx.x < 64) {
     const int k = threadIdx.x;
     int64_t row = -1;
@@ -401,7 +402,7 @@ __global__ __launch_bounds__(COMBINE_THREADS) void combine_kernel(const CombineA
 template <class D>
 __global__ __launch_bounds__(COMBINE_THREADS) void combine_backward_kernel(const CombineArgs a) {
   __shared__ float part[COMBINE_THREADS / 64];
-  const int64_t row = blockIdx.x;
+  const int64_t row = a.block0 + blockIdx.x;
   if (row >= a.rows) {
     const int64_t i = (row - a.rows) * COMBINE_THREADS + threadIdx.x;
     if (i < a.tokens * a.top_k && entry_row(a, i) < 0) a.dweights[i] = 0.f;

@@ -33,7 +33,8 @@ __global__ __launch_bounds__(64 * SKINNY_WAVES) void skinny_kernel(const GemmArg
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kw = wave % KW, gw = wave / KW;
   const bool grouped = g.r.num_experts > 0;
-  const int nt = blockIdx.x % g.n_tiles, mt = blockIdx.x / g.n_tiles;
+  const uint32_t block = blockIdx.x + g.block0;
+  const int nt = block % g.n_tiles, mt = block / g.n_tiles;
   const int m0 = mt * BM, n0 = nt * GW * NC;
   int e = 0;
   bool live = true;

@@ -206,6 +206,7 @@ struct GemmArgs {
   int32_t splits, k_split;
   float *partial;
   uint32_t top_k_magic, top_k_shift; // entry / top_k as a product; magic 0: top_k is 1
+  uint32_t block0;         // number of the launch's first block
 };
 
 }  // namespace moe_ffn

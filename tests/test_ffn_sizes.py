@@ -3,6 +3,7 @@ GPU: seen through the workspace sizes, which differ between the ways that a
 call may take."""
 import ctypes
 import os
+import re
 
 import pytest
 
@@ -81,3 +82,27 @@ def test_misaligned_x_counts_as_its_copy(L):
         weights = 0 if hidden == h8 else 2 * a256(n * 64 * h8 * 2)
         assert L.moe_gated_ffn_workspace_bytes(ctypes.byref(a), 0) == \
             a256((rows if wide else tokens) * h8 * 2) + weights
+
+
+def test_the_headers_envelope_is_the_codes(L):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "include", "moe_ffn.h")).read()
+    most = 1 << int(re.search(r"#define MOE_FFN_MAX_ROWS \(1 << (\d+)\)", text).group(1))
+    assert re.search(r"tokens and rows up to 2\^%d\b" % (most.bit_length() - 1), text)
+
+    def linear(rows, experts=0):
+        w = mat(64, 64, max(1, experts))
+        none = ffn.Matrix()
+        desc = rows_of(rows, experts, 16) if experts else ffn.ExpertRows()
+        return ffn.LinearArgs(0, 0, rows, 64, 64, desc, mat(rows, 64), w, none, none, mat(rows, 64),
+                              none, none, none, none, none)
+    for experts in (0, 4):
+        size = [L.moe_linear_workspace_bytes(ctypes.byref(linear(n, experts)), 0)
+                for n in (most, most + 1)]
+        assert size[0] >= 0 and size[1] == -1
+    for kw in (dict(tokens=most + 1, rows=1), dict(tokens=1, rows=most + 1)):
+        y = mat(1, 64)
+        a = ffn.CombineArgs(0, 64, kw["tokens"], kw["rows"], 1, 4, 8, P, P, P, P, P, P, P, y, y, y,
+                            y, y, P)
+        assert L.moe_combine(ctypes.byref(a), None) == -4
+        assert L.moe_combine_backward(ctypes.byref(a), None) == -4

@@ -4,7 +4,8 @@ import pytest
 import torch
 
 import moe_expert_routing_amd as M
-from ffn_util import assert_close, gated_grads, groups, hand_layout, normal
+from ffn_util import (F32, TINY, assert_close, gated_grads, gated_oracle, groups, hand_layout,
+                      normal)
 from test_gpu_ffn import check_expert_gated
 
 pytestmark = [
@@ -56,3 +57,45 @@ def test_layout_of_tokens_that_x_does_not_have(T):
     for e, at, tok in groups(lay, n, rows, 1):
         ref, bd = gated_grads(dh[at], pre[at], some[tok], wg[e], wu[e], "silu", dt)["dx"]
         assert_close(b["dx"][at], ref, bd, f"dx of {e}")
+
+
+def test_combine_of_more_rows_than_one_grid_takes():
+    """2^24 tokens and more, one block each: a launch's 2^32 work items hold 2^24 - 1
+    of them. Each entry has weight 1, so the rows come back as they are."""
+    T, W, n = (1 << 24) + 77, 8, 3
+    ids = torch.randint(0, n, (T, 1), device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+    lay = hand_layout(ids, n, 16)
+    real = lay["row_entry"] >= 0
+    entry = lay["row_entry"][real].long()
+    y = normal(1, real.numel(), W, dt=BF)
+    want = torch.empty((T, W), dtype=BF, device="cuda")
+    want[entry] = y[real]
+    assert torch.equal(M.combine(y, lay, num_experts=n), want)
+    dout = normal(2, T, W, dt=BF)
+    r = M.combine_backward(dout, y, lay, num_experts=n)
+    assert torch.equal(r["dy"][real], dout[entry]) and not bool(r["dy"][~real].any())
+    d, v = dout[entry].double(), y[real].double()
+    S = (d * v).abs().sum(1)
+    assert_close(r["dweights"][entry, 0], (d * v).sum(1), (W + 8) * F32 * S + TINY[torch.float32], "dw")
+    # and entries without a row, past the rows' blocks: their gradient is 0
+    half = {**lay, "m_indices": lay["m_indices"][:64], "row_entry": lay["row_entry"][:64]}
+    r = M.combine_backward(dout, y[:64], half, num_experts=n)
+    kept = torch.zeros(T, dtype=torch.bool, device="cuda")
+    kept[half["row_entry"][half["row_entry"] >= 0].long()] = True
+    assert not bool(r["dweights"][~kept].any()) and bool(r["dweights"][kept].all())
+
+
+def test_product_of_more_tiles_than_one_grid_takes():
+    """4096 experts of 64 rows, 32832 wide: 2^23 blocks of 512 threads and some."""
+    n, each, H, F = 4096, 64, 8, 32832
+    T = n * each
+    ids = (torch.arange(T, device="cuda") // each)[:, None]
+    lay = hand_layout(ids, n, 16)
+    x = normal(1, T, H, dt=BF)
+    g = torch.Generator("cuda").manual_seed(2)
+    w = torch.randn((n, F, H), device="cuda", dtype=BF, generator=g)
+    r = M.expert_gated_ffn(x, w, w, lay, tile_m=16, top_k=1)
+    for e in (0, 1, 2047, 4094, 4095):
+        at = slice(e * each, (e + 1) * each)
+        h, bh, _, _ = gated_oracle(x[at], w[e], w[e], "silu", BF)
+        assert_close(r["h"][at], h, bh, f"h of {e}")
