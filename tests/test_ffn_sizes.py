@@ -106,3 +106,28 @@ def test_the_headers_envelope_is_the_codes(L):
                             y, y, P)
         assert L.moe_combine(ctypes.byref(a), None) == -4
         assert L.moe_combine_backward(ctypes.byref(a), None) == -4
+
+
+# experts, tile, rows of the layout: whether its experts may be taken to have few rows. The
+# few-row products read odd widths in place, the tiles read padded copies.
+FEW = [
+    (64, 256, 4096, False),     # exact, two experts with 2000 rows each
+    (64, 256, 16384, False),    # every expert half a tile on average
+    (64, 4096, 4096, False),    # one expert with up to 4096
+    (64, 16, 1024, True),       # decode: a tile an expert
+    (112, 16, 1776, True),      # the same with buffers of fixed size
+    (112, 16, 96, True),        # a few of the experts
+]
+
+
+@pytest.mark.parametrize("experts,tile,rows,few", FEW)
+def test_experts_without_entries_have_no_padding(L, experts, tile, rows, few):
+    """At most rows / tile experts have rows, and only those have padding to take off
+    the estimate of what an expert has."""
+    H, F = 1001, 64
+    a = expert_gated(5000, H, F, rows, experts, tile)
+    got = L.moe_gated_ffn_workspace_bytes(ctypes.byref(a), 0)
+    assert (got == 0) == few
+    a = expert_gated(5000, H, F, rows, experts, tile, True, ("dw",))
+    got = L.moe_gated_ffn_workspace_bytes(ctypes.byref(a), 1)
+    assert (got < a256(5000 * up8(H) * 2)) == few

@@ -99,3 +99,12 @@ def test_product_of_more_tiles_than_one_grid_takes():
         at = slice(e * each, (e + 1) * each)
         h, bh, _, _ = gated_oracle(x[at], w[e], w[e], "silu", BF)
         assert_close(r["h"][at], h, bh, f"h of {e}")
+
+
+@pytest.mark.parametrize("n,tile,live,each", [(64, 256, 2, 700), (32, 4096, 1, 900), (64, 64, 10, 40),
+                                              (48, 128, 9, 3), (64, 16, 1, 500)])
+def test_few_of_the_experts_have_rows(n, tile, live, each):
+    """Tight layouts in which most experts have no rows."""
+    ids = (torch.arange(live * each) % live * (n // live))[:, None]
+    lay = hand_layout(ids, n, tile)
+    check_expert_gated(lay, n, 1, normal(1, live * each, 136, dt=BF), 72, tile, BF)
