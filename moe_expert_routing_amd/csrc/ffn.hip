@@ -369,10 +369,11 @@ static int run_gated_backward(const moe_gated_ffn_args *a, Arena &ws, hipStream_
   const int H = a->hidden, F = a->inter, Fa = round8(F);
   const bool gather = a->rows.num_experts > 0 && a->rows.row_entry;
   int status = MOE_OK;
-  uint16_t *dz = ws.take((size_t)rows * 2 * Fa * 2);
   Operand x = {}, wg = {}, wu = {};
   GemmArgs g = gemm_args(a->rows, rows, gather);
   const bool few = a->dw_gate.p && few_rows(a->rows, rows);
+  const bool products = a->dx.p || (a->dw_gate.p && !few);
+  uint16_t *dz = products ? ws.take((size_t)rows * 2 * Fa * 2) : nullptr;
   const bool wide = gather && is_wide(a->x, a->tokens, H);
   if (a->dw_gate.p && !few && wide) x = gathered(a->x, a->tokens, H, g.r, rows, ws, st, &status);
   if (a->dw_gate.p && !few && !wide) x = operand(a->x, a->tokens, H, 1, ws, st, &status);
@@ -384,7 +385,7 @@ static int run_gated_backward(const moe_gated_ffn_args *a, Arena &ws, hipStream_
     wu = operand(a->w_up, F, H, mats, ws, st, &status, copy);
   }
   if (status != MOE_OK) return status;
-  if (rows > 0 && (a->dx.p || !few) && !ws.dry) {
+  if (rows > 0 && products && !ws.dry) {
     const dim3 grid = row_grid(rows, Fa, 1), block(COL_THREADS, ROW_THREADS);
     const auto kernel = a->dtype == MOE_BF16 ? gated_dz_kernel<Bf16> : gated_dz_kernel<F16>;
     kernel<<<grid, block, 0, st>>>((const uint16_t *)a->dh.p, a->dh.ld,

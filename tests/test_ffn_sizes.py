@@ -131,3 +131,15 @@ def test_experts_without_entries_have_no_padding(L, experts, tile, rows, few):
     a = expert_gated(5000, H, F, rows, experts, tile, True, ("dw",))
     got = L.moe_gated_ffn_workspace_bytes(ctypes.byref(a), 1)
     assert (got < a256(5000 * up8(H) * 2)) == few
+
+
+@pytest.mark.parametrize("rows,experts", [(8, 0), (1, 0), (1024, 64)])
+def test_weight_gradients_of_few_rows_need_no_workspace(L, rows, experts):
+    """They are made from dh and pre; the pre-activations' gradient is for dx alone."""
+    H, F = 1001, 72
+    a = expert_gated(rows, H, F, rows, max(1, experts), 16, True, ("dw",))
+    if not experts:
+        a.rows = ffn.ExpertRows()
+    assert L.moe_gated_ffn_workspace_bytes(ctypes.byref(a), 1) == 0
+    a.dx = mat(rows, H)
+    assert L.moe_gated_ffn_workspace_bytes(ctypes.byref(a), 1) >= rows * 2 * F * 2
