@@ -25,9 +25,12 @@ static int launch(GemmArgs g, hipStream_t st) {
   if (MODE == WGRAD) blocks *= (int64_t)(g.r.num_experts > 0 ? g.r.num_experts : 1) * g.segs;
   if (g.partial) blocks *= g.splits;
   if (blocks > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
-  auto kernel = gemm_kernel<D, MODE, C, false>;
-  if constexpr (MODE == GATED || MODE == WGRAD)
-    if (g.r.row_entry) kernel = gemm_kernel<D, MODE, C, true>;
+  // the forward tiles of dense_plan alone never gather
+  constexpr bool DENSE = std::is_same_v<C, Tile128> || std::is_same_v<C, Tile64>;
+  constexpr bool GATHERS = MODE == WGRAD || (MODE == GATED && !DENSE);
+  if (!GATHERS && g.r.row_entry) return MOE_ERR_UNSUPPORTED;
+  const auto kernel =
+      g.r.row_entry ? gemm_kernel<D, MODE, C, GATHERS> : gemm_kernel<D, MODE, C, false>;
   return in_parts(blocks, C::NTHREADS, [&](int64_t first, uint32_t n) {
     g.block0 = (uint32_t)first;
     kernel<<<n, C::NTHREADS, 0, st>>>(g);
@@ -42,8 +45,10 @@ static int launch_skinny_kw(GemmArgs g, hipStream_t st) {
   g.n_tiles = (g.N + COLS - 1) / COLS;
   const int64_t blocks = (int64_t)g.m_tiles * g.n_tiles;
   if (blocks > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
-  const auto kernel = MODE == GATED && g.r.row_entry ? skinny_kernel<D, MODE, 1, KW, 4, MODE == GATED>
-                                                     : skinny_kernel<D, MODE, 1, KW, 4, false>;
+  constexpr bool GATHERS = MODE == GATED && KW < 8;  // 8 waves: dense calls alone
+  if (!GATHERS && g.r.row_entry) return MOE_ERR_UNSUPPORTED;
+  const auto kernel =
+      g.r.row_entry ? skinny_kernel<D, MODE, KW, 4, GATHERS> : skinny_kernel<D, MODE, KW, 4, false>;
   return in_parts(blocks, 64 * SKINNY_WAVES, [&](int64_t first, uint32_t n) {
     g.block0 = (uint32_t)first;
     kernel<<<n, 64 * SKINNY_WAVES, 0, st>>>(g);

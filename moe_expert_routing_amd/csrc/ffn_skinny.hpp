@@ -23,12 +23,11 @@ namespace moe_ffn {
 
 constexpr int SKINNY_WAVES = 8;
 
-// rows of a block: 16 RX
-template <class D, int MODE, int RX, int KW, int U, bool GATHER>
+template <class D, int MODE, int KW, int U, bool GATHER>
 __global__ __launch_bounds__(64 * SKINNY_WAVES) void skinny_kernel(const GemmArgs g) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  constexpr int GW = SKINNY_WAVES / KW, NC = MODE == GATED ? 8 : 16, BM = 16 * RX;
-  __shared__ __attribute__((aligned(16))) float part[SKINNY_WAVES][RX][16][20];
+  constexpr int GW = SKINNY_WAVES / KW, NC = MODE == GATED ? 8 : 16, BM = 16;
+  __shared__ __attribute__((aligned(16))) float part[SKINNY_WAVES][BM][20];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kw = wave % KW, gw = wave / KW;
@@ -43,9 +42,7 @@ __global__ __launch_bounds__(64 * SKINNY_WAVES) void skinny_kernel(const GemmArg
     live = e >= 0 && e < g.r.num_experts && g.a_rows > 0;
   }
   const int K = g.K, fr = lane & 15, fq = lane >> 4;
-  f32x4 acc[RX];
-#pragma unroll
-  for (int x = 0; x < RX; ++x) acc[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 
   if (live) {
     // whole k-steps, handed out in pairs so that waves part at 128-byte lines
@@ -56,33 +53,25 @@ __global__ __launch_bounds__(64 * SKINNY_WAVES) void skinny_kernel(const GemmArg
     const uint16_t *w = second ? g.b1 + e * g.b_stride1 + (int64_t)min(nb, g.N - 1) * g.ldb1
                                : g.b0 + e * g.b_stride0 + (int64_t)min(nb, g.N - 1) * g.ldb0;
     w += s0 * 32 + fq * 8;
-    const uint16_t *xr[RX];
     const uint32_t magic = g.top_k_magic, shift = g.top_k_shift;
-#pragma unroll
-    for (int x = 0; x < RX; ++x) {
-      int64_t row = min(m0 + 16 * x + fr, g.M - 1);
-      if (GATHER) {
-        const uint32_t en = (uint32_t)g.r.row_entry[row];
-        const uint32_t t = magic ? __umulhi(en, magic) >> shift : en;
-        row = t < (uint64_t)g.a_rows ? t : 0;
-      }
-      xr[x] = g.a + row * g.lda + s0 * 32 + fq * 8;
+    int64_t row = min(m0 + fr, g.M - 1);
+    if (GATHER) {
+      const uint32_t en = (uint32_t)g.r.row_entry[row];
+      const uint32_t t = magic ? __umulhi(en, magic) >> shift : en;
+      row = t < (uint64_t)g.a_rows ? t : 0;
     }
-    s16x8 fw[2][U], fx[2][U][RX];
+    const uint16_t *xr = g.a + row * g.lda + s0 * 32 + fq * 8;
+    s16x8 fw[2][U], fx[2][U];
     auto load = [&](int set, int s) MOE_INLINE {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         fw[set][u] = *reinterpret_cast<const s16x8_any *>(w + (s + u) * 32);
-#pragma unroll
-        for (int x = 0; x < RX; ++x)
-          fx[set][u][x] = *reinterpret_cast<const s16x8_any *>(xr[x] + (s + u) * 32);
+        fx[set][u] = *reinterpret_cast<const s16x8_any *>(xr + (s + u) * 32);
       }
     };
     auto multiply = [&](int set) MOE_INLINE {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int x = 0; x < RX; ++x) acc[x] = D::mfma(fw[set][u], fx[set][u][x], acc[x]);
+      for (int u = 0; u < U; ++u) acc = D::mfma(fw[set][u], fx[set][u], acc);
     };
     // batches whose last step lies inside K
     const int whole = max(0, (min(s1, K / 32) - s0) / U);
@@ -98,14 +87,10 @@ __global__ __launch_bounds__(64 * SKINNY_WAVES) void skinny_kernel(const GemmArg
     for (int s = whole * U; s < s1 - s0; ++s) {  // the rest, and K's own tail
       const int in = K - (s0 + s) * 32 - fq * 8;  // elements left in this lane's piece
       const s16x8 a = load8_raw(w + s * 32, 0, in);
-      s16x8 c[RX];
-#pragma unroll
-      for (int x = 0; x < RX; ++x) c[x] = load8_raw(xr[x] + s * 32, 0, in);
-#pragma unroll
-      for (int x = 0; x < RX; ++x) acc[x] = D::mfma(a, c[x], acc[x]);
+      const s16x8 c = load8_raw(xr + s * 32, 0, in);
+      acc = D::mfma(a, c, acc);
     }
-#pragma unroll
-    for (int x = 0; x < RX; ++x) *reinterpret_cast<f32x4 *>(&part[wave][x][fr][4 * fq]) = acc[x];
+    *reinterpret_cast<f32x4 *>(&part[wave][fr][4 * fq]) = acc;
   }
   __syncthreads();
   // eight columns of a row a thread
@@ -120,7 +105,7 @@ __global__ __launch_bounds__(64 * SKINNY_WAVES) void skinny_kernel(const GemmArg
     if (real) {
 #pragma unroll
       for (int k = 0; k < KW; ++k) {
-        const float *p = &part[gr * KW + k][r >> 4][r & 15][c];
+        const float *p = &part[gr * KW + k][r][c];
 #pragma unroll
         for (int v = 0; v < 8; ++v) {
           z[v] += p[v];
