@@ -194,6 +194,14 @@ def _index(t, name: str, dev, least: int = 0) -> int:
     return t.data_ptr()
 
 
+def _zeros(out: Dict[str, torch.Tensor], *names: str) -> Dict[str, torch.Tensor]:
+    """The outputs of a call over no experts, checked like any other's."""
+    for n in names:
+        if out.get(n) is not None:
+            out[n].zero_()
+    return out
+
+
 _DENSE = (0, 0, 0, 0, 0, 0, 0, 0)
 
 
@@ -228,15 +236,12 @@ def _gated(x, w_gate, w_up, activation, save_pre, out, ws, lay, tile_m, top_k):
     if save_pre and out.get("pre") is None:
         out["pre"] = torch.empty((rows, 2 * inter), dtype=x.dtype, device=x.device)
     pre = out.get("pre") if save_pre else None
-    if lay is not None and lead[0] == 0:  # no experts here: every row is zero
-        for t in (out["h"], pre):
-            if t is not None:
-                t.zero_()
-        return out
     a = _PACK_GATED(d, act, tokens, hidden, inter, *desc, *_mat(x, "x", (tokens, hidden), x),
                     *_mat(w_gate, "w_gate", wshape, x), *_mat(w_up, "w_up", wshape, x),
                     *_mat(out["h"], "h", (rows, inter), x),
                     *_mat(pre, "pre", (rows, 2 * inter), x), *_NONE * 4)
+    if lay is not None and lead[0] == 0:  # no experts here: every row is zero
+        return _zeros(out, "h", "pre" if save_pre else "h")
     _GATED(a, x.device, ws)
     return out
 
@@ -280,16 +285,14 @@ def _gated_backward(dh, pre, x, w_gate, w_up, activation, out, ws, lay, tile_m, 
         out = {"dx": torch.empty((rows, hidden), dtype=x.dtype, device=x.device),
                "dw_gate": torch.empty(wshape, dtype=x.dtype, device=x.device),
                "dw_up": torch.empty(wshape, dtype=x.dtype, device=x.device)}
-    if lay is not None and lead[0] == 0:
-        if out.get("dx") is not None:
-            out["dx"].zero_()
-        return out
     a = _PACK_GATED(d, act, tokens, hidden, inter, *desc, *_mat(x, "x", (tokens, hidden), x),
                     *_mat(w_gate, "w_gate", wshape, x), *_mat(w_up, "w_up", wshape, x), *_NONE,
                     *_mat(pre, "pre", (rows, 2 * inter), x), *_mat(dh, "dh", (rows, inter), x),
                     *_mat(out.get("dx"), "dx", (rows, hidden), x),
                     *_mat(out.get("dw_gate"), "dw_gate", wshape, x),
                     *_mat(out.get("dw_up"), "dw_up", wshape, x))
+    if lay is not None and lead[0] == 0:
+        return _zeros(out, "dx")
     _GATED_BACKWARD(a, x.device, ws)
     return out
 
@@ -334,17 +337,14 @@ def _linear(x, w, bias, activation, residual, save_pre, out, ws, lay, tile_m):
     if save_pre and out.get("pre") is None:
         out["pre"] = torch.empty((rows, n_out), dtype=x.dtype, device=x.device)
     pre = out.get("pre") if save_pre else None
-    if lay is not None and lead[0] == 0:
-        for t in (out["y"], pre):
-            if t is not None:
-                t.zero_()
-        return out
     a = _PACK_LINEAR(d, act, rows, n_in, n_out, *desc, *_mat(x, "x", (rows, n_in), x),
                      *_mat(w, "w", (*lead, n_out, n_in), x),
                      *_vec(bias, "bias", (*lead, n_out), x),
                      *_mat(residual, "residual", (rows, n_out), x),
                      *_mat(out["y"], "y", (rows, n_out), x),
                      *_mat(pre, "pre", (rows, n_out), x), *_NONE * 4)
+    if lay is not None and lead[0] == 0:
+        return _zeros(out, "y", "pre" if save_pre else "y")
     _LINEAR(a, x.device, ws)
     return out
 
@@ -390,10 +390,6 @@ def _linear_backward(dy, x, w, pre, activation, bias_grad, out, ws, lay, tile_m)
                "dw": torch.empty(wshape, dtype=x.dtype, device=x.device)}
         if bias_grad:
             out["dbias"] = torch.empty((*lead, n_out), dtype=x.dtype, device=x.device)
-    if lay is not None and lead[0] == 0:
-        if out.get("dx") is not None:
-            out["dx"].zero_()
-        return out
     a = _PACK_LINEAR(d, act, rows, n_in, n_out, *desc, *_mat(x, "x", (rows, n_in), x),
                      *_mat(w, "w", wshape, x), *_NONE * 3,
                      *(_mat(pre, "pre", (rows, n_out), x) if act else _NONE),
@@ -401,6 +397,8 @@ def _linear_backward(dy, x, w, pre, activation, bias_grad, out, ws, lay, tile_m)
                      *_mat(out.get("dx"), "dx", (rows, n_in), x),
                      *_mat(out.get("dw"), "dw", wshape, x),
                      *_vec(out.get("dbias"), "dbias", (*lead, n_out), x))
+    if lay is not None and lead[0] == 0:
+        return _zeros(out, "dx")
     _LINEAR_BACKWARD(a, x.device, ws)
     return out
 
