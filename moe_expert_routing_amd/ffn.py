@@ -26,6 +26,7 @@ without it a call that needs one takes one for itself.
 from __future__ import annotations
 
 import ctypes
+import operator
 import struct
 from typing import Dict, Optional
 
@@ -194,6 +195,40 @@ def _index(t, name: str, dev, least: int = 0) -> int:
     return t.data_ptr()
 
 
+def _number(v, name: str) -> int:
+    try:
+        v = operator.index(v)
+    except TypeError:
+        _fail(f"{name} must be a whole number, not {v!r}")
+    if not -1 << 31 <= v < 1 << 31:
+        _fail(f"{name} must fit 32 bits")
+    return v
+
+
+def _of(lay, name: str):
+    """A tensor of the layout."""
+    t = lay.get(name)
+    if t is None:
+        _fail(f"the layout has no {name}")
+    return t
+
+
+def _out(out, name: str):
+    """An output that a caller's dict may not leave out."""
+    t = out.get(name)
+    if t is None:
+        _fail(f"out must have {name}")
+    return t
+
+
+def _lead(w, name: str, lay) -> torch.Size:
+    """() or (experts,), the leading dimensions of a weight."""
+    ndim = 2 if lay is None else 3
+    if not isinstance(w, torch.Tensor) or w.dim() != ndim:
+        _fail(f"{name} must be a tensor of {ndim} dimensions")
+    return w.shape[:-2]
+
+
 def _zeros(out: Dict[str, torch.Tensor], *names: str) -> Dict[str, torch.Tensor]:
     """The outputs of a call over no experts, checked like any other's."""
     for n in names:
@@ -206,25 +241,23 @@ _DENSE = (0, 0, 0, 0, 0, 0, 0, 0)
 
 
 def _rows(lay, n_experts: int, tile_m: int, top_k: int, dev, gather: bool) -> tuple:
-    m = lay["m_indices"]
+    m = _of(lay, "m_indices")
     p = _index(m, "m_indices", dev)
     rows = m.numel()
     entry = lay.get("row_entry") if gather else None
+    e = 0 if entry is None else _index(entry, "row_entry", dev)
     if entry is not None and entry.numel() != rows:
         _fail("row_entry must have as many elements as m_indices")
-    return (_index(lay["counts"], "counts", dev, n_experts),
-            _index(lay["padded_offsets"], "padded_offsets", dev, n_experts + 1),
-            p, 0 if entry is None else _index(entry, "row_entry", dev), rows, n_experts,
-            tile_m, top_k)
+    return (_index(_of(lay, "counts"), "counts", dev, n_experts),
+            _index(_of(lay, "padded_offsets"), "padded_offsets", dev, n_experts + 1),
+            p, e, rows, n_experts, _number(tile_m, "tile_m"), _number(top_k, "top_k"))
 
 
 def _gated(x, w_gate, w_up, activation, save_pre, out, ws, lay, tile_m, top_k):
     d = _first(x, "x")
     act = _activation(activation)
     tokens, hidden = x.shape
-    lead = w_gate.shape[:-2]
-    if w_gate.dim() != (2 if lay is None else 3):
-        _fail("w_gate must have %s" % ("2 dimensions" if lay is None else "3 dimensions"))
+    lead = _lead(w_gate, "w_gate", lay)
     inter = w_gate.shape[-2]
     rows, desc = tokens, _DENSE
     if lay is not None:
@@ -238,7 +271,7 @@ def _gated(x, w_gate, w_up, activation, save_pre, out, ws, lay, tile_m, top_k):
     pre = out.get("pre") if save_pre else None
     a = _PACK_GATED(d, act, tokens, hidden, inter, *desc, *_mat(x, "x", (tokens, hidden), x),
                     *_mat(w_gate, "w_gate", wshape, x), *_mat(w_up, "w_up", wshape, x),
-                    *_mat(out["h"], "h", (rows, inter), x),
+                    *_mat(_out(out, "h"), "h", (rows, inter), x),
                     *_mat(pre, "pre", (rows, 2 * inter), x), *_NONE * 4)
     if lay is not None and lead[0] == 0:  # no experts here: every row is zero
         return _zeros(out, "h", "pre" if save_pre else "h")
@@ -272,9 +305,7 @@ def _gated_backward(dh, pre, x, w_gate, w_up, activation, out, ws, lay, tile_m, 
     d = _first(x, "x")
     act = _activation(activation)
     tokens, hidden = x.shape
-    lead = w_gate.shape[:-2]
-    if w_gate.dim() != (2 if lay is None else 3):
-        _fail("w_gate must have %s" % ("2 dimensions" if lay is None else "3 dimensions"))
+    lead = _lead(w_gate, "w_gate", lay)
     inter = w_gate.shape[-2]
     rows, desc = tokens, _DENSE
     if lay is not None:
@@ -323,9 +354,7 @@ def _linear(x, w, bias, activation, residual, save_pre, out, ws, lay, tile_m):
     d = _first(x, "x")
     act = _activation(activation)
     rows, n_in = x.shape
-    lead = w.shape[:-2]
-    if w.dim() != (2 if lay is None else 3):
-        _fail("w must have %s" % ("2 dimensions" if lay is None else "3 dimensions"))
+    lead = _lead(w, "w", lay)
     n_out = w.shape[-2]
     desc = _DENSE
     if lay is not None:
@@ -341,7 +370,7 @@ def _linear(x, w, bias, activation, residual, save_pre, out, ws, lay, tile_m):
                      *_mat(w, "w", (*lead, n_out, n_in), x),
                      *_vec(bias, "bias", (*lead, n_out), x),
                      *_mat(residual, "residual", (rows, n_out), x),
-                     *_mat(out["y"], "y", (rows, n_out), x),
+                     *_mat(_out(out, "y"), "y", (rows, n_out), x),
                      *_mat(pre, "pre", (rows, n_out), x), *_NONE * 4)
     if lay is not None and lead[0] == 0:
         return _zeros(out, "y", "pre" if save_pre else "y")
@@ -373,9 +402,7 @@ def _linear_backward(dy, x, w, pre, activation, bias_grad, out, ws, lay, tile_m)
     d = _first(x, "x")
     act = _activation(activation)
     rows, n_in = x.shape
-    lead = w.shape[:-2]
-    if w.dim() != (2 if lay is None else 3):
-        _fail("w must have %s" % ("2 dimensions" if lay is None else "3 dimensions"))
+    lead = _lead(w, "w", lay)
     n_out = w.shape[-2]
     if act and pre is None:
         _fail("pre is needed where there is an activation")
@@ -424,28 +451,36 @@ def expert_linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
     return _linear_backward(dy, x, w, pre, activation, bias_grad, out, ws, lay, tile_m)
 
 
+def _tokens(lay) -> torch.Size:
+    """(tokens, entries a token) of the layout."""
+    packed = _of(lay, "packed")
+    if not isinstance(packed, torch.Tensor) or packed.dim() != 2:
+        _fail("packed must be a tensor of 2 dimensions")
+    return packed.shape
+
+
 def _combine_args(y_rows, width, d, lay, num_experts, weighted, like, backward, mats, dweights):
-    packed = lay["packed"]
     dev = like.device
-    if packed.dim() != 2:
-        _fail("packed must have 2 dimensions")
-    tokens, top_k = packed.shape
-    offsets = lay["offsets"]
-    w = lay["topk_weights"] if weighted else None
-    if w is not None and (w.dtype != torch.float32 or w.shape != packed.shape or
-                          w.device != dev or not w.is_contiguous()):
+    tokens, top_k = _tokens(lay)
+    packed = lay["packed"]
+    w = _of(lay, "topk_weights") if weighted else None
+    if w is not None and (not isinstance(w, torch.Tensor) or w.dtype != torch.float32 or
+                          w.shape != packed.shape or w.device != dev or not w.is_contiguous()):
         _fail(f"topk_weights must be a contiguous float32 tensor like packed on {dev}")
     n = tokens * top_k
+    offsets = _of(lay, "offsets")
+    o = _index(offsets, "offsets", dev, 1)
     num_ids = offsets.numel() - 1
+    num_experts = _number(num_experts, "num_experts")
     if not 0 <= num_experts <= num_ids:
         _fail(f"num_experts must be between 0 and the {num_ids} ids of the layout")
     rows = (0, 0)
     if backward:
-        rows = [_index(lay[k], k, dev, y_rows) for k in ("m_indices", "row_entry")]
+        rows = [_index(_of(lay, k), k, dev, y_rows) for k in ("m_indices", "row_entry")]
     return _PACK_COMBINE(d, width, tokens, y_rows, top_k, num_experts, num_ids,
-                         _index(packed, "packed", dev), _index(lay["inv_perm"], "inv_perm", dev, n),
-                         _index(offsets, "offsets", dev, 1),
-                         _index(lay["padded_offsets"], "padded_offsets", dev, num_ids + 1),
+                         _index(packed, "packed", dev),
+                         _index(_of(lay, "inv_perm"), "inv_perm", dev, n), o,
+                         _index(_of(lay, "padded_offsets"), "padded_offsets", dev, num_ids + 1),
                          *rows, 0 if w is None else w.data_ptr(), *mats, dweights)
 
 
@@ -457,7 +492,7 @@ def combine(y: torch.Tensor, lay: Dict[str, torch.Tensor], *, num_experts: int,
     the entries of the experts 0 .. num_experts-1."""
     d = _first(y, "y")
     rows, width = y.shape
-    tokens = lay["packed"].shape[0]
+    tokens, _ = _tokens(lay)
     if out is None:
         out = torch.empty((tokens, width), dtype=y.dtype, device=y.device)
     a = _combine_args(rows, width, d, lay, num_experts, weighted, y, False,
@@ -477,25 +512,30 @@ def combine_backward(dout: torch.Tensor, y: Optional[torch.Tensor],
     the rows are then those of m_indices). The residual's gradient is dout."""
     d = _first(dout, "dout")
     tokens, width = dout.shape
+    entries = _tokens(lay)
+    if y is None:
+        _index(_of(lay, "m_indices"), "m_indices", dout.device)
+    elif not isinstance(y, torch.Tensor) or y.dim() != 2:
+        _fail("y must be a tensor of 2 dimensions")
     rows = lay["m_indices"].numel() if y is None else y.shape[0]
     if out is None:
         out = {"dy": torch.empty((rows, width), dtype=dout.dtype, device=dout.device)}
         if weighted:
-            out["dweights"] = torch.empty(lay["packed"].shape, dtype=torch.float32,
+            out["dweights"] = torch.empty(entries, dtype=torch.float32,
                                           device=dout.device)
     dw = out.get("dweights")
     if dw is not None:
         if y is None:
             _fail("y is needed for dweights")
-        if dw.dtype != torch.float32 or dw.shape != lay["packed"].shape or \
+        if dw.dtype != torch.float32 or dw.shape != entries or \
                 not dw.is_contiguous() or dw.device != dout.device:
             _fail("dweights must be a contiguous float32 tensor like packed")
-    if lay["packed"].shape[0] != tokens:
+    if entries[0] != tokens:
         _fail("dout must have one row for each token of the layout")
     a = _combine_args(rows, width, d, lay, num_experts, weighted, dout, True,
                       (*_mat(y, "y", (rows, width), dout), *_NONE * 2,
                        *_mat(dout, "dout", (tokens, width), dout),
-                       *_mat(out["dy"], "dy", (rows, width), dout)),
+                       *_mat(_out(out, "dy"), "dy", (rows, width), dout)),
                       0 if dw is None else dw.data_ptr())
     _COMBINE_BACKWARD(a, dout.device)
     return out

@@ -110,6 +110,36 @@ def test_the_calls_below_are_right_but_for_one_thing(calls):
     assert len(calls) == 6
 
 
+@pytest.mark.parametrize("op,kw", [
+    ("gated", dict(out={})), ("linear", dict(out={})), ("combine_backward", dict(out={})),
+    ("gated", dict(out={"h": None})), ("combine_backward", dict(out={"dy": None})),
+    ("gated", dict(w=None)), ("gated_backward", dict(w=[])), ("linear", dict(w=None)),
+    ("linear_backward", dict(w=3)),
+    ("gated", dict(tile_m=None)), ("gated_backward", dict(top_k=2.0)), ("linear", dict(tile_m="16")),
+    ("linear_backward", dict(tile_m=1 << 31)), ("gated", dict(tile_m=-1 << 40)),
+    ("combine", dict(num_experts=None)), ("combine_backward", dict(num_experts=1.5)),
+])
+def test_refusals_are_the_packages_own(calls, op, kw):
+    with pytest.raises(M.MoeRouteError):
+        some_calls()[op](**kw)
+    assert not calls
+
+
+@pytest.mark.parametrize("op,need", [
+    ("gated", ("counts", "padded_offsets", "m_indices")),
+    ("gated_backward", ("counts", "padded_offsets", "m_indices")),
+    ("linear", ("padded_offsets", "m_indices")), ("linear_backward", ("counts", "m_indices")),
+    ("combine", ("packed", "inv_perm", "offsets", "padded_offsets", "topk_weights")),
+    ("combine_backward", ("packed", "m_indices", "row_entry")),
+])
+def test_what_a_layout_lacks_is_named(calls, op, need):
+    for k in need:
+        for lay in ({a: b for a, b in layout(3).items() if a != k}, {**layout(3), k: None}):
+            with pytest.raises(M.MoeRouteError, match=k):
+                some_calls()[op](lay=lay)
+    assert not calls
+
+
 def test_no_experts_here(calls):
     """Without experts the rows are zeroed, after the same checks as ever."""
     ops = some_calls(0)
