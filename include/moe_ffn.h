@@ -15,12 +15,18 @@
  * anything is launched, deterministic results, no allocation):
  *  - Matrices hold bf16 or fp16 (moe_dtype), all of a call the same; sums are
  *    fp32 and each output is rounded once. Inside moe_gated_ffn_backward and
- *    moe_linear_backward the gradient of the pre-activations is rounded once
- *    to the matrices' type before the two products that take it (weight
- *    gradients of up to 8 rows, or rows an expert, take it unrounded).
+ *    moe_linear_backward the gradient of the pre-activations (dg and du, or dz)
+ *    is rounded once to the matrices' type before the two products that take
+ *    it, so it has that type's range too: with fp16 one above 65504 becomes
+ *    infinite, and its row of dx and its column's dw with it, and one below
+ *    3e-8 is lost before the sums (a loss scale has to leave room for
+ *    dh * u * act'). Bf16 has the range of fp32. Linear calls without an
+ *    activation have nothing to round, and weight gradients of up to 8 rows,
+ *    or rows an expert, take it unrounded and in fp32's range.
  *  - A moe_matrix has contiguous columns and rows `ld` elements apart; a
  *    stack of one matrix per expert has them `stride` elements apart. Any ld
- *    of at least the columns, any stride and any element alignment works.
+ *    from the columns up to MOE_FFN_MAX_LD (rows that lie further apart are
+ *    copied by the caller), any stride and any element alignment works.
  *    The matrix cores read 16-byte pieces: an operand of a product whose
  *    pointer, ld, stride or columns are no multiple of 8 elements is first
  *    copied into the workspace with its rows padded (but for forward
@@ -122,8 +128,9 @@ int moe_gated_ffn_backward(const moe_gated_ffn_args *a, void *workspace, size_t 
  *       when there is an activation.
  * Backward: dz = dy act'(pre), or dy without an activation;
  *   dx [rows, in] = dz W, dw [out, in] = dz^T x, dbias [out] = sum of dz's
- *   rows, per expert. The gradient of the residual is dy itself. Any of dx,
- *   dw and dbias may be left out (p NULL).
+ *   rows, per expert. The gradient of the residual is dy itself (on rows
+ *   with an entry: the others' y is zero whatever the residual holds). Any of
+ *   dx, dw and dbias may be left out (p NULL).
  */
 typedef struct moe_linear_args {
   int32_t dtype, activation;

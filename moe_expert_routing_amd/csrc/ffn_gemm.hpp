@@ -30,8 +30,8 @@
 //
 // What bounds it, on one MI355X, and what was measured on the way:
 //  - 256 x 256 tiles, 8 waves of 128 x 64 (gated block of 4096 x 7168 -> 2048 in
-//    training, 240 GFLOP): 180 us, 1.33 PFLOP/s; the MFMA pipes are busy 65 % of
-//    the time at 1.95 GHz, where the power limit holds the clock. Its 112
+//    training, 240 GFLOP): 180-190 us, 1.27-1.33 PFLOP/s; the MFMA pipes are busy
+//    65 % of the time at 1.9 GHz, where the power limit holds the clock. Its 112
 //    stages take 153 us; the rest is the first loads and the stores, with every
 //    compute unit on one tile. 4 waves of 128 x 128 took 205 us: with one wave
 //    on a SIMD nothing covers its other instructions. Stages of 32 k, four or
@@ -39,15 +39,16 @@
 //  - The loop has no branches: stages past the last load zeros by an offset
 //    past the buffer. With a branch for the tail, or 64-bit addresses for
 //    each piece, the accumulators spilled.
-//  - Linear 8192 x 2048 -> 7168: 214 us plain, 250 with gelu, 285 with gelu,
-//    bias and residual: 3.5 tiles a compute unit take 4 rounds of 43 us for the
-//    stages, 4 for the stores, 5.5 for gelu and 4 for the residual, whose loads
-//    are issued together (one at a time: 304 us).
+//  - Linear 8192 x 2048 -> 7168: 214 us plain, 255 with gelu, 270 with gelu,
+//    bias and residual, and 285-300 with all of it on other inputs each call: 3.5
+//    tiles a compute unit take 4 rounds of 43 us for the stages, 4 for the stores,
+//    5.5 for gelu and 4 for the residual, whose loads are issued together (one at
+//    a time: 304 us where together took 285).
 //  - 112 experts with about 146 rows, 2048 -> 1024, 128 x 256 tiles: 265 us
 //    for 137 GFLOP (about 190 with the rows that fill up tiles) and 1 GB. Blocks
 //    that stay and go from tile to tile, the next tile's loads under the stores,
 //    were no faster (274 us; weight gradients 502 against 446).
-//  - Weight gradients of these experts, 256 x 256 tiles: 410-450 us, of which
+//  - Weight gradients of these experts, 256 x 256 tiles: 410-460 us, of which
 //    writing 940 MB could take 140: with three stages a tile, the first loads
 //    (4 us), the stages (5.7) and the stores (3.4) follow each other. 128 x 128
 //    and 256 x 128 tiles, two or three blocks to a compute unit, took the same.

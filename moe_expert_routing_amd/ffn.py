@@ -6,7 +6,8 @@ backward.
 Argument marshalling only, as in the package's own module: tensors are
 checked, outputs and a workspace are allocated when the caller gives none, and
 the HIP kernels behind the C ABI do every step. The backward passes are calls
-of their own; nothing is kept between calls.
+of their own: outputs carry no autograd graph, also where inputs require
+gradients, and nothing is kept between calls.
 
     gated_ffn(x, w_gate, w_up)                 -> moe_gated_ffn
     gated_ffn_backward(dh, pre, x, w_gate, w_up) -> moe_gated_ffn_backward

@@ -108,3 +108,18 @@ def test_few_of_the_experts_have_rows(n, tile, live, each):
     ids = (torch.arange(live * each) % live * (n // live))[:, None]
     lay = hand_layout(ids, n, tile)
     check_expert_gated(lay, n, 1, normal(1, live * each, 136, dt=BF), 72, tile, BF)
+
+
+def test_weight_gradients_of_few_rows_have_the_range_of_fp32():
+    """fp16, dh u act'(g) up to 1e6 on 8 rows: dW takes it unrounded."""
+    T, H, F = 8, 40, 24
+    x = normal(1, T, H, dt=FP, scale=1e-3)
+    dh, pre = normal(2, T, F, dt=FP, scale=300.0), normal(3, T, 2 * F, dt=FP, scale=300.0)
+    wg = normal(4, F, H, dt=FP)
+    out = {"dw_gate": torch.empty_like(wg), "dw_up": torch.empty_like(wg)}
+    r = M.gated_ffn_backward(dh, pre, x, wg, wg, out=out)
+    grads = gated_grads(dh, pre, x, wg, wg, "silu", FP)
+    for k in out:
+        ref, b = grads[k]
+        assert bool(torch.isfinite(r[k]).all()) and float((dh.double() * pre[:, F:].double()).abs().max()) > 65504
+        assert_close(r[k], ref, b, k)
