@@ -21,7 +21,9 @@ Calls (same names as the C ABI):
     sigmoid_rn32(x, mode=0)                        -> moe_sigmoid_rn32 (diagnostic)
 and the feed-forward operators on the routed rows and on the tokens (module
 ``ffn``, C ABI ``include/moe_ffn.h``): gated_ffn, linear, combine, their
-expert forms and their backward passes.
+expert forms and their backward passes; and the operators around them (module
+``block``, C ABI ``include/moe_block.h``): rms_norm, dropout, mxfp8_values and
+their backward passes.
 """
 from __future__ import annotations
 
@@ -32,7 +34,8 @@ from typing import Dict, Optional
 
 import torch
 
-from . import ffn
+from . import block, ffn
+from .block import dropout, dropout_backward, mxfp8_values, rms_norm, rms_norm_backward
 from .ffn import (combine, combine_backward, expert_gated_ffn, expert_gated_ffn_backward,
                   expert_linear, expert_linear_backward, gated_ffn, gated_ffn_backward, linear,
                   linear_backward)
@@ -110,7 +113,8 @@ def lib() -> ctypes.CDLL:
             raise MoeRouteError(
                 f"{LIB_PATH} is missing: build it with `python -m moe_expert_routing_amd.build`")
         handle = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in (*EXPORTS.items(), *ffn.EXPORTS.items()):
+        for name, (res, args) in (*EXPORTS.items(), *ffn.EXPORTS.items(),
+                                  *block.EXPORTS.items()):
             fn = getattr(handle, name)
             fn.restype = res
             fn.argtypes = args

@@ -1,27 +1,9 @@
 // ffn.hip - the C entry points of the feed-forward operators: checks, padded
 // copies where an operand needs one, and the launches.
-#include "ffn.hpp"
+#include "ffn_host.hpp"
 #include "ffn_rows.hpp"
 
 namespace moe_ffn {
-
-static const int64_t MAX_ROWS = MOE_FFN_MAX_ROWS;
-
-static int round8(int v) { return (v + 7) & ~7; }
-static size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
-
-// Hands out the workspace in 256-byte aligned parts. A dry one only counts
-// them: the same code sizes the workspace and then runs the call.
-struct Arena {
-  uint8_t *base;
-  bool dry;
-  size_t used;
-  uint16_t *take(size_t bytes) {
-    uint8_t *p = dry ? nullptr : base + used;
-    used += align256(bytes);
-    return reinterpret_cast<uint16_t *>(p);
-  }
-};
 
 static int launch_gemm(int dtype, int mode, int kind, const GemmArgs &g, hipStream_t st) {
   return dtype == MOE_BF16 ? launch_gemm_bf16(mode, kind, g, st) : launch_gemm_f16(mode, kind, g, st);
@@ -33,19 +15,12 @@ static dim3 row_grid(int64_t rows, int cols8, int z) {
               (uint32_t)(y < 65535 ? y : 65535), (uint32_t)z);
 }
 
-// An operand of a product: the matrix itself where its 16-byte pieces are
-// aligned, else a padded copy in the workspace. `mats` matrices of [rows,
-// cols].
-struct Operand {
-  const uint16_t *p;
-  int64_t ld, stride;
-};
 static bool is_aligned(const moe_matrix &m, int cols, int mats) {
   return ((uintptr_t)m.p & 15) == 0 && ((m.ld | cols) & 7) == 0 &&
          (mats == 1 || (m.stride & 7) == 0);
 }
-static Operand operand(const moe_matrix &m, int64_t rows, int cols, int mats, Arena &a,
-                       hipStream_t st, int *status, bool copy = false) {
+Operand operand(const moe_matrix &m, int64_t rows, int cols, int mats, Arena &a, hipStream_t st,
+                int *status, bool copy) {
   if ((is_aligned(m, cols, mats) && !copy) || rows == 0) return {(const uint16_t *)m.p, m.ld, m.stride};
   const int c8 = round8(cols);
   uint16_t *dst = a.take((size_t)mats * rows * c8 * 2);
@@ -57,10 +32,6 @@ static Operand operand(const moe_matrix &m, int64_t rows, int cols, int mats, Ar
   return {dst, c8, rows * c8};
 }
 
-// How a product runs: its tile, and the ranges that its k is split into.
-struct Plan {
-  int kind, splits;
-};
 // Plan of `mats` products of M x N over K: the one with the least estimated time,
 // its rounds over the 256 compute units times (64-k stages times a stage's
 // time, plus a fixed part). The stage times, in microseconds, are measured
@@ -120,7 +91,7 @@ static int64_t expert_rows(const moe_expert_rows &r, int64_t rows) {
 // forward product of up to 16 rows goes by the skinny kernel; dx of as few, whose
 // weights are read transposed, by the plan (16-row tiles and the plan: 8 rows of 7168
 // from 7168 48 and 26 us, 12 rows of 4096 from 14336 87 and 31).
-static Plan row_plan(const moe_expert_rows &r, bool forward, int64_t M, int64_t N, int64_t K) {
+Plan row_plan(const moe_expert_rows &r, bool forward, int64_t M, int64_t N, int64_t K) {
   if (r.num_experts > 0) {
     const int64_t mean = expert_rows(r, M);
     if (mean >= 320) return {TILE_256, 1};
@@ -151,8 +122,8 @@ static Plan weight_plan(const moe_expert_rows &r, int64_t segs, int64_t M, int64
 // Runs a product by its plan, with the partial sums of a split one in the
 // workspace. `width`: the partial sums of a row of C. `tile_m`: the alignment of
 // the layout, 0 for a dense product.
-static int run_product(int dtype, int mode, const Plan &plan, GemmArgs &g, int width, int tile_m,
-                       Arena &ws, hipStream_t st) {
+int run_product(int dtype, int mode, const Plan &plan, GemmArgs &g, int width, int tile_m,
+                Arena &ws, hipStream_t st) {
   const int64_t stages = (g.K + 63) / 64;
   const int bm = rows_of_tile(plan.kind);
   if (mode != WGRAD && tile_m % bm != 0) {
@@ -204,7 +175,7 @@ static int check_common(int dtype, int act, int64_t tokens, int w0, int w1,
 
 // A matrix of `rows` x `cols`, one or `mats` of them. Optional matrices may be
 // NULL, and any may where it has no elements.
-static int check_matrix(const moe_matrix &m, int64_t rows, int cols, int mats, bool optional) {
+int check_matrix(const moe_matrix &m, int64_t rows, int cols, int mats, bool optional) {
   if (!m.p) return optional || rows == 0 ? MOE_OK : MOE_ERR_NULL;
   if ((uintptr_t)m.p % 2 != 0) return MOE_ERR_SHAPE;
   if (rows > 1 && m.ld < cols) return MOE_ERR_SHAPE;
@@ -213,12 +184,6 @@ static int check_matrix(const moe_matrix &m, int64_t rows, int cols, int mats, b
   if (mats > 1 && m.stride < (rows - 1) * m.ld + cols) return MOE_ERR_SHAPE;
   return MOE_OK;
 }
-#define MOE_TRY(x)              \
-  do {                          \
-    const int st_ = (x);        \
-    if (st_ != MOE_OK) return st_; \
-  } while (0)
-
 static int64_t call_rows(const moe_expert_rows &r, int64_t tokens) {
   return r.num_experts > 0 ? r.rows : tokens;
 }
@@ -571,24 +536,6 @@ static CombineArgs combine_args(const moe_combine_args *a) {
   c.ld_dy = a->dy.ld;
   c.dweights = a->dweights;
   return c;
-}
-
-template <class Args>
-static int64_t sized(const Args *a, int check, int (*run)(const Args *, Arena &, hipStream_t)) {
-  if (check != MOE_OK) return -1;
-  Arena ws = {nullptr, true, 0};
-  run(a, ws, nullptr);
-  return (int64_t)ws.used;
-}
-template <class Args>
-static int checked_run(const Args *a, int check, int (*run)(const Args *, Arena &, hipStream_t),
-                       void *workspace, size_t bytes, void *stream) {
-  MOE_TRY(check);
-  const int64_t need = sized(a, MOE_OK, run);
-  if (need > 0 && (!workspace || (uintptr_t)workspace % 16 != 0 || bytes < (size_t)need))
-    return MOE_ERR_WORKSPACE;
-  Arena ws = {(uint8_t *)workspace, false, 0};
-  return run(a, ws, (hipStream_t)stream);
 }
 
 }  // namespace moe_ffn
