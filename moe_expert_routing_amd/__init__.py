@@ -23,7 +23,9 @@ and the feed-forward operators on the routed rows and on the tokens (module
 ``ffn``, C ABI ``include/moe_ffn.h``): gated_ffn, linear, combine, their
 expert forms and their backward passes; and the operators around them (module
 ``block``, C ABI ``include/moe_block.h``): rms_norm, dropout, mxfp8_values and
-their backward passes.
+their backward passes; and the linear product with low-rank adapters (module
+``adapters``, C ABI ``include/moe_adapter.h``): adapter_linear and its backward
+pass.
 """
 from __future__ import annotations
 
@@ -34,7 +36,8 @@ from typing import Dict, Optional
 
 import torch
 
-from . import block, ffn
+from . import adapters, block, ffn
+from .adapters import adapter_linear, adapter_linear_backward
 from .block import dropout, dropout_backward, mxfp8_values, rms_norm, rms_norm_backward
 from .ffn import (combine, combine_backward, expert_gated_ffn, expert_gated_ffn_backward,
                   expert_linear, expert_linear_backward, gated_ffn, gated_ffn_backward, linear,
@@ -114,7 +117,7 @@ def lib() -> ctypes.CDLL:
                 f"{LIB_PATH} is missing: build it with `python -m moe_expert_routing_amd.build`")
         handle = ctypes.CDLL(LIB_PATH)
         for name, (res, args) in (*EXPORTS.items(), *ffn.EXPORTS.items(),
-                                  *block.EXPORTS.items()):
+                                  *block.EXPORTS.items(), *adapters.EXPORTS.items()):
             fn = getattr(handle, name)
             fn.restype = res
             fn.argtypes = args

@@ -26,7 +26,7 @@ LIB_PATH = os.path.join(LIB_DIR, "libmoe_route.so")
 TEMPS = os.path.join(ROOT, "_build")
 SOURCES = [os.path.join(CSRC, name) for name in (
     "moe_route.hip", "router_gemm.hip", "ffn.hip", "ffn_bf16.hip", "ffn_f16.hip",
-    "block.hip")]
+    "block.hip", "adapters.hip", "adapter_bf16.hip", "adapter_f16.hip")]
 ARCH = "gfx950"
 
 HIP_FLAGS = [

@@ -1,0 +1,134 @@
+// adapter_expand.hpp - the low-rank term of a product, s B_a^T with the adapter a of
+// each row, added to the sums that the product kernels hold before their epilogue.
+//
+// s is fp32. The matrix cores take it in two halves of the matrices' type, high and low:
+// 16 (bf16) or 22 (fp16) bits of it, so that its rounding stays far below the output's;
+// the second half costs 1/(in / 32) of the product's operations. In fp16, whose range
+// s may pass, a row's values are taken at a power of two that makes the largest of
+// 32 of them lie in [2^14, 2^15).
+//
+// A row takes only its own adapter's result, by a selection and not by factors of zero:
+// infinities or NaN in one adapter stay out of the other requests' rows.
+#pragma once
+
+#include "ffn_types.hpp"
+
+namespace moe_ffn {
+
+// v in two halves of the type. What is no finite number stays in the high half.
+template <class D>
+__device__ __forceinline__ void halves(f32x8 v, s16x8 &hi, s16x8 &lo) {
+  hi = pack8<D>(v);
+  const f32x8 h = unpack8<D>(hi);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __builtin_isfinite(h[i]) ? v[i] - h[i] : 0.f;
+  lo = pack8<D>(v);
+}
+// The power of two that takes `most`, the largest of some magnitudes, into [2^14, 2^15).
+__device__ __forceinline__ int exponent_for(float most) {
+  const int e = (int)(__float_as_uint(most) >> 23 & 0xff);
+  return e == 0 || e == 255 ? 0 : 14 + 127 - e;
+}
+
+// acc[i][j] of a wave: rows row0 + 16 i + fr, columns col0 + 16 j + 4 fq .. 4 fq + 3 in
+// a lane (fr = lane & 15, fq = lane >> 4). For every 16 rows the adapters among them
+// are taken one after the other; the fragments of B stay from one 16 rows to the next
+// while the adapter is the same, as in a prompt's rows.
+template <class D, int FM, int FN>
+__device__ __forceinline__ void add_low_rank(f32x4 (&acc)[FM][FN], const LowRank &g, int row0,
+                                             int row_end, int col0, int N) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr bool SCALED = D::MAX_EXPONENT < 127;
+  const int lane = threadIdx.x & 63, fr = lane & 15, fq = lane >> 4;
+  // 64 rows at a time: their values of s are loaded together
+  constexpr int GROUP = FM < 4 ? FM : 4;
+#pragma unroll
+  for (int i0 = 0; i0 < FM; i0 += GROUP) {
+    int id[GROUP];
+#pragma unroll
+    for (int i = 0; i < GROUP; ++i) {
+      const int m = row0 + 16 * (i0 + i) + fr;
+      id[i] = m < row_end ? g.ids[m] : -1;
+      if ((uint32_t)id[i] >= (uint32_t)g.n) id[i] = -1;
+    }
+#pragma unroll 1
+    for (int k0 = 0; k0 < g.rank; k0 += 32) {
+      const int k = k0 + fq * 8;
+      f32x8 v[GROUP];
+#pragma unroll
+      for (int i = 0; i < GROUP; ++i) {
+        v[i] = f32x8{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (id[i] >= 0)
+          v[i] = load8_f32(g.s + (int64_t)(row0 + 16 * (i0 + i) + fr) * g.rank, k, g.rank);
+      }
+      int have = -1;
+      s16x8 fb[FN];
+#pragma unroll
+      for (int i = 0; i < GROUP; ++i) {
+        uint32_t todo = (uint32_t)__ballot(id[i] >= 0) & 0xffffu;
+        if (!todo) continue;
+        int power = 0;
+        if constexpr (SCALED) {
+          float most = 0.f;
+#pragma unroll
+          for (int t = 0; t < 8; ++t) most = fmaxf(most, fabsf(v[i][t]));
+          most = fmaxf(most, __shfl_xor(most, 16));
+          most = fmaxf(most, __shfl_xor(most, 32));
+          power = exponent_for(most);
+#pragma unroll
+          for (int t = 0; t < 8; ++t) v[i][t] = __builtin_amdgcn_ldexpf(v[i][t], power);
+        }
+        s16x8 hi, lo;
+        halves<D>(v[i], hi, lo);
+        while (todo) {
+          const int a = __builtin_amdgcn_readlane(id[i], __builtin_ctz(todo));
+          const bool mine = id[i] == a;
+          todo &= ~(uint32_t)__ballot(mine);
+          if (a != have) {
+            have = a;
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+              fb[j] = load8_raw(
+                  g.b + a * g.stride + (int64_t)min(col0 + 16 * j + fr, N - 1) * g.ldb, k, g.rank);
+          }
+#pragma unroll
+          for (int j = 0; j < FN; ++j) {
+            f32x4 t = D::mfma(fb[j], lo, f32x4{0.f, 0.f, 0.f, 0.f});
+            t = D::mfma(fb[j], hi, t);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if constexpr (SCALED) t[e] = __builtin_amdgcn_ldexpf(t[e], -power);
+              acc[i0 + i][j][e] = mine ? acc[i0 + i][j][e] + t[e] : acc[i0 + i][j][e];
+            }
+          }
+        }
+      }
+    }
+  }
+#endif
+}
+
+// The term of row m and columns n .. n + 7 in fp32, for the few-row products.
+template <class D>
+__device__ __forceinline__ f32x8 low_rank_run(const LowRank &g, int64_t m, int n, int N) {
+  f32x8 d = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  const int id = g.ids[m];
+  if ((uint32_t)id >= (uint32_t)g.n) return d;
+  const uint16_t *b = g.b + id * g.stride + (int64_t)n * g.ldb;
+#pragma unroll 2
+  for (int k = 0; k < g.rank; k += 8) {
+    const f32x8 s = load8_f32(g.s + m * g.rank, k, g.rank);
+    s16x8 raw[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) raw[c] = load8_raw(b + min(c, N - 1 - n) * g.ldb, k, g.rank);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const f32x8 w = unpack8<D>(raw[c]);
+#pragma unroll
+      for (int t = 0; t < 8; ++t) d[c] = fmaf(s[t], w[t], d[c]);
+    }
+  }
+  return d;
+}
+
+}  // namespace moe_ffn

@@ -6,6 +6,8 @@
 namespace moe_ffn {
 
 static int launch_gemm(int dtype, int mode, int kind, const GemmArgs &g, hipStream_t st) {
+  if (g.low.ids)
+    return dtype == MOE_BF16 ? launch_low_bf16(mode, kind, g, st) : launch_low_f16(mode, kind, g, st);
   return dtype == MOE_BF16 ? launch_gemm_bf16(mode, kind, g, st) : launch_gemm_f16(mode, kind, g, st);
 }
 

@@ -11,6 +11,9 @@ enum TileKind { TILE_16, TILE_32, TILE_64, TILE_64W, TILE_128, TILE_128W, TILE_2
 // Launches a product of the given mode (Mode); compiled for each element type.
 int launch_gemm_bf16(int mode, int kind, const GemmArgs &g, hipStream_t st);
 int launch_gemm_f16(int mode, int kind, const GemmArgs &g, hipStream_t st);
+// The same with a low-rank term.
+int launch_low_bf16(int mode, int kind, const GemmArgs &g, hipStream_t st);
+int launch_low_f16(int mode, int kind, const GemmArgs &g, hipStream_t st);
 
 // A launch takes fewer than 2^32 work items in a dimension of its grid: more blocks
 // go in several, each of which is told the number of its first. Its status.

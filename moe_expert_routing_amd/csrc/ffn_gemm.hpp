@@ -57,6 +57,7 @@
 #include <type_traits>
 #include <utility>
 
+#include "adapter_expand.hpp"
 #include "ffn_types.hpp"
 
 namespace moe_ffn {
@@ -160,7 +161,7 @@ __device__ __forceinline__ void tile_at(int t, int m_tiles, int n_tiles, int &mt
   nt = t / size;
 }
 
-template <class D, int MODE, class C, bool GATHER>
+template <class D, int MODE, class C, bool GATHER, bool LOW = false>
 __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm_kernel(
     const GemmArgs g) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -504,6 +505,11 @@ __global__ __launch_bounds__(C::NTHREADS, (C::BLOCKS * C::NW + 3) / 4) void gemm
       settle_entries();
       step(1, s + 1, 0, std::true_type(), s + NS);
     }
+  }
+
+  // the low-rank term joins the sums of the first k range
+  if constexpr (LOW) {
+    if (split == 0) add_low_rank<D, C::FM, C::FN>(acc, g.low, m0 + wm, m_end, n0 + wn, g.N);
   }
 
   // Epilogue. A lane holds row fr and columns 4 fq .. 4 fq + 3 of every 16 x 16

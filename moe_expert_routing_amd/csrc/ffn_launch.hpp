@@ -16,7 +16,7 @@ typedef Tile<64, 64, 32, 32, 4, 2> Tile64;
 typedef Tile<32, 64, 16, 32, 4, 2> Tile32;
 typedef Tile<16, 128, 16, 32, 4, 2> Tile16;
 
-template <class D, int MODE, class C>
+template <class D, int MODE, class C, bool LOW = false>
 static int launch(GemmArgs g, hipStream_t st) {
   const int bn = MODE == GATED ? C::BN / 2 : C::BN;
   if (!g.tile_map) g.m_tiles = (g.M + C::BM - 1) / C::BM;
@@ -27,10 +27,10 @@ static int launch(GemmArgs g, hipStream_t st) {
   if (blocks > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
   // the forward tiles of dense_plan alone never gather
   constexpr bool DENSE = std::is_same_v<C, Tile128> || std::is_same_v<C, Tile64>;
-  constexpr bool GATHERS = MODE == WGRAD || (MODE == GATED && !DENSE);
+  constexpr bool GATHERS = !LOW && (MODE == WGRAD || (MODE == GATED && !DENSE));
   if (!GATHERS && g.r.row_entry) return MOE_ERR_UNSUPPORTED;
   const auto kernel =
-      g.r.row_entry ? gemm_kernel<D, MODE, C, GATHERS> : gemm_kernel<D, MODE, C, false>;
+      g.r.row_entry ? gemm_kernel<D, MODE, C, GATHERS, LOW> : gemm_kernel<D, MODE, C, false, LOW>;
   return in_parts(blocks, C::NTHREADS, [&](int64_t first, uint32_t n) {
     g.block0 = (uint32_t)first;
     kernel<<<n, C::NTHREADS, 0, st>>>(g);
@@ -38,7 +38,7 @@ static int launch(GemmArgs g, hipStream_t st) {
   });
 }
 
-template <class D, int MODE, int KW>
+template <class D, int MODE, int KW, bool LOW = false>
 static int launch_skinny_kw(GemmArgs g, hipStream_t st) {
   constexpr int COLS = SKINNY_WAVES / KW * (MODE == GATED ? 8 : 16);
   g.m_tiles = (g.M + 15) / 16;
@@ -48,7 +48,8 @@ static int launch_skinny_kw(GemmArgs g, hipStream_t st) {
   constexpr bool GATHERS = MODE == GATED && KW < 8;  // 8 waves: dense calls alone
   if (!GATHERS && g.r.row_entry) return MOE_ERR_UNSUPPORTED;
   const auto kernel =
-      g.r.row_entry ? skinny_kernel<D, MODE, KW, 4, GATHERS> : skinny_kernel<D, MODE, KW, 4, false>;
+      g.r.row_entry ? skinny_kernel<D, MODE, KW, 4, GATHERS, LOW>
+                    : skinny_kernel<D, MODE, KW, 4, false, LOW>;
   return in_parts(blocks, 64 * SKINNY_WAVES, [&](int64_t first, uint32_t n) {
     g.block0 = (uint32_t)first;
     kernel<<<n, 64 * SKINNY_WAVES, 0, st>>>(g);
@@ -90,6 +91,29 @@ static int launch_kind(int kind, const GemmArgs &g, hipStream_t st) {
   } else if constexpr (MODE != WGRAD) {
     if (kind == TILE_16) return launch_skinny<D, MODE>(g, st);
   }
+  return MOE_ERR_UNSUPPORTED;
+}
+
+// Dense products with a low-rank term: y's and dx's.
+template <class D, int MODE>
+static int launch_low_kind(int kind, const GemmArgs &g, hipStream_t st) {
+  switch (kind) {
+    case TILE_256: return launch<D, MODE, Tile256, true>(g, st);
+    case TILE_128: return launch<D, MODE, Tile128, true>(g, st);
+    case TILE_64: return launch<D, MODE, Tile64, true>(g, st);
+    case TILE_32: return launch<D, MODE, Tile32, true>(g, st);
+  }
+  if constexpr (MODE == LINEAR) {
+    if (kind == TILE_16)
+      return g.N / 16 >= 384 ? launch_skinny_kw<D, MODE, 4, true>(g, st)
+                             : launch_skinny_kw<D, MODE, 8, true>(g, st);
+  }
+  return MOE_ERR_UNSUPPORTED;
+}
+template <class D>
+static int launch_low(int mode, int kind, const GemmArgs &g, hipStream_t st) {
+  if (mode == LINEAR) return launch_low_kind<D, LINEAR>(kind, g, st);
+  if (mode == DGRAD) return launch_low_kind<D, DGRAD>(kind, g, st);
   return MOE_ERR_UNSUPPORTED;
 }
 

@@ -20,6 +20,7 @@ typedef float f32x8 __attribute__((ext_vector_type(8)));
 
 // The two element types: conversions (to nearest even) and their MFMA.
 struct Bf16 {
+  static constexpr int MAX_EXPONENT = 127;
   typedef __bf16 scalar;
   typedef bf16x4 v4;
   typedef bf16x8 v8;
@@ -29,6 +30,7 @@ struct Bf16 {
   }
 };
 struct F16 {
+  static constexpr int MAX_EXPONENT = 15;
   typedef _Float16 scalar;
   typedef f16x4 v4;
   typedef f16x8 v8;
@@ -177,6 +179,16 @@ struct Rows {
 // The uses of the product kernel.
 enum Mode { GATED = 0, LINEAR = 1, DGRAD = 2, WGRAD = 3 };
 
+// A low-rank term beside a product: C[m, n] += sum over r of s[m, r] b[id m][n, r], for
+// the rows whose id is 0 .. n - 1.
+struct LowRank {
+  const int32_t *ids;  // [M]; NULL: none
+  const float *s;      // [M, rank]
+  const uint16_t *b;   // [N, rank] of each adapter
+  int64_t ldb, stride;
+  int32_t n, rank;
+};
+
 // What one product kernel gets. C[m, n] = sum over k of A(m, k) B(n, k).
 struct GemmArgs {
   const uint16_t *a;       // M side
@@ -207,6 +219,7 @@ struct GemmArgs {
   float *partial;
   uint32_t top_k_magic, top_k_shift; // entry / top_k as a product; magic 0: top_k is 1
   uint32_t block0;         // number of the launch's first block
+  LowRank low;             // kernels that add a low-rank term
 };
 
 }  // namespace moe_ffn
