@@ -41,7 +41,7 @@ __device__ __forceinline__ void add_low_rank(f32x4 (&acc)[FM][FN], const LowRank
   constexpr bool SCALED = D::MAX_EXPONENT < 127;
   const int lane = threadIdx.x & 63, fr = lane & 15, fq = lane >> 4;
   // 64 rows at a time: their values of s are loaded together
-  constexpr int GROUP = FM < 4 ? FM : 4;
+  constexpr int GROUP = FM < 4 ? FM : 4, AT_ONCE = FN <= 2 ? 8 : 2;
 #pragma unroll
   for (int i0 = 0; i0 < FM; i0 += GROUP) {
     int id[GROUP];
@@ -59,10 +59,10 @@ __device__ __forceinline__ void add_low_rank(f32x4 (&acc)[FM][FN], const LowRank
       for (int i = 0; i < GROUP; ++i) {
         v[i] = f32x8{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (id[i] >= 0)
-          v[i] = load8_f32(g.s + (int64_t)(row0 + 16 * (i0 + i) + fr) * g.rank, k, g.rank);
+          v[i] = load8_f32(g.s + (int64_t)(row0 + 16 * (i0 + i) + fr) * g.lds, k, g.rank);
       }
-      int have = -1;
-      s16x8 fb[FN];
+      int have = -1;  // the adapter of fb[0], where it is there alone
+      s16x8 fb[AT_ONCE][FN];
 #pragma unroll
       for (int i = 0; i < GROUP; ++i) {
         uint32_t todo = (uint32_t)__ballot(id[i] >= 0) & 0xffffu;
@@ -81,24 +81,39 @@ __device__ __forceinline__ void add_low_rank(f32x4 (&acc)[FM][FN], const LowRank
         s16x8 hi, lo;
         halves<D>(v[i], hi, lo);
         while (todo) {
-          const int a = __builtin_amdgcn_readlane(id[i], __builtin_ctz(todo));
-          const bool mine = id[i] == a;
-          todo &= ~(uint32_t)__ballot(mine);
-          if (a != have) {
-            have = a;
+          // the next adapters' fragments are loaded together: a decode batch's rows
+          // have one each
+          int a[AT_ONCE];
 #pragma unroll
-            for (int j = 0; j < FN; ++j)
-              fb[j] = load8_raw(
-                  g.b + a * g.stride + (int64_t)min(col0 + 16 * j + fr, N - 1) * g.ldb, k, g.rank);
+          for (int q = 0; q < AT_ONCE; ++q) {
+            a[q] = todo ? __builtin_amdgcn_readlane(id[i], __builtin_ctz(todo)) : -1;
+            if (a[q] >= 0) todo &= ~(uint32_t)__ballot(id[i] == a[q]);
+          }
+          if (a[0] != have || a[1] >= 0) {
+            have = a[1] >= 0 ? -1 : a[0];
+#pragma unroll
+            for (int q = 0; q < AT_ONCE; ++q)
+              if (a[q] >= 0) {
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+                  fb[q][j] = load8_raw(g.b + a[q] * g.stride +
+                                           (int64_t)min(col0 + 16 * j + fr, N - 1) * g.ldb,
+                                       k, g.rank);
+              }
           }
 #pragma unroll
-          for (int j = 0; j < FN; ++j) {
-            f32x4 t = D::mfma(fb[j], lo, f32x4{0.f, 0.f, 0.f, 0.f});
-            t = D::mfma(fb[j], hi, t);
+          for (int q = 0; q < AT_ONCE; ++q) {
+            if (a[q] < 0) continue;
+            const bool mine = id[i] == a[q];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if constexpr (SCALED) t[e] = __builtin_amdgcn_ldexpf(t[e], -power);
-              acc[i0 + i][j][e] = mine ? acc[i0 + i][j][e] + t[e] : acc[i0 + i][j][e];
+            for (int j = 0; j < FN; ++j) {
+              f32x4 t = D::mfma(fb[q][j], lo, f32x4{0.f, 0.f, 0.f, 0.f});
+              t = D::mfma(fb[q][j], hi, t);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if constexpr (SCALED) t[e] = __builtin_amdgcn_ldexpf(t[e], -power);
+                acc[i0 + i][j][e] = mine ? acc[i0 + i][j][e] + t[e] : acc[i0 + i][j][e];
+              }
             }
           }
         }
@@ -106,29 +121,6 @@ __device__ __forceinline__ void add_low_rank(f32x4 (&acc)[FM][FN], const LowRank
     }
   }
 #endif
-}
-
-// The term of row m and columns n .. n + 7 in fp32, for the few-row products.
-template <class D>
-__device__ __forceinline__ f32x8 low_rank_run(const LowRank &g, int64_t m, int n, int N) {
-  f32x8 d = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  const int id = g.ids[m];
-  if ((uint32_t)id >= (uint32_t)g.n) return d;
-  const uint16_t *b = g.b + id * g.stride + (int64_t)n * g.ldb;
-#pragma unroll 2
-  for (int k = 0; k < g.rank; k += 8) {
-    const f32x8 s = load8_f32(g.s + m * g.rank, k, g.rank);
-    s16x8 raw[8];
-#pragma unroll
-    for (int c = 0; c < 8; ++c) raw[c] = load8_raw(b + min(c, N - 1 - n) * g.ldb, k, g.rank);
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const f32x8 w = unpack8<D>(raw[c]);
-#pragma unroll
-      for (int t = 0; t < 8; ++t) d[c] = fmaf(s[t], w[t], d[c]);
-    }
-  }
-  return d;
 }
 
 }  // namespace moe_ffn

@@ -1,6 +1,6 @@
 // adapter_rows.hpp - the kernels of the low-rank adapters beside the product: s = c_a
-// x A_a^T (and u = c_a dy B_a, the same on a transposed copy of B), the tokens in
-// the order of their adapters, transposed copies, and the adapters' gradients.
+// x A_a^T (and u = c_a dy B_a, the same on a transposed copy of B), y of a few rows,
+// the tokens in the order of their adapters, and the adapters' gradients.
 #pragma once
 
 #include "../../include/moe_adapter.h"
@@ -11,6 +11,140 @@ namespace moe_adapter {
 
 using namespace moe_ffn;
 
+// acc[r][i] += rows of a times rows of x over k elements, for products whose operands
+// have few rows: 16 RB rows of a, 16 MT of x, each wave on its own range of k.
+//
+// What a compute unit can take in depends on how its lanes ask. Measured with
+// one block alone, 672 KB of 14 KB rows from L2: 5.7 us contiguous, 11 with loads of 8
+// rows x 128 bytes in the order of the lanes, 19.5 with 16 rows x 64 bytes, as MFMA
+// fragments lie, or 8 x 128 in another order. So each wave stages blocks of 64 k in
+// LDS of its own with loads of the second kind, NS blocks deep, and reads fragments
+// there; there are no barriers. Lane l of a load takes row l >> 3 of eight and chunk (l &
+// 7) ^ (l >> 3) of its line, which it writes at 16 l: reading 16 rows of one chunk
+// then goes over all banks. Loads past k's end, or past the range, bring zeros.
+// Rows that are not 16-byte aligned, or whose k is no multiple of 8, are read as fragments.
+template <int MT, int RB, int NS>
+struct Stream {
+  static constexpr int PIECES = 2 * (MT + RB);      // loads of a block of 64 k
+  static constexpr int BYTES = NS * PIECES * 1024;  // a wave's LDS
+  static_assert(PIECES * (NS - 1) <= 63, "vmcnt range");
+};
+struct StreamRows {
+  const uint16_t *p;  // first row, at the wave's first k
+  int64_t ld;
+  int rows;  // at least 1; rows past them repeat the last one
+};
+
+template <class D, int RB, int MT, int NS, bool STAGED>
+__device__ __forceinline__ void stream_products(f32x4 (&acc)[RB][MT], const StreamRows &a,
+                                                const StreamRows &x, int k, uint8_t *lds) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const int lane = threadIdx.x & 63, fr = lane & 15, fq = lane >> 4;
+  if constexpr (STAGED) {
+    typedef Stream<MT, RB, NS> S;
+    const int chunk = (lane & 7) ^ (lane >> 3);
+    uint32_t off[S::PIECES];  // bytes, below 2^31 (128 rows of MOE_FFN_MAX_LD)
+#pragma unroll
+    for (int q = 0; q < S::PIECES; ++q) {
+      const StreamRows &s = q < 2 * RB ? a : x;
+      const int row = (q < 2 * RB ? q : q - 2 * RB) * 8 + (lane >> 3);
+      off[q] = (uint32_t)(min(row, s.rows - 1) * s.ld + chunk * 8) * 2;
+    }
+    const int blocks = (k + 63) / 64;
+    auto issue = [&](int s) MOE_INLINE {
+      const bool past = s * 64 + chunk * 8 >= k;
+#pragma unroll
+      for (int q = 0; q < S::PIECES; ++q)
+        lds_piece<true>(reinterpret_cast<const uint8_t *>((q < 2 * RB ? a.p : x.p) + s * 64),
+                        past ? PAST : off[q], lds + (s % NS * S::PIECES + q) * 1024);
+    };
+#pragma unroll
+    for (int s = 0; s < NS; ++s) issue(s);
+#pragma unroll 1
+    for (int s = 0; s < blocks; ++s) {
+      wait_vmcnt_imm<S::PIECES *(NS - 1)>();
+      const uint8_t *from = lds + s % NS * S::PIECES * 1024;
+      s16x8 f[2][RB + MT];
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int q = 0; q < RB + MT; ++q)
+          f[ks][q] = *reinterpret_cast<const s16x8 *>(from + q * 2048 + fr * 128 +
+                                                      (((ks * 4 + fq) ^ (fr & 7)) * 16));
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before it is filled again
+      issue(s + NS);
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int r = 0; r < RB; ++r)
+#pragma unroll
+          for (int i = 0; i < MT; ++i) acc[r][i] = D::mfma(f[ks][r], f[ks][RB + i], acc[r][i]);
+    }
+    wait_vmcnt_imm<0>();  // the zeros still on their way
+  } else {
+    const uint16_t *ar[RB], *xr[MT];
+#pragma unroll
+    for (int r = 0; r < RB; ++r) ar[r] = a.p + min(16 * r + fr, a.rows - 1) * a.ld + fq * 8;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) xr[i] = x.p + min(16 * i + fr, x.rows - 1) * x.ld + fq * 8;
+    int s = 0;
+#pragma unroll 4
+    for (; s + 32 <= k; s += 32) {
+      s16x8 fa[RB];
+#pragma unroll
+      for (int r = 0; r < RB; ++r) fa[r] = *reinterpret_cast<const s16x8_any *>(ar[r] + s);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const s16x8 fx = *reinterpret_cast<const s16x8_any *>(xr[i] + s);
+#pragma unroll
+        for (int r = 0; r < RB; ++r) acc[r][i] = D::mfma(fa[r], fx, acc[r][i]);
+      }
+    }
+    if (s < k) {
+      const int left = k - s - fq * 8;
+      s16x8 fa[RB];
+#pragma unroll
+      for (int r = 0; r < RB; ++r) fa[r] = load8_raw(ar[r] + s, 0, left);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const s16x8 fx = load8_raw(xr[i] + s, 0, left);
+#pragma unroll
+        for (int r = 0; r < RB; ++r) acc[r][i] = D::mfma(fa[r], fx, acc[r][i]);
+      }
+    }
+  }
+#endif
+}
+
+// The waves' sums of a block, [WAVES][16 MT rows][16 RB + 4] in `part`.
+template <int WAVES, int RB, int MT>
+struct Part {
+  static constexpr int LD = 16 * RB + 4, BYTES = WAVES * 16 * MT * LD * 4;
+  static __device__ __forceinline__ void put(float *part, int wave, const f32x4 (&acc)[RB][MT]) {
+    const int lane = threadIdx.x & 63, fr = lane & 15, fq = lane >> 4;
+#pragma unroll
+    for (int r = 0; r < RB; ++r)
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        *reinterpret_cast<f32x4 *>(part + (wave * 16 * MT + 16 * i + fr) * LD + 16 * r + 4 * fq) = acc[r][i];
+  }
+  // of row t and column r, in the order of the waves
+  static __device__ __forceinline__ float sum(const float *part, int t, int r) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) v += part[(w * 16 * MT + t) * LD + r];
+    return v;
+  }
+};
+template <int RB, int MT>
+__device__ __forceinline__ void clear(f32x4 (&acc)[RB][MT]) {
+#pragma unroll
+  for (int r = 0; r < RB; ++r)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[r][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+}
+constexpr int most(int a, int b) { return a > b ? a : b; }
+
 // ------------------------------------------------------------ s = c_a x A_a^T
 
 struct ShrinkArgs {
@@ -18,199 +152,276 @@ struct ShrinkArgs {
   int64_t ldx, lda, stride;
   const int32_t *ids;
   const float *scale;  // NULL: 1
-  float *s;            // [M, rank]
-  int32_t M, K, rank, n;
+  float *s;            // [M, rank], rows lds elements apart
+  int32_t M, K, rank, n, lds;
+  int32_t turns;       // blocks for the same rows
+  int64_t block0;      // number of the launch's first block
 };
 
-// A block takes 16 MT rows, its waves share K; x and A go from memory straight into
-// MFMA operands, one batch of U k-steps loading while the other multiplies, and the
-// waves' sums meet in LDS. For each adapter among the rows the block goes through
-// K once: requests lie together, so a prompt's blocks have one or two. A decode
-// batch's rows may all have adapters of their own, and gridDim.y blocks share them.
-template <class D, int MT, int RB, int WAVES>
+// A block takes 16 MT rows, its waves share K and their sums meet in LDS. For each
+// adapter among the rows the block goes through K once; the blocks of `turns` rounds
+// over the rows share the adapters of a block's rows. Requests lie together, so a
+// prompt's rows have one or two and the second round's blocks mostly none; a decode
+// batch's rows may have 16. (The rounds follow each other: with the blocks of the same
+// rows side by side every second one ends at once, and as they go to the XCDs in turn,
+// half of these stood idle: 66 us instead of 35.)
+template <class D, int MT, int RB, int WAVES, int NS, bool STAGED>
 __global__ __launch_bounds__(64 * WAVES) void shrink_kernel(const ShrinkArgs g) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  constexpr int ROWS = 16 * MT, U = MT + RB <= 3 ? 4 : 2;
-  __shared__ __attribute__((aligned(16))) float part[WAVES][ROWS][16 * RB + 4];
-  const int lane = threadIdx.x & 63, fr = lane & 15, fq = lane >> 4;
+  constexpr int ROWS = 16 * MT, RING = STAGED ? Stream<MT, RB, NS>::BYTES : 0;
+  typedef Part<WAVES, RB, MT> P;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[most(WAVES * RING, P::BYTES)];
+  float *part = reinterpret_cast<float *>(lds);
+  const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int row0 = blockIdx.x * ROWS;
+  const uint32_t block = (uint32_t)(blockIdx.x + g.block0);
+  const uint32_t row_blocks = (g.M + ROWS - 1) / ROWS;
+  const int row0 = block % row_blocks * ROWS, my_turn = block / row_blocks;
   int id = lane < ROWS && row0 + lane < g.M ? g.ids[row0 + lane] : -1;
   if ((uint32_t)id >= (uint32_t)g.n) id = -1;
   const uint64_t with = __ballot(id >= 0);
   // rows without an adapter
-  if (blockIdx.y == 0)
+  if (my_turn == 0 && __popcll(with) < ROWS)
     for (int o = threadIdx.x; o < ROWS * g.rank; o += 64 * WAVES) {
       const int r = o / g.rank;
-      if (row0 + r < g.M && !(with >> r & 1)) g.s[(int64_t)row0 * g.rank + o] = 0.f;
+      if (row0 + r < g.M && !(with >> r & 1)) g.s[(int64_t)(row0 + r) * g.lds + o % g.rank] = 0.f;
     }
-  const int steps = (g.K + 31) / 32, per = ((steps + WAVES - 1) / WAVES + 1) & ~1;
-  const int s0 = min(steps, wave * per), s1 = min(steps, s0 + per);
-  const int whole = max(0, (min(s1, g.K / 32) - s0) / U);
-  const uint16_t *xr[MT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-    xr[i] = g.x + (int64_t)min(row0 + 16 * i + fr, g.M - 1) * g.ldx + s0 * 32 + fq * 8;
+  const int per = ((g.K + 63) / 64 + WAVES - 1) / WAVES * 64;
+  const int k0 = min(g.K, wave * per), k = min(g.K - k0, per);
+  const StreamRows x = {g.x + row0 * g.ldx + k0, g.ldx, g.M - row0};
   uint64_t todo = with;
-  for (uint32_t turn = 0; todo; ++turn) {
+  for (int turn = 0; todo; ++turn) {
     const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
     const uint64_t mine = __ballot(id == a);
     todo &= ~mine;
-    if (turn % gridDim.y != blockIdx.y) continue;
-    const uint16_t *ar[RB];
-#pragma unroll
-    for (int r = 0; r < RB; ++r)
-      ar[r] = g.a + a * g.stride + (int64_t)min(16 * r + fr, g.rank - 1) * g.lda + s0 * 32 + fq * 8;
+    if (turn % g.turns != my_turn) continue;
     f32x4 acc[RB][MT];
-#pragma unroll
-    for (int r = 0; r < RB; ++r)
-#pragma unroll
-      for (int i = 0; i < MT; ++i) acc[r][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    s16x8 fa[2][U][RB], fx[2][U][MT];
-    auto load = [&](int set, int s) MOE_INLINE {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-#pragma unroll
-        for (int r = 0; r < RB; ++r)
-          fa[set][u][r] = *reinterpret_cast<const s16x8_any *>(ar[r] + (s + u) * 32);
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-          fx[set][u][i] = *reinterpret_cast<const s16x8_any *>(xr[i] + (s + u) * 32);
-      }
-    };
-    auto multiply = [&](int set) MOE_INLINE {
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int r = 0; r < RB; ++r)
-#pragma unroll
-          for (int i = 0; i < MT; ++i)
-            acc[r][i] = D::mfma(fa[set][u][r], fx[set][u][i], acc[r][i]);
-    };
-    int b = 0;
-    if (whole > 0) load(0, 0);
-    for (; b + 2 <= whole; b += 2) {
-      load(1, (b + 1) * U);
-      multiply(0);
-      if (b + 2 < whole) load(0, (b + 2) * U);
-      multiply(1);
-    }
-    if (b < whole) multiply(0);
-    for (int s = whole * U; s < s1 - s0; ++s) {  // the rest, and K's own tail
-      const int in = g.K - (s0 + s) * 32 - fq * 8;
-      s16x8 ta[RB];
-#pragma unroll
-      for (int r = 0; r < RB; ++r) ta[r] = load8_raw(ar[r] + s * 32, 0, in);
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const s16x8 tx = load8_raw(xr[i] + s * 32, 0, in);
-#pragma unroll
-        for (int r = 0; r < RB; ++r) acc[r][i] = D::mfma(ta[r], tx, acc[r][i]);
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < RB; ++r)
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-        *reinterpret_cast<f32x4 *>(&part[wave][16 * i + fr][16 * r + 4 * fq]) = acc[r][i];
+    clear(acc);
+    stream_products<D, RB, MT, NS, STAGED>(acc, {g.a + a * g.stride + k0, g.lda, g.rank}, x, k,
+                                           lds + wave * RING);
+    __syncthreads();  // the waves' staging memory holds the sums now
+    P::put(part, wave, acc);
     __syncthreads();
     const float c = g.scale ? g.scale[a] : 1.f;
     for (int o = threadIdx.x; o < ROWS * 16 * RB; o += 64 * WAVES) {
       const int t = o / (16 * RB), r = o % (16 * RB);
-      if (!(mine >> t & 1) || r >= g.rank) continue;
-      float v = 0.f;
-#pragma unroll
-      for (int w = 0; w < WAVES; ++w) v += part[w][t][r];
-      g.s[(int64_t)(row0 + t) * g.rank + r] = v * c;
+      if ((mine >> t & 1) && r < g.rank)
+        g.s[(int64_t)(row0 + t) * g.lds + r] = P::sum(part, t, r) * c;
     }
-    __syncthreads();  // before the next adapter's sums
+    __syncthreads();  // before the next adapter's rows
   }
 #endif
 }
 
-// ------------------------------------------- the tokens of each adapter, in order
+// ------------------------------------------------- y of up to 64 rows, two launches
 
-constexpr int SORT_THREADS = 1024;
+// For a decode batch, bound by reading W and the adapters among its tokens once.
+// First launch: x times the rows of W and of each such A_a together, so that reading
+// the adapters costs no time of its own; k is split over the waves of `splits` blocks,
+// each of which leaves fp32 sums. Second launch: the sums added in their order, s B_a^T in
+// fp32 without halves, bias and residual, one rounding.
+constexpr int FEW_ROWS = 64;
+struct FewArgs {
+  const uint16_t *x, *w, *a, *b, *bias, *res;
+  int64_t ldx, ldw, lda, a_stride, ldb, b_stride, ldr, ldy;
+  const int32_t *ids;
+  const float *scale;
+  float *part_y, *part_s;  // [splits][M][N], [splits][M][rank]
+  float *s;                // [M, rank] or NULL
+  uint16_t *y;
+  int32_t M, N, K, rank, n, splits, per;  // per: k of a wave, a multiple of 64
+  int32_t w_tiles, rank_tiles;
+};
+constexpr int FEW_WAVES = 4;
 
-// perm: the tokens with an adapter, by adapter and then by number; offsets[a]: where
-// those of adapter a begin. A block for each adapter counts the ids below its own and
-// its own, and writes its tokens: two reads of the ids a block, and no atomics.
-__global__ __launch_bounds__(SORT_THREADS) void sort_ids_kernel(const int32_t *__restrict__ ids,
-                                                                int T, int n,
-                                                                int32_t *__restrict__ offsets,
-                                                                int32_t *__restrict__ perm) {
-  __shared__ int sums[SORT_THREADS], below;
-  const int a = blockIdx.x, t = threadIdx.x;
-  if (t == 0) below = 0;
-  __syncthreads();
-  const int each = (T + SORT_THREADS - 1) / SORT_THREADS;
-  const int lo = (int)min((int64_t)t * each, (int64_t)T), hi = (int)min((int64_t)lo + each, (int64_t)T);
-  int less = 0, same = 0;
-  for (int i = lo; i < hi; ++i) {
-    const int id = ids[i];
-    less += id >= 0 && id < a;
-    same += id == a;
+template <class D, int MT, int RB, int NS, bool STAGED>
+__global__ __launch_bounds__(64 * FEW_WAVES) void few_stream_kernel(const FewArgs g) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int ROWS = 16 * MT, TILE = 16 * RB, RING = STAGED ? Stream<MT, RB, NS>::BYTES : 0;
+  typedef Part<FEW_WAVES, RB, MT> P;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[most(FEW_WAVES * RING, P::BYTES)];
+  float *part = reinterpret_cast<float *>(lds);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int tile = blockIdx.x;
+  StreamRows rows = {g.w, g.ldw, g.N};
+  uint64_t mine = ~0ull;
+  const bool adapter = tile >= g.w_tiles;
+  if (adapter) {  // of the slot-th adapter among the tokens
+    const int slot = (tile - g.w_tiles) / g.rank_tiles;
+    tile = (tile - g.w_tiles) % g.rank_tiles;
+    int id = lane < g.M ? g.ids[lane] : -1;
+    if ((uint32_t)id >= (uint32_t)g.n) id = -1;
+    uint64_t todo = __ballot(id >= 0);
+    int a = 0;
+    for (int i = 0; todo && i <= slot; ++i) {
+      a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+      mine = __ballot(id == a);
+      if (i < slot) todo &= ~mine;
+    }
+    if (!todo) return;
+    rows = {g.a + a * g.a_stride, g.lda, g.rank};
   }
-  atomicAdd(&below, less);  // a sum of whole numbers: any order
-  sums[t] = same;
+  const int r0 = tile * TILE, n = rows.rows;
+  const int k0 = min(g.K, ((int)blockIdx.y * FEW_WAVES + wave) * g.per), k = min(g.K - k0, g.per);
+  rows.p += r0 * rows.ld + k0;
+  rows.rows -= r0;
+  f32x4 acc[RB][MT];
+  clear(acc);
+  stream_products<D, RB, MT, NS, STAGED>(acc, rows, {g.x + k0, g.ldx, g.M}, k, lds + wave * RING);
   __syncthreads();
-  for (int d = 1; d < SORT_THREADS; d *= 2) {  // inclusive sums
-    const int v = t >= d ? sums[t - d] : 0;
-    __syncthreads();
-    sums[t] += v;
-    __syncthreads();
+  P::put(part, wave, acc);
+  __syncthreads();
+  float *out = adapter ? g.part_s : g.part_y;
+  for (int o = threadIdx.x; o < ROWS * TILE; o += 64 * FEW_WAVES) {
+    const int t = o / TILE, r = o % TILE;
+    if (t < g.M && r0 + r < n && (mine >> t & 1))
+      out[((int64_t)blockIdx.y * g.M + t) * n + r0 + r] = P::sum(part, t, r);
   }
-  const int first = below;
-  if (t == 0) offsets[a] = first;
-  if (a == n - 1 && t == SORT_THREADS - 1) offsets[n] = first + sums[t];
-  int at = first + sums[t] - same;
-  for (int i = lo; i < hi; ++i)
-    if (ids[i] == a) perm[at++] = i;
+#endif
 }
 
-// ---------------------------------------------------------- transposed copies
+// A column of one token's y a thread.
+template <class D>
+__global__ __launch_bounds__(256) void few_finish_kernel(const FewArgs g) {
+  __shared__ __attribute__((aligned(16))) float s[MOE_ADAPTER_MAX_RANK];
+  const int t = blockIdx.y, n = blockIdx.x * 256 + threadIdx.x, at = min(n, g.N - 1);
+  const int id = g.ids[t];
+  const bool with = (uint32_t)id < (uint32_t)g.n;
+  float y = 0.f;
+  for (int k = 0; k < g.splits; ++k) y += g.part_y[((int64_t)k * g.M + t) * g.N + at];
+  if ((int)threadIdx.x < MOE_ADAPTER_MAX_RANK) {
+    float v = 0.f;
+    if (with && (int)threadIdx.x < g.rank) {
+      for (int k = 0; k < g.splits; ++k) v += g.part_s[((int64_t)k * g.M + t) * g.rank + threadIdx.x];
+      v *= g.scale ? g.scale[id] : 1.f;
+    }
+    s[threadIdx.x] = v;
+    if (g.s && blockIdx.x == 0 && (int)threadIdx.x < g.rank) g.s[(int64_t)t * g.rank + threadIdx.x] = v;
+  }
+  __syncthreads();
+  if (with) {
+    const uint16_t *b = g.b + id * g.b_stride + at * g.ldb;
+    float d = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < g.rank; k += 8) {
+      const f32x8 w = unpack8<D>(load8_raw(b, k, g.rank));
+      const f32x8 v = *reinterpret_cast<const f32x8_any *>(s + k);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d = fmaf(v[e], w[e], d);
+    }
+    y += d;
+  }
+  if (n >= g.N) return;
+  if (g.bias) y += to_f<D>(g.bias[n]);
+  if (g.res) y += to_f<D>(g.res[t * g.ldr + n]);
+  g.y[t * g.ldy + n] = from_f<D>(y);
+}
 
-// dst [cols, rows8] = src [rows, cols] transposed, zeros from rows to rows8, of the
-// adapters that have tokens: A for dx's product, whose operand needs the rank along
-// its rows, and B (rows and columns exchanged) for u's.
-struct TransposeArgs {
-  const uint16_t *src;
-  int64_t ld, stride;
-  uint16_t *dst;
-  int32_t rank, width, ld_dst;  // the long side's length
+// ------------------- the tokens of each adapter, in order, and transposed copies
+
+constexpr int PREP_THREADS = 1024, PREP_WAVES = PREP_THREADS / 64;
+
+// at [in, rank8] = A transposed of each adapter, for dx's product, whose operand needs
+// the rank along its rows; bt [rank, out8] = B transposed, for u's. NULL: not needed.
+// perm: the tokens with an adapter, by adapter and then by number; offsets[a]: where
+// those of adapter a begin. s4: s with rows of whole 16 bytes (NULL: not needed). zeros:
+// 16 bytes that the gradients' loads take for what is not there.
+struct PrepArgs {
+  const int32_t *ids;
+  int32_t *offsets, *perm;
+  const uint16_t *a, *b;
+  int64_t lda, a_stride, ldb, b_stride;
+  uint16_t *at, *bt;
+  const float *s;
+  float *s4, *zeros;
+  int32_t T, n, in, out, rank, rank4, rank8, out8;
+  int64_t block0, copy_block;  // numbers of the launch's first block, and of the first that copies s
 };
-// A [rank, in] -> [in, rank8]
-__device__ __forceinline__ void transpose_a(const TransposeArgs &g, int a, int c) {
-  const uint16_t *src = g.src + a * g.stride + c;
-  uint16_t *dst = g.dst + ((int64_t)a * g.width + c) * g.ld_dst;
-  for (int r = 0; r < g.rank; r += 8) {
+
+// A block for each adapter counts the ids below its own and its own, a wave 64 tokens
+// at a time by ballots, and then writes its tokens: two reads of the ids a block, no
+// order that changes. The blocks after those make the copies, 8 of the rank a thread.
+__global__ __launch_bounds__(PREP_THREADS) void prep_kernel(const PrepArgs g) {
+  __shared__ int sames[PREP_WAVES], lesses[PREP_WAVES];
+  const int64_t block = blockIdx.x + g.block0;
+  if (block < g.n) {
+    const int a = (int)block, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t each = ((int64_t)(g.T + PREP_THREADS - 1) / PREP_THREADS) * 64;
+    const int lo = (int)min(wave * each, (int64_t)g.T), hi = (int)min(lo + each, (int64_t)g.T);
+    int less = 0, same = 0;
+    constexpr int AT_ONCE = 8;  // groups of 64 whose ids are loaded together
+    int ids[AT_ONCE];
+    auto load_ids = [&](int i) MOE_INLINE {
+#pragma unroll
+      for (int q = 0; q < AT_ONCE; ++q) {
+        const int t = i + q * 64 + lane;
+        ids[q] = g.ids[min(t, hi - 1)];
+        if (t >= hi) ids[q] = -1;
+      }
+    };
+    for (int i = lo; i < hi; i += 64 * AT_ONCE) {
+      load_ids(i);
+#pragma unroll
+      for (int q = 0; q < AT_ONCE; ++q) {
+        less += __popcll(__ballot(ids[q] >= 0 && ids[q] < a));
+        same += __popcll(__ballot(ids[q] == a));
+      }
+    }
+    if (lane == 0) sames[wave] = same, lesses[wave] = less;
+    __syncthreads();
+    int first = 0, before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < PREP_WAVES; ++w) {
+      first += lesses[w];
+      before += w < wave ? sames[w] : 0;
+      total += sames[w];
+    }
+    if (a == 0 && threadIdx.x < 4 && g.zeros) g.zeros[threadIdx.x] = 0.f;
+    if (threadIdx.x == 0) {
+      g.offsets[a] = first;
+      if (a == g.n - 1) g.offsets[g.n] = first + total;
+    }
+    int at = first + before;
+    for (int i = lo; i < hi; i += 64 * AT_ONCE) {
+      if (hi - lo > 64 * AT_ONCE) load_ids(i);
+#pragma unroll
+      for (int q = 0; q < AT_ONCE; ++q) {
+        const uint64_t all = __ballot(ids[q] == a);
+        if (ids[q] == a) g.perm[at + __popcll(all & ((1ull << lane) - 1))] = i + q * 64 + lane;
+        at += __popcll(all);
+      }
+    }
+    return;
+  }
+  if (block >= g.copy_block) {
+    const int64_t i = (block - g.copy_block) * PREP_THREADS + threadIdx.x;
+    const int64_t t = i / g.rank4;
+    const int r = (int)(i % g.rank4);
+    if (t < g.T) g.s4[i] = r < g.rank ? g.s[t * g.rank + r] : 0.f;
+    return;
+  }
+  const int runs = g.rank8 / 8, a_items = g.at ? g.in * runs : 0, items = a_items + g.out * runs;
+  const int blocks = (items + PREP_THREADS - 1) / PREP_THREADS;
+  const int a = (int)((block - g.n) / blocks);
+  int i = (int)((block - g.n) % blocks) * PREP_THREADS + threadIdx.x;
+  if (i < a_items) {
+    const int c = i % g.in, r = i / g.in * 8;
+    const uint16_t *src = g.a + a * g.a_stride + c;
     s16x8 w = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
     for (int v = 0; v < 8; ++v)
-      if (r + v < g.rank) w[v] = (short)src[(r + v) * g.ld];
-    *reinterpret_cast<s16x8 *>(dst + r) = w;
-  }
-}
-// B [out, rank] -> [rank, out8]
-__device__ __forceinline__ void transpose_b(const TransposeArgs &g, int a, int c) {
-  const uint16_t *src = g.src + a * g.stride + c * g.ld;
-  uint16_t *dst = g.dst + (int64_t)a * g.rank * g.ld_dst + c;
-  for (int r = 0; r < g.rank; r += 8) {
-    const s16x8 w = load8_raw(src, r, g.rank);
+      if (r + v < g.rank) w[v] = (short)src[(r + v) * g.lda];
+    *reinterpret_cast<s16x8 *>(g.at + ((int64_t)a * g.in + c) * g.rank8 + r) = w;
+  } else if (i < items) {
+    i -= a_items;
+    const int c = i % g.out, r = i / g.out * 8;
+    const s16x8 w = load8_raw(g.b + a * g.b_stride + c * g.ldb, r, g.rank);
+    uint16_t *dst = g.bt + (int64_t)a * g.rank * g.out8 + c;
 #pragma unroll
     for (int v = 0; v < 8; ++v)
-      if (r + v < g.rank) dst[(int64_t)(r + v) * g.ld_dst] = (uint16_t)w[v];
+      if (r + v < g.rank) dst[(int64_t)(r + v) * g.out8] = (uint16_t)w[v];
   }
-}
-__global__ __launch_bounds__(256) void transpose_kernel(const TransposeArgs a, const TransposeArgs b,
-                                                        const int32_t *__restrict__ offsets, int n,
-                                                        int a_blocks) {
-  const int e = blockIdx.y;
-  if (offsets[e + 1] == offsets[e]) return;
-  const bool second = (int)blockIdx.x >= a_blocks;
-  const int c = (blockIdx.x - (second ? a_blocks : 0)) * 256 + threadIdx.x;
-  if (!second && c < a.width) transpose_a(a, e, c);
-  if (second && c < b.width) transpose_b(b, e, c);
 }
 
 // ------------------------------------------------------- the adapters' gradients
@@ -218,34 +429,55 @@ __global__ __launch_bounds__(256) void transpose_kernel(const TransposeArgs a, c
 // sum over the tokens t of adapter a of v[t, r] m[t, c]: dA with v = u and m = x, dB
 // (transposed) with v = s and m = dy.
 struct GradSide {
-  const uint16_t *m;
+  const uint16_t *m;  // rows 16-byte aligned
   int64_t ld;
-  const float *v;  // [T, rank]
-  float *part;     // [slots][rank][width4]
+  const float *v;     // [T, rank], rows ldv elements (whole 16 bytes) apart
+  float *part;        // [slots][rank][width4]
   int32_t width, width4, tiles;
 };
 struct GradArgs {
   GradSide side[2];
   const int32_t *offsets, *perm;
-  int32_t rank, n, chunk;  // sorted tokens of a block
+  const float *zeros;  // 16 bytes
+  int32_t rank, ldv, n, chunk;  // chunk: sorted tokens of a block
 };
 
-constexpr int GRAD_COLS = 256, GRAD_K = 64, GRAD_WAVES = 4;
+// 16 bytes a lane, each from its own address, to dst + 16 lane in LDS. As in lds_piece the
+// compiler is not told of the write: the kernel's own waits order it.
+__device__ __forceinline__ void lds_gather(const void *from, uint8_t *dst) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const uint32_t to = (uint32_t)(uintptr_t)(lds_ptr_t)dst;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from)
+               : "m0");
+#endif
+}
+
+constexpr int GRAD_COLS = 256, GRAD_K = 32, GRAD_WAVES = 4, GRAD_WINDOW = 1024;
 
 // A block takes 256 columns of m and `chunk` tokens of the sorted order, and adds
 // up each adapter among them apart: the part of adapter a in chunk k goes to slot
-// a + k, of which there is one for each pair that meets. 64 tokens at a time go through
-// LDS: m as it lies, read through the transposing LDS load, and v in two halves of the
-// type, transposed as it is written. In fp16, whose range v may pass, the 64
-// values of a column of v are taken at a power of two of their own.
-template <class D, int RB>
-__global__ __launch_bounds__(64 * GRAD_WAVES, RB <= 2 ? 2 : 1) void grad_kernel(const GradArgs g) {
+// a + k, of which there is one for each pair that meets. 32 tokens at a time go through
+// LDS, NS stages deep: m as it lies, read through the transposing LDS load, and v in fp32,
+// which each wave takes into two halves of the type in the registers of its fragments. In
+// fp16, whose range v may pass, the 32 values of a column of v are taken at a power
+// of two of their own. What is not there (tokens past the end, columns past the width or the
+// rank) is loaded from a few zeros, so that nothing a buffer happens to hold counts.
+template <class D, int RB, int NS>
+__global__ __launch_bounds__(64 * GRAD_WAVES, 2) void grad_kernel(const GradArgs g) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr bool SCALED = D::MAX_EXPONENT < 127;
-  constexpr int ROW = GRAD_COLS * 2, M_BYTES = GRAD_K * ROW, V_BYTES = 16 * RB * GRAD_K * 2;
-  __shared__ __attribute__((aligned(1024))) uint8_t m_lds[2][M_BYTES];
-  __shared__ __attribute__((aligned(1024))) uint8_t v_lds[2][2][V_BYTES];  // high, low
-  __shared__ int power[2][16 * RB];
+  constexpr int ROW = GRAD_COLS * 2, M_BYTES = GRAD_K * ROW;
+  constexpr int V_CHUNKS = 4 * RB, V_ROW = V_CHUNKS * 16, V_BYTES = GRAD_K * V_ROW;
+  constexpr int STAGE = M_BYTES + V_BYTES;
+  constexpr int M_LOADS = M_BYTES / 1024 / GRAD_WAVES;                          // of a wave
+  constexpr int V_PIECES = V_BYTES / 1024, V_LOADS = (V_PIECES + GRAD_WAVES - 1) / GRAD_WAVES;
+  constexpr int LOADS_MIN = M_LOADS + V_PIECES / GRAD_WAVES;
+  // waves side by side over the rank, each with RW 16s of it and J 16s of the columns: a
+  // wave converts what it multiplies
+  constexpr int WR = RB < 4 ? 1 : RB / 2, WC = GRAD_WAVES / WR, RW = RB / WR, J = 16 / WC;
+  static_assert(2 * (NS * STAGE + GRAD_WINDOW * 4) <= 160 * 1024, "two blocks to a compute unit");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * STAGE];
+  __shared__ int token_of[GRAD_WINDOW];
   const int lane = threadIdx.x & 63, fr = lane & 15, fq = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const bool second = (int)blockIdx.x >= g.side[0].tiles;
@@ -254,7 +486,7 @@ __global__ __launch_bounds__(64 * GRAD_WAVES, RB <= 2 ? 2 : 1) void grad_kernel(
   const int total = g.offsets[g.n];
   const int64_t first64 = (int64_t)blockIdx.y * g.chunk;
   if (first64 >= total) return;
-  const int first = (int)first64, last = min(first + g.chunk, total);
+  const int first = (int)first64, last = (int)min(first64 + g.chunk, (int64_t)total);
 
   // the adapter of the chunk's first token: the last one that begins at or before it
   int lo = 0, hi = g.n - 1;
@@ -263,137 +495,126 @@ __global__ __launch_bounds__(64 * GRAD_WAVES, RB <= 2 ? 2 : 1) void grad_kernel(
     if (g.offsets[mid] <= first) lo = mid; else hi = mid - 1;
   }
 
-  // this thread's pieces of a stage: 16 bytes of rows k0 + 8 q
-  const int k0 = threadIdx.x >> 5, piece = threadIdx.x & 31;
-  auto chunk_at = [&](int k, int c) MOE_INLINE { return k * ROW + ((c ^ swz<GRAD_COLS>(k)) * 16); };
-  // transposed reads: a lane's k-row and chunk of the wave's first 16 columns
+  // where this lane's pieces lie: m's are 2 rows of 32 chunks, v's 64 chunks of its rows
+  int m_row[M_LOADS], v_row[V_LOADS];
+  const uint16_t *m_at[M_LOADS];
+  const float *v_at[V_LOADS];
+#pragma unroll
+  for (int q = 0; q < M_LOADS; ++q) {
+    const int k = (q * GRAD_WAVES + wave) * 2 + (lane >> 5);
+    const int c = c0 + ((lane & 31) ^ swz<GRAD_COLS>(k)) * 8;
+    m_row[q] = k;
+    m_at[q] = c < sd.width ? sd.m + c : nullptr;
+  }
+#pragma unroll
+  for (int q = 0; q < V_LOADS; ++q) {
+    const int i = (q * GRAD_WAVES + wave) * 64 + lane;
+    v_row[q] = i / V_CHUNKS;
+    v_at[q] = i % V_CHUNKS * 4 < g.rank ? sd.v + i % V_CHUNKS * 4 : nullptr;
+  }
+  const int my_col = wave % WC * J * 16, my_rank = wave / WC * RW * 16;
+  // transposed reads: a lane's k-row and, in chunk c of it, the place of column 16 j
   const int tk = fq * 8 + (fr >> 2);
-  const uint32_t tr = tk * ROW + (((wave * 8) + ((fr & 3) >> 1)) ^ swz<GRAD_COLS>(tk)) * 16 + (fr & 1) * 8;
+  auto tr = [&](int j) MOE_INLINE {
+    const int c = my_col / 8 + 2 * j + ((fr & 3) >> 1);
+    return (uint32_t)(tk * ROW + (c ^ swz<GRAD_COLS>(tk)) * 16 + (fr & 1) * 8);
+  };
 
   for (int a = lo; a < g.n && g.offsets[a] < last; ++a) {
     const int begin = max(g.offsets[a], first), end = min(g.offsets[a + 1], last);
     if (begin >= end) continue;
-    const int stages = (end - begin + GRAD_K - 1) / GRAD_K;
-    f32x4 acc[RB][4];
+    f32x4 acc[RW][J];
 #pragma unroll
-    for (int r = 0; r < RB; ++r)
+    for (int r = 0; r < RW; ++r)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[r][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    int token[8], v_token;
-    s16x8 m[8];
-    f32x4 v[RB];
-    auto load_tokens = [&](int s) MOE_INLINE {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) token[q] = g.perm[min(begin + s * GRAD_K + k0 + 8 * q, end - 1)];
-      v_token = g.perm[min(begin + s * GRAD_K + lane, end - 1)];
-    };
-    // rows past the end are zeros on both sides
-    auto load_stage = [&](int s) MOE_INLINE {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        m[q] = s16x8{0, 0, 0, 0, 0, 0, 0, 0};
-        if (begin + s * GRAD_K + k0 + 8 * q < end)
-          m[q] = load8_raw(sd.m + (int64_t)token[q] * sd.ld, c0 + piece * 8, sd.width);
-      }
-#pragma unroll
-      for (int r = 0; r < RB; ++r) {  // this wave's 4 RB of the rank
-        const int at = (wave * RB + r) * 4;
-        v[r] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (begin + s * GRAD_K + lane < end) {
-          const float *p = sd.v + (int64_t)v_token * g.rank + at;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (at + e < g.rank) v[r][e] = p[e];
-        }
-      }
-    };
-    auto store_stage = [&](int buf) MOE_INLINE {
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        *reinterpret_cast<s16x8 *>(m_lds[buf] + chunk_at(k0 + 8 * q, piece)) = m[q];
-#pragma unroll
-      for (int r = 0; r < RB; ++r)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int at = (wave * RB + r) * 4 + e;
-          float f = v[r][e];
-          if constexpr (SCALED) {
-            float most = fabsf(f);
-#pragma unroll
-            for (int d = 1; d < 64; d *= 2) most = fmaxf(most, __shfl_xor(most, d));
-            const int p = exponent_for(most);
-            if (lane == 0) power[buf][at] = p;
-            f = __builtin_amdgcn_ldexpf(f, p);
-          }
-          const uint16_t h = from_f<D>(f);
-          const float fh = to_f<D>(h);
-          const int o = at * (GRAD_K * 2) + (((lane >> 3) ^ (at & 7)) * 16) + (lane & 7) * 2;
-          *reinterpret_cast<uint16_t *>(v_lds[buf][0] + o) = h;
-          *reinterpret_cast<uint16_t *>(v_lds[buf][1] + o) = from_f<D>(__builtin_isfinite(fh) ? f - fh : 0.f);
-        }
-    };
-    load_tokens(0);
-    load_stage(0);
-    if (stages > 1) load_tokens(1);
-    for (int s = 0; s < stages; ++s) {
-      const int buf = s & 1;
-      store_stage(buf);
-      if (s + 1 < stages) load_stage(s + 1);
-      if (s + 2 < stages) load_tokens(s + 2);
-      // the buffer's last readers, two stages ago, passed the barrier in between
+      for (int j = 0; j < J; ++j) acc[r][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int from = begin; from < end; from += GRAD_WINDOW) {
+      const int count = min(end - from, GRAD_WINDOW), stages = (count + GRAD_K - 1) / GRAD_K;
+      __syncthreads();  // everybody is done with the window before
+      for (int i = threadIdx.x; i < count; i += 64 * GRAD_WAVES) token_of[i] = g.perm[from + i];
       __syncthreads();
-      f32x4 sum[SCALED ? RB : 1][4];
-      if constexpr (SCALED) {
+      auto issue = [&](int s) MOE_INLINE {
+        uint8_t *to = lds + s % NS * STAGE;
 #pragma unroll
-        for (int r = 0; r < RB; ++r)
+        for (int q = 0; q < M_LOADS; ++q) {
+          const int i = s * GRAD_K + m_row[q];
+          const void *p = i < count && m_at[q] ? (const void *)(m_at[q] + token_of[min(i, count - 1)] * sd.ld)
+                                               : (const void *)g.zeros;
+          lds_gather(p, to + (q * GRAD_WAVES + wave) * 1024);
+        }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) sum[r][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-      }
+        for (int q = 0; q < V_LOADS; ++q) {
+          if (V_PIECES % GRAD_WAVES != 0 && q * GRAD_WAVES + wave >= V_PIECES) continue;
+          const int i = s * GRAD_K + v_row[q];
+          const void *p = i < count && v_at[q] ? (const void *)(v_at[q] + (int64_t)token_of[min(i, count - 1)] * g.ldv)
+                                               : (const void *)g.zeros;
+          lds_gather(p, to + M_BYTES + (q * GRAD_WAVES + wave) * 1024);
+        }
+      };
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        s16x8 fm[4];
+      for (int s = 0; s < NS - 1; ++s)
+        if (s < stages) issue(s);
+#pragma unroll 1
+      for (int s = 0; s < stages; ++s) {
+        if (s + NS - 1 <= stages)
+          wait_vmcnt_imm<LOADS_MIN *(NS - 2)>();
+        else
+          wait_vmcnt_imm<0>();
+        // every wave's loads of this stage are here, and its reads of the last one done
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (s + NS - 1 < stages) issue(s + NS - 1);
+        const uint8_t *m_lds = lds + s % NS * STAGE, *v_lds = m_lds + M_BYTES;
+        s16x8 fm[J];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint8_t *p = m_lds[buf] + (tr ^ (j * 32)) + ks * 32 * ROW;
+        for (int j = 0; j < J; ++j) {
+          const uint8_t *p = m_lds + tr(j);
           const s16x4 x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr_t)p);
           const s16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr_t)(p + 4 * ROW));
           fm[j] = __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7);
         }
 #pragma unroll
-        for (int r = 0; r < RB; ++r) {
-          const int row = 16 * r + fr;
-          const int o = row * (GRAD_K * 2) + (((ks * 4 + fq) ^ (row & 7)) * 16);
-          const s16x8 hi = *reinterpret_cast<const s16x8 *>(v_lds[buf][0] + o);
-          const s16x8 low = *reinterpret_cast<const s16x8 *>(v_lds[buf][1] + o);
+        for (int r = 0; r < RW; ++r) {
+          f32x8 v;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            f32x4 &to = SCALED ? sum[SCALED ? r : 0][j] : acc[r][j];
-            to = D::mfma(fm[j], low, to);
-            to = D::mfma(fm[j], hi, to);
+          for (int e = 0; e < 8; ++e)
+            v[e] = *reinterpret_cast<const float *>(v_lds + (fq * 8 + e) * V_ROW + (my_rank + 16 * r + fr) * 4);
+          int power = 0;
+          if constexpr (SCALED) {
+            float most = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(v[e]));
+            most = fmaxf(most, __shfl_xor(most, 16));
+            most = fmaxf(most, __shfl_xor(most, 32));
+            power = exponent_for(most);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = __builtin_amdgcn_ldexpf(v[e], power);
           }
-        }
-      }
-      if constexpr (SCALED) {
+          s16x8 high, low;
+          halves<D>(v, high, low);
 #pragma unroll
-        for (int r = 0; r < RB; ++r) {
-          const int p = -power[buf][16 * r + fr];
+          for (int j = 0; j < J; ++j) {
+            if constexpr (SCALED) {
+              f32x4 t = D::mfma(fm[j], low, f32x4{0.f, 0.f, 0.f, 0.f});
+              t = D::mfma(fm[j], high, t);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[r][j][e] += __builtin_amdgcn_ldexpf(sum[r][j][e], p);
+              for (int e = 0; e < 4; ++e) acc[r][j][e] += __builtin_amdgcn_ldexpf(t[e], -power);
+            } else {
+              acc[r][j] = D::mfma(fm[j], low, acc[r][j]);
+              acc[r][j] = D::mfma(fm[j], high, acc[r][j]);
+            }
+          }
         }
       }
     }
     float *part = sd.part + (int64_t)(a + blockIdx.y) * g.rank * sd.width4;
 #pragma unroll
-    for (int r = 0; r < RB; ++r)
+    for (int r = 0; r < RW; ++r)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = c0 + wave * 64 + 16 * j + 4 * fq, row = 16 * r + fr;
+      for (int j = 0; j < J; ++j) {
+        const int c = c0 + my_col + 16 * j + 4 * fq, row = my_rank + 16 * r + fr;
         if (row < g.rank && c < sd.width4)
           *reinterpret_cast<f32x4 *>(part + (int64_t)row * sd.width4 + c) = acc[r][j];
       }
-    __syncthreads();  // before the next adapter's stages
   }
 #endif
 }
@@ -412,27 +633,40 @@ __global__ __launch_bounds__(256) void grad_join_kernel(const JoinSide da, const
                                                         int rank, int chunk) {
   const int a = blockIdx.y, begin = offsets[a], end = offsets[a + 1];
   const int k0 = begin / chunk, k1 = end > begin ? (end - 1) / chunk : k0 - 1;
+  // four chunks' parts at a time, those past the last one without their value
+  constexpr int AT_ONCE = 4;
   f32x8 v = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if ((int)blockIdx.x < da.blocks) {
     const int runs = (da.width + 7) / 8;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int r = (int)(i / runs), c = (int)(i % runs) * 8;
     if (r >= rank) return;
-    for (int k = k0; k <= k1; ++k) {
-      const f32x8 p = load8_f32(da.part + ((int64_t)(a + k) * rank + r) * da.width4, c, da.width);
+    for (int k = k0; k <= k1; k += AT_ONCE) {
+      f32x8 p[AT_ONCE];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += p[e];
+      for (int q = 0; q < AT_ONCE; ++q)
+        p[q] = load8_f32(da.part + ((int64_t)(a + min(k + q, k1)) * rank + r) * da.width4, c, da.width);
+#pragma unroll
+      for (int q = 0; q < AT_ONCE; ++q)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = k + q <= k1 ? v[e] + p[q][e] : v[e];
     }
     store8<D>(da.out + a * da.stride + r * da.ld, c, da.width, v);
   } else {
     const int64_t i = (int64_t)(blockIdx.x - da.blocks) * 256 + threadIdx.x;
     const int r = (int)(i / db.width) * 8, c = (int)(i % db.width);
     if (r >= rank) return;
-    for (int k = k0; k <= k1; ++k) {
-      const float *p = db.part + ((int64_t)(a + k) * rank + r) * db.width4 + c;
+    for (int k = k0; k <= k1; k += AT_ONCE) {
+      float p[AT_ONCE][8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (r + e < rank) v[e] += p[(int64_t)e * db.width4];
+      for (int q = 0; q < AT_ONCE; ++q)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          p[q][e] = db.part[((int64_t)(a + min(k + q, k1)) * rank + min(r + e, rank - 1)) * db.width4 + c];
+#pragma unroll
+      for (int q = 0; q < AT_ONCE; ++q)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = k + q <= k1 ? v[e] + p[q][e] : v[e];
     }
     store8<D>(db.out + a * db.stride + c * db.ld, r, rank, v);
   }

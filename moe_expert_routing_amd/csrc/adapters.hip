@@ -35,32 +35,91 @@ static int check(const moe_adapter_linear_args *a, bool backward) {
   return check_matrix(a->db, O, R, n, true);
 }
 
-template <class D, int MT, int RB, int WAVES>
-static int shrink_as(const ShrinkArgs &g, int turns, hipStream_t st) {
-  const dim3 grid((uint32_t)((g.M + 16 * MT - 1) / (16 * MT)), (uint32_t)turns);
-  shrink_kernel<D, MT, RB, WAVES><<<grid, 64 * WAVES, 0, st>>>(g);
-  return hip_status();
+// Whether rows can be staged: their 16-byte pieces are aligned.
+static bool staged(const void *p, int64_t ld, int64_t stride, int cols) {
+  return ((uintptr_t)p & 15) == 0 && ((ld | stride | cols) & 7) == 0;
 }
-// Few rows: 16 a block, and blocks of their own for the adapters among them, of which
-// a decode batch has up to 16. More: 32, so that A is read half as often.
+
+template <class D, int MT, int RB, int WAVES, int NS>
+static int shrink_as(ShrinkArgs g, int turns, hipStream_t st) {
+  g.turns = turns;
+  const int64_t blocks = (int64_t)((g.M + 16 * MT - 1) / (16 * MT)) * turns;
+  const bool whole = staged(g.x, g.ldx, 0, g.K) && staged(g.a, g.lda, g.stride, g.K);
+  const auto kernel =
+      whole ? shrink_kernel<D, MT, RB, WAVES, NS, true> : shrink_kernel<D, MT, RB, WAVES, NS, false>;
+  return in_parts(blocks, 64 * WAVES, [&](int64_t first, uint32_t n) {
+    g.block0 = first;
+    kernel<<<n, 64 * WAVES, 0, st>>>(g);
+    return hip_status();
+  });
+}
+// Few rows: 16 a block, of which a decode batch has up to 16 adapters. More: 32, so that
+// A is read half as often.
 template <class D>
 static int shrink_of(const ShrinkArgs &g, hipStream_t st) {
   const int distinct = g.n < 16 ? g.n : 16;
-  const int turns = g.M <= 1024 ? distinct : g.M <= 4096 ? (distinct < 4 ? distinct : 4) : 1;
   const int rb = (g.rank + 15) / 16;
-  if (g.M <= 4096) {
-    if (rb == 1) return shrink_as<D, 1, 1, 16>(g, turns, st);
-    if (rb == 2) return shrink_as<D, 1, 2, 16>(g, turns, st);
-    if (rb <= 4) return shrink_as<D, 1, 4, 8>(g, turns, st);
-    return shrink_as<D, 1, 8, 8>(g, turns, st);
+  if (g.M <= 1024) {
+    if (rb == 1) return shrink_as<D, 1, 1, 8, 4>(g, distinct, st);
+    if (rb == 2) return shrink_as<D, 1, 2, 8, 3>(g, distinct, st);
+    if (rb <= 4) return shrink_as<D, 1, 4, 4, 3>(g, distinct, st);
+    return shrink_as<D, 1, 8, 4, 2>(g, distinct, st);
   }
-  if (rb == 1) return shrink_as<D, 2, 1, 8>(g, 1, st);
-  if (rb == 2) return shrink_as<D, 2, 2, 8>(g, 1, st);
-  if (rb <= 4) return shrink_as<D, 2, 4, 8>(g, 1, st);
-  return shrink_as<D, 1, 8, 8>(g, 1, st);
+  const int turns = distinct < 2 ? 1 : 2;
+  if (rb == 1) return shrink_as<D, 2, 1, 4, 3>(g, turns, st);
+  if (rb == 2) return shrink_as<D, 2, 2, 8, 2>(g, turns, st);
+  if (rb <= 4) return shrink_as<D, 2, 4, 4, 3>(g, turns, st);
+  return shrink_as<D, 1, 8, 4, 2>(g, turns, st);
 }
 static int shrink(int dtype, const ShrinkArgs &g, hipStream_t st) {
   return dtype == MOE_BF16 ? shrink_of<Bf16>(g, st) : shrink_of<F16>(g, st);
+}
+
+template <class D, int MT, int RB, int NS>
+static int few_as(FewArgs g, hipStream_t st) {
+  g.w_tiles = (g.N + 16 * RB - 1) / (16 * RB);
+  g.rank_tiles = (g.rank + 16 * RB - 1) / (16 * RB);
+  const int slots = g.n < g.M ? g.n : g.M;
+  const dim3 grid(g.w_tiles + slots * g.rank_tiles, g.splits);
+  const bool whole = staged(g.x, g.ldx, 0, g.K) && staged(g.w, g.ldw, 0, g.K) &&
+                     staged(g.a, g.lda, g.a_stride, g.K);
+  const auto kernel =
+      whole ? few_stream_kernel<D, MT, RB, NS, true> : few_stream_kernel<D, MT, RB, NS, false>;
+  kernel<<<grid, 64 * FEW_WAVES, 0, st>>>(g);
+  MOE_TRY(hip_status());
+  few_finish_kernel<D><<<dim3((g.N + 255) / 256, g.M), 256, 0, st>>>(g);
+  return hip_status();
+}
+template <class D>
+static int few_of(const FewArgs &g, hipStream_t st) {
+  if (g.M <= 16) return few_as<D, 1, 1, 4>(g, st);
+  if (g.M <= 32) return few_as<D, 2, 2, 3>(g, st);
+  return few_as<D, 4, 2, 2>(g, st);
+}
+static int run_few(const moe_adapter_linear_args *a, Arena &ws, hipStream_t st) {
+  FewArgs g = {};
+  g.M = (int)a->tokens, g.N = a->out, g.K = a->in, g.rank = a->rank, g.n = a->adapters;
+  // some 4096 waves, of at least 128 k
+  const int blocks = (g.K + 63) / 64, tile = g.M <= 16 ? 16 : 32;
+  const int tiles = (g.N + tile - 1) / tile;
+  int splits = 1024 / tiles;
+  splits = splits < 1 ? 1 : splits > 8 ? 8 : splits;
+  g.per = (blocks + splits * FEW_WAVES - 1) / (splits * FEW_WAVES);
+  if (g.per < 2) g.per = 2;  // blocks of 64
+  g.splits = (blocks + g.per * FEW_WAVES - 1) / (g.per * FEW_WAVES);  // none of them empty
+  g.per *= 64;
+  g.part_y = reinterpret_cast<float *>(ws.take((size_t)g.splits * g.M * g.N * sizeof(float)));
+  g.part_s = reinterpret_cast<float *>(ws.take((size_t)g.splits * g.M * g.rank * sizeof(float)));
+  if (ws.dry) return MOE_OK;
+  g.x = (const uint16_t *)a->x.p, g.ldx = a->x.ld;
+  g.w = (const uint16_t *)a->w.p, g.ldw = a->w.ld;
+  g.a = (const uint16_t *)a->a.p, g.lda = a->a.ld, g.a_stride = a->a.stride;
+  g.b = (const uint16_t *)a->b.p, g.ldb = a->b.ld, g.b_stride = a->b.stride;
+  g.bias = (const uint16_t *)a->bias.p;
+  g.res = (const uint16_t *)a->residual.p, g.ldr = a->residual.ld;
+  g.ids = a->ids, g.scale = a->scale, g.s = a->s;
+  g.y = (uint16_t *)a->y.p, g.ldy = a->y.ld;
+  return a->dtype == MOE_BF16 ? few_of<Bf16>(g, st) : few_of<F16>(g, st);
 }
 
 static int run_forward(const moe_adapter_linear_args *a, Arena &ws, hipStream_t st) {
@@ -68,6 +127,7 @@ static int run_forward(const moe_adapter_linear_args *a, Arena &ws, hipStream_t 
   const int I = a->in, O = a->out;
   int status = MOE_OK;
   if (T == 0) return MOE_OK;
+  if (T <= FEW_ROWS) return run_few(a, ws, st);
   const moe_expert_rows dense = {};
   const Plan plan = row_plan(dense, true, T, O, I);
   float *s = a->s ? a->s : reinterpret_cast<float *>(ws.take((size_t)T * a->rank * sizeof(float)));
@@ -79,7 +139,7 @@ static int run_forward(const moe_adapter_linear_args *a, Arena &ws, hipStream_t 
     k.x = (const uint16_t *)a->x.p, k.ldx = a->x.ld;
     k.a = (const uint16_t *)a->a.p, k.lda = a->a.ld, k.stride = a->a.stride;
     k.ids = a->ids, k.scale = a->scale, k.s = s;
-    k.M = (int)T, k.K = I, k.rank = a->rank, k.n = a->adapters;
+    k.M = (int)T, k.K = I, k.rank = k.lds = a->rank, k.n = a->adapters;
     MOE_TRY(shrink(a->dtype, k, st));
   }
   GemmArgs g = {};
@@ -90,25 +150,27 @@ static int run_forward(const moe_adapter_linear_args *a, Arena &ws, hipStream_t 
   g.bias = (const uint16_t *)a->bias.p;
   g.res = (const uint16_t *)a->residual.p, g.ldr = a->residual.ld;
   g.M = (int)T, g.N = O, g.K = I, g.act = MOE_ACT_NONE;
-  g.low = {a->ids, s, (const uint16_t *)a->b.p, a->b.ld, a->b.stride, a->adapters, a->rank};
+  g.low = {a->ids, s, (const uint16_t *)a->b.p, a->b.ld, a->b.stride, a->adapters, a->rank, a->rank};
   return run_product(a->dtype, LINEAR, plan, g, O, 0, ws, st);
 }
 
 // Tokens of a block of the gradients: some 512 blocks over both sides, and no fewer
-// than 256 tokens, below which the partial sums outweigh what they are made from.
-static int grad_chunk(int64_t tokens, int tiles) {
+// than 16 for each of the rank, where the partial sums are a quarter of what they are made
+// from.
+static int grad_chunk(int64_t tokens, int tiles, int rank) {
   const int64_t chunks = (512 + tiles - 1) / tiles;
-  const int64_t each = ((tokens + chunks - 1) / chunks + GRAD_K - 1) / GRAD_K * GRAD_K;
-  return (int)(each < 256 ? 256 : each);
+  int64_t each = (tokens + chunks - 1) / chunks;
+  each = each > 16 * rank ? each : 16 * rank;
+  return (int)((each + GRAD_K - 1) / GRAD_K * GRAD_K);
 }
 
 template <class D>
 static int grads_of(const GradArgs &g, dim3 grid, hipStream_t st) {
   const int rb = (g.rank + 15) / 16;
-  const auto kernel = rb == 1   ? grad_kernel<D, 1>
-                      : rb == 2 ? grad_kernel<D, 2>
-                      : rb <= 4 ? grad_kernel<D, 4>
-                                : grad_kernel<D, 8>;
+  const auto kernel = rb == 1   ? grad_kernel<D, 1, 4>
+                      : rb == 2 ? grad_kernel<D, 2, 3>
+                      : rb <= 4 ? grad_kernel<D, 4, 3>
+                                : grad_kernel<D, 8, 2>;
   kernel<<<grid, 64 * GRAD_WAVES, 0, st>>>(g);
   return hip_status();
 }
@@ -116,69 +178,84 @@ static int grads_of(const GradArgs &g, dim3 grid, hipStream_t st) {
 static int run_backward(const moe_adapter_linear_args *a, Arena &ws, hipStream_t st) {
   const int64_t T = a->tokens;
   const int I = a->in, O = a->out, R = a->rank, n = a->adapters;
-  const int R8 = round8(R), O8 = round8(O), I4 = (I + 3) & ~3, O4 = (O + 3) & ~3;
-  const bool dx = a->dx.p && T > 0, grads = a->da.p || a->db.p, needs_u = T > 0 && (a->dx.p || a->da.p);
+  const int R4 = (R + 3) & ~3, R8 = round8(R), O8 = round8(O), I4 = (I + 3) & ~3, O4 = (O + 3) & ~3;
+  const bool dx = a->dx.p && T > 0, da = a->da.p, db = a->db.p, needs_u = T > 0 && (a->dx.p || da);
   const bool bf = a->dtype == MOE_BF16;
   int status = MOE_OK;
-  if (!dx && !grads) return MOE_OK;
+  if (!dx && !da && !db) return MOE_OK;
   int32_t *offsets = reinterpret_cast<int32_t *>(ws.take((size_t)(n + 1) * 4));
   int32_t *perm = reinterpret_cast<int32_t *>(ws.take((size_t)T * 4));
+  float *zeros = reinterpret_cast<float *>(ws.take(16));
   uint16_t *at = dx ? ws.take((size_t)n * I * R8 * 2) : nullptr;
   uint16_t *bt = needs_u ? ws.take((size_t)n * R * O8 * 2) : nullptr;
-  float *u = needs_u ? reinterpret_cast<float *>(ws.take((size_t)T * R * 4)) : nullptr;
+  float *u = needs_u ? reinterpret_cast<float *>(ws.take((size_t)T * R4 * 4)) : nullptr;
+  // s where its rows are whole 16 bytes, else a copy of it whose rows are
+  const bool copy_s = db && T > 0 && (R != R4 || (uintptr_t)a->s % 16 != 0);
+  float *s4 = copy_s ? reinterpret_cast<float *>(ws.take((size_t)T * R4 * 4)) : nullptr;
+  // dy is an operand of dx and of dB, x of dA
+  Operand dy = {}, x = {}, w = {};
+  if (dx || db) dy = operand(a->dy, T, O, 1, ws, st, &status);
+  if (da) x = operand(a->x, T, I, 1, ws, st, &status);
+  if (dx) w = operand(a->w, O, I, 1, ws, st, &status);
+  if (status != MOE_OK) return status;
   if (!ws.dry) {
-    sort_ids_kernel<<<n, SORT_THREADS, 0, st>>>(a->ids, (int)T, n, offsets, perm);
-    MOE_TRY(hip_status());
+    PrepArgs p = {};
+    p.ids = a->ids, p.offsets = offsets, p.perm = perm, p.T = (int)T, p.n = n;
+    p.a = (const uint16_t *)a->a.p, p.lda = a->a.ld, p.a_stride = a->a.stride;
+    p.b = (const uint16_t *)a->b.p, p.ldb = a->b.ld, p.b_stride = a->b.stride;
+    p.at = at, p.bt = bt, p.in = I, p.out = O, p.rank = R, p.rank4 = R4, p.rank8 = R8, p.out8 = O8;
+    p.s = a->s, p.s4 = s4, p.zeros = zeros;
+    const int64_t items = (int64_t)((dx ? I : 0) + (needs_u ? O : 0)) * (R8 / 8);
+    p.copy_block = n + n * ((items + PREP_THREADS - 1) / PREP_THREADS);
+    const int64_t copies = copy_s ? (T * R4 + PREP_THREADS - 1) / PREP_THREADS : 0;
+    MOE_TRY(in_parts(p.copy_block + copies, PREP_THREADS, [&](int64_t first, uint32_t blocks) {
+      p.block0 = first;
+      prep_kernel<<<blocks, PREP_THREADS, 0, st>>>(p);
+      return hip_status();
+    }));
   }
   if (needs_u && !ws.dry) {
-    const TransposeArgs ta = {(const uint16_t *)a->a.p, a->a.ld, a->a.stride, at, R, I, R8};
-    const TransposeArgs tb = {(const uint16_t *)a->b.p, a->b.ld, a->b.stride, bt, R, O, O8};
-    const int a_blocks = dx ? (I + 255) / 256 : 0;
-    transpose_kernel<<<dim3(a_blocks + (O + 255) / 256, n), 256, 0, st>>>(ta, tb, offsets, n, a_blocks);
-    MOE_TRY(hip_status());
     ShrinkArgs k = {};
     k.x = (const uint16_t *)a->dy.p, k.ldx = a->dy.ld;
     k.a = bt, k.lda = O8, k.stride = (int64_t)R * O8;
     k.ids = a->ids, k.scale = a->scale, k.s = u;
-    k.M = (int)T, k.K = O, k.rank = R, k.n = n;
+    k.M = (int)T, k.K = O, k.rank = R, k.lds = R4, k.n = n;
     MOE_TRY(shrink(a->dtype, k, st));
   }
   if (dx) {
     const moe_expert_rows dense = {};
-    const Operand dy = operand(a->dy, T, O, 1, ws, st, &status);
-    const Operand w = operand(a->w, O, I, 1, ws, st, &status);
-    if (status != MOE_OK) return status;
     GemmArgs g = {};
     g.segs = 1;
     g.a = dy.p, g.lda = dy.ld, g.a_rows = T;
     g.b0 = w.p, g.ldb0 = w.ld;
     g.c0 = (uint16_t *)a->dx.p, g.ldc0 = a->dx.ld;
     g.M = (int)T, g.N = I, g.K = O;
-    g.low = {a->ids, u, at, R8, (int64_t)I * R8, n, R};
+    g.low = {a->ids, u, at, R8, (int64_t)I * R8, n, R, R4};
     MOE_TRY(run_product(a->dtype, DGRAD, row_plan(dense, false, T, I, O), g, I, 0, ws, st));
   }
-  if (!grads) return MOE_OK;
-  const int a_tiles = a->da.p ? (I + GRAD_COLS - 1) / GRAD_COLS : 0;
-  const int b_tiles = a->db.p ? (O + GRAD_COLS - 1) / GRAD_COLS : 0;
-  const int chunk = grad_chunk(T, a_tiles + b_tiles);
+  if (!da && !db) return MOE_OK;
+  const int a_tiles = da ? (I + GRAD_COLS - 1) / GRAD_COLS : 0;
+  const int b_tiles = db ? (O + GRAD_COLS - 1) / GRAD_COLS : 0;
+  const int chunk = grad_chunk(T, a_tiles + b_tiles, R);
   const int64_t chunks = (T + chunk - 1) / chunk, slots = chunks + n - 1;
   GradArgs g = {};
-  g.side[0] = {(const uint16_t *)a->x.p, a->x.ld, u, nullptr, I, I4, a_tiles};
-  g.side[1] = {(const uint16_t *)a->dy.p, a->dy.ld, a->s, nullptr, O, O4, b_tiles};
-  if (a->da.p) g.side[0].part = reinterpret_cast<float *>(ws.take((size_t)slots * R * I4 * 4));
-  if (a->db.p) g.side[1].part = reinterpret_cast<float *>(ws.take((size_t)slots * R * O4 * 4));
+  g.side[0] = {x.p, x.ld, u, nullptr, I, I4, a_tiles};
+  g.side[1] = {dy.p, dy.ld, s4 ? s4 : a->s, nullptr, O, O4, b_tiles};
+  if (da) g.side[0].part = reinterpret_cast<float *>(ws.take((size_t)slots * R * I4 * 4));
+  if (db) g.side[1].part = reinterpret_cast<float *>(ws.take((size_t)slots * R * O4 * 4));
   if (ws.dry) return MOE_OK;
-  g.offsets = offsets, g.perm = perm, g.rank = R, g.n = n, g.chunk = chunk;
+  g.offsets = offsets, g.perm = perm, g.zeros = zeros;
+  g.rank = R, g.ldv = R4, g.n = n, g.chunk = chunk;
   if (T > 0) {
     const dim3 grid(a_tiles + b_tiles, (uint32_t)chunks);
     MOE_TRY(bf ? grads_of<Bf16>(g, grid, st) : grads_of<F16>(g, grid, st));
   }
-  const int64_t a_runs = a->da.p ? (int64_t)R * ((I + 7) / 8) : 0;
-  const int64_t b_runs = a->db.p ? (int64_t)((R + 7) / 8) * O : 0;
-  const JoinSide da = {g.side[0].part, (uint16_t *)a->da.p, a->da.ld, a->da.stride, I, I4, (int)((a_runs + 255) / 256)};
-  const JoinSide db = {g.side[1].part, (uint16_t *)a->db.p, a->db.ld, a->db.stride, O, O4, (int)((b_runs + 255) / 256)};
+  const int64_t a_runs = da ? (int64_t)R * ((I + 7) / 8) : 0;
+  const int64_t b_runs = db ? (int64_t)((R + 7) / 8) * O : 0;
+  const JoinSide ja = {g.side[0].part, (uint16_t *)a->da.p, a->da.ld, a->da.stride, I, I4, (int)((a_runs + 255) / 256)};
+  const JoinSide jb = {g.side[1].part, (uint16_t *)a->db.p, a->db.ld, a->db.stride, O, O4, (int)((b_runs + 255) / 256)};
   const auto kernel = bf ? grad_join_kernel<Bf16> : grad_join_kernel<F16>;
-  kernel<<<dim3(da.blocks + db.blocks, n), 256, 0, st>>>(da, db, offsets, R, chunk);
+  kernel<<<dim3(ja.blocks + jb.blocks, n), 256, 0, st>>>(ja, jb, offsets, R, chunk);
   return hip_status();
 }
 

@@ -38,7 +38,7 @@ static int launch(GemmArgs g, hipStream_t st) {
   });
 }
 
-template <class D, int MODE, int KW, bool LOW = false>
+template <class D, int MODE, int KW>
 static int launch_skinny_kw(GemmArgs g, hipStream_t st) {
   constexpr int COLS = SKINNY_WAVES / KW * (MODE == GATED ? 8 : 16);
   g.m_tiles = (g.M + 15) / 16;
@@ -48,8 +48,7 @@ static int launch_skinny_kw(GemmArgs g, hipStream_t st) {
   constexpr bool GATHERS = MODE == GATED && KW < 8;  // 8 waves: dense calls alone
   if (!GATHERS && g.r.row_entry) return MOE_ERR_UNSUPPORTED;
   const auto kernel =
-      g.r.row_entry ? skinny_kernel<D, MODE, KW, 4, GATHERS, LOW>
-                    : skinny_kernel<D, MODE, KW, 4, false, LOW>;
+      g.r.row_entry ? skinny_kernel<D, MODE, KW, 4, GATHERS> : skinny_kernel<D, MODE, KW, 4, false>;
   return in_parts(blocks, 64 * SKINNY_WAVES, [&](int64_t first, uint32_t n) {
     g.block0 = (uint32_t)first;
     kernel<<<n, 64 * SKINNY_WAVES, 0, st>>>(g);
@@ -102,11 +101,6 @@ static int launch_low_kind(int kind, const GemmArgs &g, hipStream_t st) {
     case TILE_128: return launch<D, MODE, Tile128, true>(g, st);
     case TILE_64: return launch<D, MODE, Tile64, true>(g, st);
     case TILE_32: return launch<D, MODE, Tile32, true>(g, st);
-  }
-  if constexpr (MODE == LINEAR) {
-    if (kind == TILE_16)
-      return g.N / 16 >= 384 ? launch_skinny_kw<D, MODE, 4, true>(g, st)
-                             : launch_skinny_kw<D, MODE, 8, true>(g, st);
   }
   return MOE_ERR_UNSUPPORTED;
 }

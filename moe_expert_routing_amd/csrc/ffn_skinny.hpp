@@ -23,7 +23,7 @@ namespace moe_ffn {
 
 constexpr int SKINNY_WAVES = 8;
 
-template <class D, int MODE, int KW, int U, bool GATHER, bool LOW = false>
+template <class D, int MODE, int KW, int U, bool GATHER>
 __global__ __launch_bounds__(64 * SKINNY_WAVES) void skinny_kernel(const GemmArgs g) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int GW = SKINNY_WAVES / KW, NC = MODE == GATED ? 8 : 16, BM = 16;
@@ -126,11 +126,6 @@ __global__ __launch_bounds__(64 * SKINNY_WAVES) void skinny_kernel(const GemmArg
         const f32x8 b = load8<D>(g.bias + e * g.bias_stride, n, g.N);
 #pragma unroll
         for (int v = 0; v < 8; ++v) z[v] += b[v];
-      }
-      if constexpr (LOW) {
-        const f32x8 d = low_rank_run<D>(g.low, m, n, g.N);
-#pragma unroll
-        for (int v = 0; v < 8; ++v) z[v] += d[v];
       }
       if (g.pre) store8<D>(g.pre + m * g.ldp, n, g.N, z);
       z = act_value(z, g.act);  // 0 stays 0

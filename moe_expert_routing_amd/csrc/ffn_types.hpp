@@ -183,10 +183,10 @@ enum Mode { GATED = 0, LINEAR = 1, DGRAD = 2, WGRAD = 3 };
 // the rows whose id is 0 .. n - 1.
 struct LowRank {
   const int32_t *ids;  // [M]; NULL: none
-  const float *s;      // [M, rank]
+  const float *s;      // [M, rank], rows lds elements apart
   const uint16_t *b;   // [N, rank] of each adapter
   int64_t ldb, stride;
-  int32_t n, rank;
+  int32_t n, rank, lds;
 };
 
 // What one product kernel gets. C[m, n] = sum over k of A(m, k) B(n, k).
