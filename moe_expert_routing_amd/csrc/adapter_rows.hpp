@@ -11,8 +11,9 @@ namespace moe_adapter {
 
 using namespace moe_ffn;
 
-// acc[r][i] += rows of a times rows of x over k elements, for products whose operands
-// have few rows: 16 RB rows of a, 16 MT of x, each wave on its own range of k.
+// acc[r][i] += rows of the operands a[0 .. NA - 1] times rows of x over k elements, for
+// products whose operands have few rows: 16 RB rows of each a, 16 MT of x, each wave on
+// its own range of k.
 //
 // What a compute unit can take in depends on how its lanes ask. Measured with
 // one block alone, 672 KB of 14 KB rows from L2: 5.7 us contiguous, 11 with loads of 8
@@ -35,19 +36,23 @@ struct StreamRows {
   int rows;  // at least 1; rows past them repeat the last one
 };
 
-template <class D, int RB, int MT, int NS, bool STAGED>
-__device__ __forceinline__ void stream_products(f32x4 (&acc)[RB][MT], const StreamRows &a,
+template <class D, int NA, int RB, int MT, int NS, bool STAGED>
+__device__ __forceinline__ void stream_products(f32x4 (&acc)[NA * RB][MT], const StreamRows (&a)[NA],
                                                 const StreamRows &x, int k, uint8_t *lds) {
 #if defined(__HIP_DEVICE_COMPILE__)
   const int lane = threadIdx.x & 63, fr = lane & 15, fq = lane >> 4;
   if constexpr (STAGED) {
-    typedef Stream<MT, RB, NS> S;
+    constexpr int F = NA * RB;  // fragments of the a
+    typedef Stream<MT, F, NS> S;
     const int chunk = (lane & 7) ^ (lane >> 3);
     uint32_t off[S::PIECES];  // bytes, below 2^31 (128 rows of MOE_FFN_MAX_LD)
+    auto operand_of = [&](int q) MOE_INLINE -> const StreamRows & {
+      return q < 2 * F ? a[q / (2 * RB) % NA] : x;
+    };
 #pragma unroll
     for (int q = 0; q < S::PIECES; ++q) {
-      const StreamRows &s = q < 2 * RB ? a : x;
-      const int row = (q < 2 * RB ? q : q - 2 * RB) * 8 + (lane >> 3);
+      const StreamRows &s = operand_of(q);
+      const int row = (q < 2 * F ? q % (2 * RB) : q - 2 * F) * 8 + (lane >> 3);
       off[q] = (uint32_t)(min(row, s.rows - 1) * s.ld + chunk * 8) * 2;
     }
     const int blocks = (k + 63) / 64;
@@ -55,7 +60,7 @@ __device__ __forceinline__ void stream_products(f32x4 (&acc)[RB][MT], const Stre
       const bool past = s * 64 + chunk * 8 >= k;
 #pragma unroll
       for (int q = 0; q < S::PIECES; ++q)
-        lds_piece<true>(reinterpret_cast<const uint8_t *>((q < 2 * RB ? a.p : x.p) + s * 64),
+        lds_piece<true>(reinterpret_cast<const uint8_t *>(operand_of(q).p + s * 64),
                         past ? PAST : off[q], lds + (s % NS * S::PIECES + q) * 1024);
     };
 #pragma unroll
@@ -64,11 +69,11 @@ __device__ __forceinline__ void stream_products(f32x4 (&acc)[RB][MT], const Stre
     for (int s = 0; s < blocks; ++s) {
       wait_vmcnt_imm<S::PIECES *(NS - 1)>();
       const uint8_t *from = lds + s % NS * S::PIECES * 1024;
-      s16x8 f[2][RB + MT];
+      s16x8 f[2][F + MT];
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-        for (int q = 0; q < RB + MT; ++q)
+        for (int q = 0; q < F + MT; ++q)
           f[ks][q] = *reinterpret_cast<const s16x8 *>(from + q * 2048 + fr * 128 +
                                                       (((ks * 4 + fq) ^ (fr & 7)) * 16));
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before it is filled again
@@ -76,40 +81,41 @@ __device__ __forceinline__ void stream_products(f32x4 (&acc)[RB][MT], const Stre
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-        for (int r = 0; r < RB; ++r)
+        for (int r = 0; r < F; ++r)
 #pragma unroll
-          for (int i = 0; i < MT; ++i) acc[r][i] = D::mfma(f[ks][r], f[ks][RB + i], acc[r][i]);
+          for (int i = 0; i < MT; ++i) acc[r][i] = D::mfma(f[ks][r], f[ks][F + i], acc[r][i]);
     }
     wait_vmcnt_imm<0>();  // the zeros still on their way
   } else {
-    const uint16_t *ar[RB], *xr[MT];
+    const uint16_t *ar[NA * RB], *xr[MT];
 #pragma unroll
-    for (int r = 0; r < RB; ++r) ar[r] = a.p + min(16 * r + fr, a.rows - 1) * a.ld + fq * 8;
+    for (int r = 0; r < NA * RB; ++r)
+      ar[r] = a[r / RB].p + min(16 * (r % RB) + fr, a[r / RB].rows - 1) * a[r / RB].ld + fq * 8;
 #pragma unroll
     for (int i = 0; i < MT; ++i) xr[i] = x.p + min(16 * i + fr, x.rows - 1) * x.ld + fq * 8;
     int s = 0;
 #pragma unroll 4
     for (; s + 32 <= k; s += 32) {
-      s16x8 fa[RB];
+      s16x8 fa[NA * RB];
 #pragma unroll
-      for (int r = 0; r < RB; ++r) fa[r] = *reinterpret_cast<const s16x8_any *>(ar[r] + s);
+      for (int r = 0; r < NA * RB; ++r) fa[r] = *reinterpret_cast<const s16x8_any *>(ar[r] + s);
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         const s16x8 fx = *reinterpret_cast<const s16x8_any *>(xr[i] + s);
 #pragma unroll
-        for (int r = 0; r < RB; ++r) acc[r][i] = D::mfma(fa[r], fx, acc[r][i]);
+        for (int r = 0; r < NA * RB; ++r) acc[r][i] = D::mfma(fa[r], fx, acc[r][i]);
       }
     }
     if (s < k) {
       const int left = k - s - fq * 8;
-      s16x8 fa[RB];
+      s16x8 fa[NA * RB];
 #pragma unroll
-      for (int r = 0; r < RB; ++r) fa[r] = load8_raw(ar[r] + s, 0, left);
+      for (int r = 0; r < NA * RB; ++r) fa[r] = load8_raw(ar[r] + s, 0, left);
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         const s16x8 fx = load8_raw(xr[i] + s, 0, left);
 #pragma unroll
-        for (int r = 0; r < RB; ++r) acc[r][i] = D::mfma(fa[r], fx, acc[r][i]);
+        for (int r = 0; r < NA * RB; ++r) acc[r][i] = D::mfma(fa[r], fx, acc[r][i]);
       }
     }
   }
@@ -120,13 +126,14 @@ __device__ __forceinline__ void stream_products(f32x4 (&acc)[RB][MT], const Stre
 template <int WAVES, int RB, int MT>
 struct Part {
   static constexpr int LD = 16 * RB + 4, BYTES = WAVES * 16 * MT * LD * 4;
-  static __device__ __forceinline__ void put(float *part, int wave, const f32x4 (&acc)[RB][MT]) {
+  template <int F>
+  static __device__ __forceinline__ void put(float *part, int wave, const f32x4 (&acc)[F][MT], int first) {
     const int lane = threadIdx.x & 63, fr = lane & 15, fq = lane >> 4;
 #pragma unroll
     for (int r = 0; r < RB; ++r)
 #pragma unroll
       for (int i = 0; i < MT; ++i)
-        *reinterpret_cast<f32x4 *>(part + (wave * 16 * MT + 16 * i + fr) * LD + 16 * r + 4 * fq) = acc[r][i];
+        *reinterpret_cast<f32x4 *>(part + (wave * 16 * MT + 16 * i + fr) * LD + 16 * r + 4 * fq) = acc[first + r][i];
   }
   // of row t and column r, in the order of the waves
   static __device__ __forceinline__ float sum(const float *part, int t, int r) {
@@ -159,19 +166,20 @@ struct ShrinkArgs {
 };
 
 // A block takes 16 MT rows, its waves share K and their sums meet in LDS. For each
-// adapter among the rows the block goes through K once; the blocks of `turns` rounds
-// over the rows share the adapters of a block's rows. Requests lie together, so a
-// prompt's rows have one or two and the second round's blocks mostly none; a decode
-// batch's rows may have 16. (The rounds follow each other: with the blocks of the same
-// rows side by side every second one ends at once, and as they go to the XCDs in turn,
-// half of these stood idle: 66 us instead of 35.)
-template <class D, int MT, int RB, int WAVES, int NS, bool STAGED>
+// adapter among the rows the block goes through K once, or with NS2 for two of them
+// at a time (that many stages then): requests lie together, so a prompt's rows have one
+// or two, and with one block to a compute unit those that went through K twice took as
+// long again as all others (8192 rows of 7168, 16 requests: 33 us). A decode batch's
+// rows may have 16, which the blocks of `turns` rounds over the rows share. (The rounds
+// follow each other: with the blocks of the same rows side by side every second one ends
+// at once, and as they go to the XCDs in turn, half of these stood idle: 66 us.)
+template <class D, int MT, int RB, int WAVES, int NS, int NS2, bool STAGED>
 __global__ __launch_bounds__(64 * WAVES) void shrink_kernel(const ShrinkArgs g) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  constexpr int ROWS = 16 * MT, RING = STAGED ? Stream<MT, RB, NS>::BYTES : 0;
+  constexpr int ROWS = 16 * MT, NA = NS2 ? 2 : 1;
+  constexpr int RING = STAGED ? most(Stream<MT, RB, NS>::BYTES, NS2 ? Stream<MT, 2 * RB, NS2 ? NS2 : 1>::BYTES : 0) : 0;
   typedef Part<WAVES, RB, MT> P;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[most(WAVES * RING, P::BYTES)];
-  float *part = reinterpret_cast<float *>(lds);
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[most(WAVES * RING, NA * P::BYTES)];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t block = (uint32_t)(blockIdx.x + g.block0);
@@ -190,23 +198,50 @@ __global__ __launch_bounds__(64 * WAVES) void shrink_kernel(const ShrinkArgs g) 
   const int k0 = min(g.K, wave * per), k = min(g.K - k0, per);
   const StreamRows x = {g.x + row0 * g.ldx + k0, g.ldx, g.M - row0};
   uint64_t todo = with;
-  for (int turn = 0; todo; ++turn) {
+  auto next = [&](uint64_t &mine) MOE_INLINE {
     const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-    const uint64_t mine = __ballot(id == a);
+    mine = __ballot(id == a);
     todo &= ~mine;
-    if (turn % g.turns != my_turn) continue;
-    f32x4 acc[RB][MT];
-    clear(acc);
-    stream_products<D, RB, MT, NS, STAGED>(acc, {g.a + a * g.stride + k0, g.lda, g.rank}, x, k,
-                                           lds + wave * RING);
-    __syncthreads();  // the waves' staging memory holds the sums now
-    P::put(part, wave, acc);
-    __syncthreads();
+    return a;
+  };
+  auto rows_of = [&](int a) MOE_INLINE {
+    return StreamRows{g.a + a * g.stride + k0, g.lda, g.rank};
+  };
+  auto write = [&](int a, uint64_t mine, const float *part) MOE_INLINE {
     const float c = g.scale ? g.scale[a] : 1.f;
     for (int o = threadIdx.x; o < ROWS * 16 * RB; o += 64 * WAVES) {
       const int t = o / (16 * RB), r = o % (16 * RB);
       if ((mine >> t & 1) && r < g.rank)
         g.s[(int64_t)(row0 + t) * g.lds + r] = P::sum(part, t, r) * c;
+    }
+  };
+  float *part = reinterpret_cast<float *>(lds), *part1 = part + P::BYTES / 4;
+  for (int turn = 0; todo; ++turn) {
+    uint64_t mine, mine1 = 0;
+    const int a = next(mine);
+    if (turn % g.turns != my_turn) continue;
+    if (NS2 && todo) {
+      const int a1 = next(mine1);
+      f32x4 acc[NA * RB][MT];
+      clear(acc);
+      const StreamRows rows[2] = {rows_of(a), rows_of(a1)};
+      if constexpr (NS2 > 0)
+        stream_products<D, 2, RB, MT, NS2, STAGED>(acc, rows, x, k, lds + wave * RING);
+      __syncthreads();  // the waves' staging memory holds the sums now
+      P::put(part, wave, acc, 0);
+      if constexpr (NS2 > 0) P::put(part1, wave, acc, RB);
+      __syncthreads();
+      write(a, mine, part);
+      write(a1, mine1, part1);
+    } else {
+      f32x4 acc[RB][MT];
+      clear(acc);
+      const StreamRows rows[1] = {rows_of(a)};
+      stream_products<D, 1, RB, MT, NS, STAGED>(acc, rows, x, k, lds + wave * RING);
+      __syncthreads();
+      P::put(part, wave, acc, 0);
+      __syncthreads();
+      write(a, mine, part);
     }
     __syncthreads();  // before the next adapter's rows
   }
@@ -268,9 +303,10 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void few_stream_kernel(const FewArg
   rows.rows -= r0;
   f32x4 acc[RB][MT];
   clear(acc);
-  stream_products<D, RB, MT, NS, STAGED>(acc, rows, {g.x + k0, g.ldx, g.M}, k, lds + wave * RING);
+  const StreamRows operand[1] = {rows};
+  stream_products<D, 1, RB, MT, NS, STAGED>(acc, operand, {g.x + k0, g.ldx, g.M}, k, lds + wave * RING);
   __syncthreads();
-  P::put(part, wave, acc);
+  P::put(part, wave, acc, 0);
   __syncthreads();
   float *out = adapter ? g.part_s : g.part_y;
   for (int o = threadIdx.x; o < ROWS * TILE; o += 64 * FEW_WAVES) {
@@ -406,7 +442,7 @@ __global__ __launch_bounds__(PREP_THREADS) void prep_kernel(const PrepArgs g) {
   const int a = (int)((block - g.n) / blocks);
   int i = (int)((block - g.n) % blocks) * PREP_THREADS + threadIdx.x;
   if (i < a_items) {
-    const int c = i % g.in, r = i / g.in * 8;
+    const int c = i / runs, r = i % runs * 8;  // a row's 16-byte runs side by side
     const uint16_t *src = g.a + a * g.a_stride + c;
     s16x8 w = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
@@ -415,7 +451,7 @@ __global__ __launch_bounds__(PREP_THREADS) void prep_kernel(const PrepArgs g) {
     *reinterpret_cast<s16x8 *>(g.at + ((int64_t)a * g.in + c) * g.rank8 + r) = w;
   } else if (i < items) {
     i -= a_items;
-    const int c = i % g.out, r = i / g.out * 8;
+    const int c = i / runs, r = i % runs * 8;
     const s16x8 w = load8_raw(g.b + a * g.b_stride + c * g.ldb, r, g.rank);
     uint16_t *dst = g.bt + (int64_t)a * g.rank * g.out8 + c;
 #pragma unroll
@@ -463,7 +499,7 @@ constexpr int GRAD_COLS = 256, GRAD_K = 32, GRAD_WAVES = 4, GRAD_WINDOW = 1024;
 // of two of their own. What is not there (tokens past the end, columns past the width or the
 // rank) is loaded from a few zeros, so that nothing a buffer happens to hold counts.
 template <class D, int RB, int NS>
-__global__ __launch_bounds__(64 * GRAD_WAVES, 2) void grad_kernel(const GradArgs g) {
+__global__ __launch_bounds__(64 * GRAD_WAVES, RB <= 4 ? 2 : 1) void grad_kernel(const GradArgs g) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr bool SCALED = D::MAX_EXPONENT < 127;
   constexpr int ROW = GRAD_COLS * 2, M_BYTES = GRAD_K * ROW;
@@ -475,13 +511,14 @@ __global__ __launch_bounds__(64 * GRAD_WAVES, 2) void grad_kernel(const GradArgs
   // waves side by side over the rank, each with RW 16s of it and J 16s of the columns: a
   // wave converts what it multiplies
   constexpr int WR = RB < 4 ? 1 : RB / 2, WC = GRAD_WAVES / WR, RW = RB / WR, J = 16 / WC;
-  static_assert(2 * (NS * STAGE + GRAD_WINDOW * 4) <= 160 * 1024, "two blocks to a compute unit");
+  static_assert((RB <= 4 ? 2 : 1) * (NS * STAGE + GRAD_WINDOW * 4) <= 160 * 1024, "blocks of a compute unit");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * STAGE];
   __shared__ int token_of[GRAD_WINDOW];
   const int lane = threadIdx.x & 63, fr = lane & 15, fq = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const bool second = (int)blockIdx.x >= g.side[0].tiles;
-  const GradSide &sd = g.side[second];
+  const GradSide sd = g.side[second];
+  const uint64_t zeros = (uint64_t)g.zeros;
   const int c0 = (blockIdx.x - (second ? g.side[0].tiles : 0)) * GRAD_COLS;
   const int total = g.offsets[g.n];
   const int64_t first64 = (int64_t)blockIdx.y * g.chunk;
@@ -495,22 +532,25 @@ __global__ __launch_bounds__(64 * GRAD_WAVES, 2) void grad_kernel(const GradArgs
     if (g.offsets[mid] <= first) lo = mid; else hi = mid - 1;
   }
 
-  // where this lane's pieces lie: m's are 2 rows of 32 chunks, v's 64 chunks of its rows
-  int m_row[M_LOADS], v_row[V_LOADS];
-  const uint16_t *m_at[M_LOADS];
-  const float *v_at[V_LOADS];
+  // where this lane's pieces lie: m's are 2 rows of 32 chunks, v's 64 chunks of its rows;
+  // past the width or the rank the zeros, whatever the token
+  int row[M_LOADS + V_LOADS];
+  uint64_t at[M_LOADS + V_LOADS];
+  uint32_t ld[M_LOADS + V_LOADS];  // bytes
 #pragma unroll
   for (int q = 0; q < M_LOADS; ++q) {
     const int k = (q * GRAD_WAVES + wave) * 2 + (lane >> 5);
     const int c = c0 + ((lane & 31) ^ swz<GRAD_COLS>(k)) * 8;
-    m_row[q] = k;
-    m_at[q] = c < sd.width ? sd.m + c : nullptr;
+    row[q] = k;
+    at[q] = c < sd.width ? (uint64_t)(sd.m + c) : zeros;
+    ld[q] = c < sd.width ? (uint32_t)(sd.ld * 2) : 0;
   }
 #pragma unroll
   for (int q = 0; q < V_LOADS; ++q) {
-    const int i = (q * GRAD_WAVES + wave) * 64 + lane;
-    v_row[q] = i / V_CHUNKS;
-    v_at[q] = i % V_CHUNKS * 4 < g.rank ? sd.v + i % V_CHUNKS * 4 : nullptr;
+    const int i = (q * GRAD_WAVES + wave) * 64 + lane, c = i % V_CHUNKS * 4;
+    row[M_LOADS + q] = i / V_CHUNKS;
+    at[M_LOADS + q] = c < g.rank ? (uint64_t)(sd.v + c) : zeros;
+    ld[M_LOADS + q] = c < g.rank ? (uint32_t)(g.ldv * 4) : 0;
   }
   const int my_col = wave % WC * J * 16, my_rank = wave / WC * RW * 16;
   // transposed reads: a lane's k-row and, in chunk c of it, the place of column 16 j
@@ -535,20 +575,17 @@ __global__ __launch_bounds__(64 * GRAD_WAVES, 2) void grad_kernel(const GradArgs
       __syncthreads();
       auto issue = [&](int s) MOE_INLINE {
         uint8_t *to = lds + s % NS * STAGE;
+        int token[M_LOADS + V_LOADS];
 #pragma unroll
-        for (int q = 0; q < M_LOADS; ++q) {
-          const int i = s * GRAD_K + m_row[q];
-          const void *p = i < count && m_at[q] ? (const void *)(m_at[q] + token_of[min(i, count - 1)] * sd.ld)
-                                               : (const void *)g.zeros;
-          lds_gather(p, to + (q * GRAD_WAVES + wave) * 1024);
-        }
+        for (int q = 0; q < M_LOADS + V_LOADS; ++q)
+          token[q] = token_of[min(s * GRAD_K + row[q], count - 1)];
 #pragma unroll
-        for (int q = 0; q < V_LOADS; ++q) {
-          if (V_PIECES % GRAD_WAVES != 0 && q * GRAD_WAVES + wave >= V_PIECES) continue;
-          const int i = s * GRAD_K + v_row[q];
-          const void *p = i < count && v_at[q] ? (const void *)(v_at[q] + (int64_t)token_of[min(i, count - 1)] * g.ldv)
-                                               : (const void *)g.zeros;
-          lds_gather(p, to + M_BYTES + (q * GRAD_WAVES + wave) * 1024);
+        for (int q = 0; q < M_LOADS + V_LOADS; ++q) {
+          const int piece = (q < M_LOADS ? q : q - M_LOADS) * GRAD_WAVES + wave;
+          if (V_PIECES % GRAD_WAVES != 0 && q >= M_LOADS && piece >= V_PIECES) continue;
+          const uint64_t p = at[q] + (uint64_t)(uint32_t)token[q] * ld[q];
+          lds_gather(reinterpret_cast<const void *>(s * GRAD_K + row[q] < count ? p : zeros),
+                     to + (q < M_LOADS ? 0 : M_BYTES) + piece * 1024);
         }
       };
 #pragma unroll

@@ -40,13 +40,13 @@ static bool staged(const void *p, int64_t ld, int64_t stride, int cols) {
   return ((uintptr_t)p & 15) == 0 && ((ld | stride | cols) & 7) == 0;
 }
 
-template <class D, int MT, int RB, int WAVES, int NS>
+template <class D, int MT, int RB, int WAVES, int NS, int NS2>
 static int shrink_as(ShrinkArgs g, int turns, hipStream_t st) {
   g.turns = turns;
   const int64_t blocks = (int64_t)((g.M + 16 * MT - 1) / (16 * MT)) * turns;
   const bool whole = staged(g.x, g.ldx, 0, g.K) && staged(g.a, g.lda, g.stride, g.K);
   const auto kernel =
-      whole ? shrink_kernel<D, MT, RB, WAVES, NS, true> : shrink_kernel<D, MT, RB, WAVES, NS, false>;
+      whole ? shrink_kernel<D, MT, RB, WAVES, NS, NS2, true> : shrink_kernel<D, MT, RB, WAVES, NS, NS2, false>;
   return in_parts(blocks, 64 * WAVES, [&](int64_t first, uint32_t n) {
     g.block0 = first;
     kernel<<<n, 64 * WAVES, 0, st>>>(g);
@@ -60,16 +60,15 @@ static int shrink_of(const ShrinkArgs &g, hipStream_t st) {
   const int distinct = g.n < 16 ? g.n : 16;
   const int rb = (g.rank + 15) / 16;
   if (g.M <= 1024) {
-    if (rb == 1) return shrink_as<D, 1, 1, 8, 4>(g, distinct, st);
-    if (rb == 2) return shrink_as<D, 1, 2, 8, 3>(g, distinct, st);
-    if (rb <= 4) return shrink_as<D, 1, 4, 4, 3>(g, distinct, st);
-    return shrink_as<D, 1, 8, 4, 2>(g, distinct, st);
+    if (rb == 1) return shrink_as<D, 1, 1, 8, 4, 0>(g, distinct, st);
+    if (rb == 2) return shrink_as<D, 1, 2, 8, 3, 0>(g, distinct, st);
+    if (rb <= 4) return shrink_as<D, 1, 4, 4, 3, 0>(g, distinct, st);
+    return shrink_as<D, 1, 8, 4, 2, 0>(g, distinct, st);
   }
-  const int turns = distinct < 2 ? 1 : 2;
-  if (rb == 1) return shrink_as<D, 2, 1, 4, 3>(g, turns, st);
-  if (rb == 2) return shrink_as<D, 2, 2, 8, 2>(g, turns, st);
-  if (rb <= 4) return shrink_as<D, 2, 4, 4, 3>(g, turns, st);
-  return shrink_as<D, 1, 8, 4, 2>(g, turns, st);
+  if (rb == 1) return shrink_as<D, 2, 1, 8, 3, 2>(g, 1, st);
+  if (rb == 2) return shrink_as<D, 2, 2, 4, 4, 3>(g, 1, st);
+  if (rb <= 4) return shrink_as<D, 2, 4, 4, 3, 2>(g, 1, st);
+  return shrink_as<D, 1, 8, 4, 2, 0>(g, distinct < 2 ? 1 : 2, st);
 }
 static int shrink(int dtype, const ShrinkArgs &g, hipStream_t st) {
   return dtype == MOE_BF16 ? shrink_of<Bf16>(g, st) : shrink_of<F16>(g, st);
@@ -155,12 +154,12 @@ static int run_forward(const moe_adapter_linear_args *a, Arena &ws, hipStream_t 
 }
 
 // Tokens of a block of the gradients: some 512 blocks over both sides, and no fewer
-// than 16 for each of the rank, where the partial sums are a quarter of what they are made
-// from.
+// than 4 for each of the rank, where the partial sums are as many bytes as what they are
+// made from.
 static int grad_chunk(int64_t tokens, int tiles, int rank) {
   const int64_t chunks = (512 + tiles - 1) / tiles;
   int64_t each = (tokens + chunks - 1) / chunks;
-  each = each > 16 * rank ? each : 16 * rank;
+  each = each > 4 * rank ? each : 4 * rank;
   return (int)((each + GRAD_K - 1) / GRAD_K * GRAD_K);
 }
 
@@ -170,7 +169,7 @@ static int grads_of(const GradArgs &g, dim3 grid, hipStream_t st) {
   const auto kernel = rb == 1   ? grad_kernel<D, 1, 4>
                       : rb == 2 ? grad_kernel<D, 2, 3>
                       : rb <= 4 ? grad_kernel<D, 4, 3>
-                                : grad_kernel<D, 8, 2>;
+                                : grad_kernel<D, 8, 4>;
   kernel<<<grid, 64 * GRAD_WAVES, 0, st>>>(g);
   return hip_status();
 }
