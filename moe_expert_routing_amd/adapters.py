@@ -16,9 +16,8 @@ from typing import Dict, Optional
 
 import torch
 
-from .block import _plain
-from .ffn import (_MATRIX, _NONE, Matrix, _c_i32, _c_i64, _c_vp, _Entry, _fail, _first, _mat,
-                  _number, _out)
+from .block import _m, _plain, _SizedEntry
+from .ffn import (_MATRIX, _NONE, Matrix, _c_i32, _c_i64, _c_vp, _fail, _first, _number, _out)
 
 
 class AdapterLinearArgs(ctypes.Structure):
@@ -37,21 +36,31 @@ EXPORTS = {
 }
 
 _PACK = struct.Struct("@iiqiiii" + 7 * _MATRIX + "PPP" + 4 * _MATRIX).pack
-_ADAPTER = _Entry("moe_adapter_linear", "moe_adapter_linear_workspace_bytes")
-_ADAPTER_BACKWARD = _Entry("moe_adapter_linear_backward", "moe_adapter_linear_workspace_bytes", 1)
+_ADAPTER = _SizedEntry("moe_adapter_linear", "moe_adapter_linear_workspace_bytes")
+_ADAPTER_BACKWARD = _SizedEntry("moe_adapter_linear_backward", "moe_adapter_linear_workspace_bytes",
+                                1)
 
 
 def _adapters(x, w, a, b, ids, scale):
-    """Checked sizes of an adapter call: (dtype, tokens, in, out, rank, adapters)."""
+    """What both calls pass on, checked: (dtype, device, tokens, in, out, rank, adapters),
+    the sizes, the matrices x, w, a and b, ids and scale."""
     d = _first(x, "x")
     for t, name, ndim in ((w, "w", 2), (a, "a", 3), (b, "b", 3)):
         if not isinstance(t, torch.Tensor) or t.dim() != ndim:
             _fail(f"{name} must be a tensor of {ndim} dimensions")
     if ids is None:
         _fail("ids are needed")
+    dt, dev = x.dtype, x.device
+    tokens, n_in = x.shape
+    n_out = w.shape[0]
     n, rank, _ = a.shape
-    return (d, x.shape[0], _number(x.shape[1], "in"), _number(w.shape[0], "out"),
-            _number(rank, "rank"), _number(n, "adapters"))
+    head = (d, _number(rank, "rank"), tokens, _number(n_in, "in"), _number(n_out, "out"),
+            _number(n, "adapters"), 0)
+    mats = (*_m(x, "x", (tokens, n_in), dt, dev, x), *_m(w, "w", (n_out, n_in), dt, dev, x),
+            *_m(a, "a", (n, rank, n_in), dt, dev, x), *_m(b, "b", (n, n_out, rank), dt, dev, x))
+    tail = (_plain(ids, "ids", torch.int32, (tokens,), dev),
+            _plain(scale, "scale", torch.float32, (n,), dev))
+    return (dt, dev, tokens, n_in, n_out, rank, n), head, mats, tail
 
 
 def adapter_linear(x: torch.Tensor, w: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
@@ -63,22 +72,18 @@ def adapter_linear(x: torch.Tensor, w: torch.Tensor, a: torch.Tensor, b: torch.T
     s [T, R] = scale[id] x A[id]^T, from x [T, I], w [O, I], a [n, R, I], b [n, O, R],
     ids [T] (int32; a number outside 0 .. n-1: the token has no adapter) and scale [n]
     (fp32). With `save` also s (fp32), which adapter_linear_backward reads."""
-    d, tokens, n_in, n_out, rank, n = _adapters(x, w, a, b, ids, scale)
+    (dt, dev, tokens, _, n_out, rank, _), head, mats, tail = _adapters(x, w, a, b, ids, scale)
     if out is None:
-        out = {"y": torch.empty((tokens, n_out), dtype=x.dtype, device=x.device)}
+        out = {"y": x.new_empty((tokens, n_out))}
     if save and out.get("s") is None:
-        out["s"] = torch.empty((tokens, rank), dtype=torch.float32, device=x.device)
+        out["s"] = torch.empty((tokens, rank), dtype=torch.float32, device=dev)
     s = out.get("s") if save else None
-    args = _PACK(
-        d, rank, tokens, n_in, n_out, n, 0, *_mat(x, "x", (tokens, n_in), x),
-        *_mat(w, "w", (n_out, n_in), x), *_mat(a, "a", (n, rank, n_in), x),
-        *_mat(b, "b", (n, n_out, rank), x), *_mat(bias, "bias", (n_out,), x),
-        *_mat(residual, "residual", (tokens, n_out), x),
-        *_mat(_out(out, "y"), "y", (tokens, n_out), x),
-        _plain(ids, "ids", torch.int32, (tokens,), x.device),
-        _plain(scale, "scale", torch.float32, (n,), x.device),
-        _plain(s, "s", torch.float32, (tokens, rank), x.device), *_NONE * 4)
-    _ADAPTER(args, x.device, ws)
+    shape = (tokens, n_out)
+    args = _PACK(*head, *mats, *_m(bias, "bias", (n_out,), dt, dev, x),
+                 *_m(residual, "residual", shape, dt, dev, x),
+                 *_m(_out(out, "y"), "y", shape, dt, dev, x), *tail,
+                 _plain(s, "s", torch.float32, (tokens, rank), dev), *_NONE * 4)
+    _ADAPTER(args, dev, ws)
     return out
 
 
@@ -91,22 +96,18 @@ def adapter_linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, 
     an adapter without tokens) from dy [T, O] and the forward pass's s [T, R]. An
     `out` dict without one of them leaves it out; s may be None without db. The
     residual's gradient is dy, and w has none here."""
-    d, tokens, n_in, n_out, rank, n = _adapters(x, w, a, b, ids, scale)
+    (dt, dev, tokens, n_in, n_out, rank, n), head, mats, tail = _adapters(x, w, a, b, ids, scale)
     if dy is None:
         _fail("dy is needed")
     if out is None:
-        out = {"dx": torch.empty((tokens, n_in), dtype=x.dtype, device=x.device),
-               "da": torch.empty((n, rank, n_in), dtype=x.dtype, device=x.device),
-               "db": torch.empty((n, n_out, rank), dtype=x.dtype, device=x.device)}
-    args = _PACK(
-        d, rank, tokens, n_in, n_out, n, 0, *_mat(x, "x", (tokens, n_in), x),
-        *_mat(w, "w", (n_out, n_in), x), *_mat(a, "a", (n, rank, n_in), x),
-        *_mat(b, "b", (n, n_out, rank), x), *_NONE * 3,
-        _plain(ids, "ids", torch.int32, (tokens,), x.device),
-        _plain(scale, "scale", torch.float32, (n,), x.device),
-        _plain(s, "s", torch.float32, (tokens, rank), x.device),
-        *_mat(dy, "dy", (tokens, n_out), x), *_mat(out.get("dx"), "dx", (tokens, n_in), x),
-        *_mat(out.get("da"), "da", (n, rank, n_in), x),
-        *_mat(out.get("db"), "db", (n, n_out, rank), x))
-    _ADAPTER_BACKWARD(args, x.device, ws)
+        out = {"dx": x.new_empty((tokens, n_in)),
+               "da": x.new_empty((n, rank, n_in)),
+               "db": x.new_empty((n, n_out, rank))}
+    args = _PACK(*head, *mats, *_NONE * 3, *tail,
+                 _plain(s, "s", torch.float32, (tokens, rank), dev),
+                 *_m(dy, "dy", (tokens, n_out), dt, dev, x),
+                 *_m(out.get("dx"), "dx", (tokens, n_in), dt, dev, x),
+                 *_m(out.get("da"), "da", (n, rank, n_in), dt, dev, x),
+                 *_m(out.get("db"), "db", (n, n_out, rank), dt, dev, x))
+    _ADAPTER_BACKWARD(args, dev, ws)
     return out

@@ -62,8 +62,22 @@ _DROP = "PIi"
 _PACK_NORM = struct.Struct("@iiqfi" + _DROP + 4 * _MATRIX + "PPPP" + 4 * _MATRIX + "P").pack
 _PACK_DROPOUT = struct.Struct("@iiq" + _DROP + 3 * _MATRIX).pack
 
+
+
+class _SizedEntry(_Entry):
+    """An entry whose calls nearly always need a workspace: its size is asked for
+    first, which saves a call that would only say so."""
+
+    def __call__(self, args: bytes, dev: torch.device, ws: Optional[torch.Tensor] = None) -> None:
+        if ws is None:
+            need = getattr(_ffn._pkg.lib(), self.size)(args, self.backward)
+            if need > 0:
+                ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        super().__call__(args, dev, ws)
+
+
 _NORM = _Entry("moe_rms_norm")
-_NORM_BACKWARD = _Entry("moe_rms_norm_backward", "moe_rms_norm_backward_workspace_bytes", 1)
+_NORM_BACKWARD = _SizedEntry("moe_rms_norm_backward", "moe_rms_norm_backward_workspace_bytes", 1)
 _DROPOUT = _Entry("moe_dropout")
 
 
@@ -78,6 +92,17 @@ class _Values(_Entry):
 
 
 _VALUES = _Values("moe_mxfp8_values")
+
+
+def _m(t: Optional[torch.Tensor], name: str, shape: tuple, dtype, dev, like) -> tuple:
+    """_mat, in less host time where the tensor is as it should be and contiguous."""
+    if t is None:
+        return _NONE
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and \
+            t.is_contiguous() and t.device == dev:
+        cols = shape[-1]
+        return (t.data_ptr(), cols, cols * shape[-2] if len(shape) == 3 else 0)
+    return _mat(t, name, shape, like)
 
 
 def _plain(t: Optional[torch.Tensor], name: str, dtype, shape: tuple, dev) -> int:
@@ -115,44 +140,45 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: Optional[torch.
     dict gives the outputs' memory: y and rstd are left out where it has none, h
     may be the residual itself, and with quant a y in it is written too."""
     d = _first(x, "x")
-    tokens, width = x.shape
+    shape = tokens, width = x.shape
+    dt, dev = x.dtype, x.device
     if quant not in (None, "mxfp8"):
         _fail(f"quant must be None or 'mxfp8', not {quant!r}")
-    drop = _drop(p, rng, site, x.device)
+    drop = _drop(p, rng, site, dev)
     if not isinstance(eps, (int, float)) or not 0.0 <= eps <= 3.4e38:
         _fail(f"eps must be a number of 0 or more, not {eps!r}")
     if out is None:
-        out = {"rstd": torch.empty(tokens, dtype=torch.float32, device=x.device)}
+        out = {"rstd": torch.empty(tokens, dtype=torch.float32, device=dev)}
         if quant is None:
-            out["y"] = torch.empty_like(x, memory_format=torch.contiguous_format)
+            out["y"] = torch.empty_like(x)
         if residual is not None or drop[1]:
-            out["h"] = torch.empty_like(x, memory_format=torch.contiguous_format)
+            out["h"] = torch.empty_like(x)
     q = scale = 0
     if quant:
         if width % 32:
             _fail("quant needs a width that is a multiple of 32")
         for name, cols in (("act_q", width), ("act_scale", width // 32)):
             if out.get(name) is None:
-                out[name] = torch.empty((tokens, cols), dtype=torch.uint8, device=x.device)
-        q = _plain(out["act_q"], "act_q", torch.uint8, (tokens, width), x.device)
-        scale = _plain(out["act_scale"], "act_scale", torch.uint8, (tokens, width // 32), x.device)
+                out[name] = torch.empty((tokens, cols), dtype=torch.uint8, device=dev)
+        q = _plain(out["act_q"], "act_q", torch.uint8, shape, dev)
+        scale = _plain(out["act_scale"], "act_scale", torch.uint8, (tokens, width // 32), dev)
     elif out.get("y") is None:
         _fail("out must have y")
-    shape = (tokens, width)
     h = _out(out, "h") if residual is not None or drop[1] else out.get("h")
-    a = _PACK_NORM(d, _number(width, "width"), tokens, eps, 0, *drop, *_mat(x, "x", shape, x),
-                   *_mat(residual, "residual", shape, x), *_mat(h, "h", shape, x),
-                   *_mat(out.get("y"), "y", shape, x), _weight(weight, width, x),
-                   _plain(out.get("rstd"), "rstd", torch.float32, (tokens,), x.device), q, scale,
+    a = _PACK_NORM(d, _number(width, "width"), tokens, eps, 0, *drop,
+                   *_m(x, "x", shape, dt, dev, x), *_m(residual, "residual", shape, dt, dev, x),
+                   *_m(h, "h", shape, dt, dev, x), *_m(out.get("y"), "y", shape, dt, dev, x),
+                   _weight(weight, width, x),
+                   _plain(out.get("rstd"), "rstd", torch.float32, (tokens,), dev), q, scale,
                    *_NONE * 4, 0)
-    _NORM(a, x.device)
+    _NORM(a, dev)
     return out
 
 
 def _weight(weight, width: int, like: torch.Tensor) -> int:
     if weight is None:
         _fail("weight is needed")
-    return _mat(weight, "weight", (width,), like)[0]
+    return _m(weight, "weight", (width,), like.dtype, like.device, like)[0]
 
 
 def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
@@ -165,24 +191,24 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, r
     of x and, without dropout, of the residual too; dweight [W]; with dropout
     also dresidual [T, W]. An `out` dict without one of them leaves it out."""
     d = _first(h, "h")
-    tokens, width = h.shape
-    drop = _drop(p, rng, site, h.device)
+    shape = tokens, width = h.shape
+    dt, dev = h.dtype, h.device
+    drop = _drop(p, rng, site, dev)
     if out is None:
-        out = {"dx": torch.empty_like(h, memory_format=torch.contiguous_format),
-               "dweight": torch.empty(width, dtype=h.dtype, device=h.device)}
+        out = {"dx": torch.empty_like(h),
+               "dweight": h.new_empty(width)}
         if drop[1]:
-            out["dresidual"] = torch.empty_like(h, memory_format=torch.contiguous_format)
-    shape = (tokens, width)
+            out["dresidual"] = torch.empty_like(h)
     if dy is None or rstd is None:
         _fail("dy and rstd are needed")
     a = _PACK_NORM(d, _number(width, "width"), tokens, 0.0, 0, *drop, *_NONE * 2,
-                   *_mat(h, "h", shape, h), *_NONE, _weight(weight, width, h),
-                   _plain(rstd, "rstd", torch.float32, (tokens,), h.device), 0, 0,
-                   *_mat(dy, "dy", shape, h), *_mat(dh, "dh", shape, h),
-                   *_mat(out.get("dx"), "dx", shape, h),
-                   *_mat(out.get("dresidual"), "dresidual", shape, h),
-                   _mat(out.get("dweight"), "dweight", (width,), h)[0])
-    _NORM_BACKWARD(a, h.device, ws)
+                   *_m(h, "h", shape, dt, dev, h), *_NONE, _weight(weight, width, h),
+                   _plain(rstd, "rstd", torch.float32, (tokens,), dev), 0, 0,
+                   *_m(dy, "dy", shape, dt, dev, h), *_m(dh, "dh", shape, dt, dev, h),
+                   *_m(out.get("dx"), "dx", shape, dt, dev, h),
+                   *_m(out.get("dresidual"), "dresidual", shape, dt, dev, h),
+                   _m(out.get("dweight"), "dweight", (width,), dt, dev, h)[0])
+    _NORM_BACKWARD(a, dev, ws)
     return out
 
 
@@ -192,14 +218,15 @@ def dropout(x: torch.Tensor, p: float, rng: Optional[torch.Tensor], *, site: int
     """moe_dropout: out [T, W] = residual + x, x dropped out with probability p and
     scaled by 1 / (1 - p). `out` may be x or the residual."""
     d = _first(x, "x")
-    tokens, width = x.shape
-    drop = _drop(p, rng, site, x.device)
+    shape = tokens, width = x.shape
+    dt, dev = x.dtype, x.device
+    drop = _drop(p, rng, site, dev)
     if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
-    shape = (tokens, width)
-    a = _PACK_DROPOUT(d, _number(width, "width"), tokens, *drop, *_mat(x, "x", shape, x),
-                      *_mat(residual, "residual", shape, x), *_mat(out, "out", shape, x))
-    _DROPOUT(a, x.device)
+        out = torch.empty_like(x)
+    a = _PACK_DROPOUT(d, _number(width, "width"), tokens, *drop, *_m(x, "x", shape, dt, dev, x),
+                      *_m(residual, "residual", shape, dt, dev, x),
+                      *_m(out, "out", shape, dt, dev, x))
+    _DROPOUT(a, dev)
     return out
 
 
