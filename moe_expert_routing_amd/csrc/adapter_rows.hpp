@@ -33,7 +33,19 @@ struct Stream {
 struct StreamRows {
   const uint16_t *p;  // first row, at the wave's first k
   int64_t ld;
-  int rows;  // at least 1; rows past them repeat the last one
+  int rows;       // at least 1; rows past them repeat the last one
+  uint64_t some;  // not 0: the rows are those whose bits are set, no more than 16
+
+  __device__ __forceinline__ int64_t at(int row) const {  // elements from p
+    row = min(row, rows - 1);
+    if (some) {
+      int b = 0;
+      uint64_t left = some;
+      for (int i = 0; i < 16 && left; ++i, left &= left - 1) b = i <= row ? __builtin_ctzll(left) : b;
+      row = b;
+    }
+    return row * ld;
+  }
 };
 
 template <class D, int NA, int RB, int MT, int NS, bool STAGED>
@@ -53,7 +65,7 @@ __device__ __forceinline__ void stream_products(f32x4 (&acc)[NA * RB][MT], const
     for (int q = 0; q < S::PIECES; ++q) {
       const StreamRows &s = operand_of(q);
       const int row = (q < 2 * F ? q % (2 * RB) : q - 2 * F) * 8 + (lane >> 3);
-      off[q] = (uint32_t)(min(row, s.rows - 1) * s.ld + chunk * 8) * 2;
+      off[q] = (uint32_t)(s.at(row) + chunk * 8) * 2;
     }
     const int blocks = (k + 63) / 64;
     auto issue = [&](int s) MOE_INLINE {
@@ -90,9 +102,9 @@ __device__ __forceinline__ void stream_products(f32x4 (&acc)[NA * RB][MT], const
     const uint16_t *ar[NA * RB], *xr[MT];
 #pragma unroll
     for (int r = 0; r < NA * RB; ++r)
-      ar[r] = a[r / RB].p + min(16 * (r % RB) + fr, a[r / RB].rows - 1) * a[r / RB].ld + fq * 8;
+      ar[r] = a[r / RB].p + a[r / RB].at(16 * (r % RB) + fr) + fq * 8;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) xr[i] = x.p + min(16 * i + fr, x.rows - 1) * x.ld + fq * 8;
+    for (int i = 0; i < MT; ++i) xr[i] = x.p + x.at(16 * i + fr) + fq * 8;
     int s = 0;
 #pragma unroll 4
     for (; s + 32 <= k; s += 32) {
@@ -196,7 +208,7 @@ __global__ __launch_bounds__(64 * WAVES) void shrink_kernel(const ShrinkArgs g) 
     }
   const int per = ((g.K + 63) / 64 + WAVES - 1) / WAVES * 64;
   const int k0 = min(g.K, wave * per), k = min(g.K - k0, per);
-  const StreamRows x = {g.x + row0 * g.ldx + k0, g.ldx, g.M - row0};
+  const StreamRows x = {g.x + row0 * g.ldx + k0, g.ldx, g.M - row0, 0};
   uint64_t todo = with;
   auto next = [&](uint64_t &mine) MOE_INLINE {
     const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
@@ -205,7 +217,7 @@ __global__ __launch_bounds__(64 * WAVES) void shrink_kernel(const ShrinkArgs g) 
     return a;
   };
   auto rows_of = [&](int a) MOE_INLINE {
-    return StreamRows{g.a + a * g.stride + k0, g.lda, g.rank};
+    return StreamRows{g.a + a * g.stride + k0, g.lda, g.rank, 0};
   };
   auto write = [&](int a, uint64_t mine, const float *part) MOE_INLINE {
     const float c = g.scale ? g.scale[a] : 1.f;
@@ -248,14 +260,15 @@ __global__ __launch_bounds__(64 * WAVES) void shrink_kernel(const ShrinkArgs g) 
 #endif
 }
 
-// ------------------------------------------------- y of up to 64 rows, two launches
+// ----------------------------------------------------- y of few rows, two launches
 
 // For a decode batch, bound by reading W and the adapters among its tokens once.
 // First launch: x times the rows of W and of each such A_a together, so that reading
 // the adapters costs no time of its own; k is split over the waves of `splits` blocks,
 // each of which leaves fp32 sums. Second launch: the sums added in their order, s B_a^T in
 // fp32 without halves, bias and residual, one rounding.
-constexpr int FEW_ROWS = 64;
+// Tokens go in groups of 64, each with blocks of its own.
+constexpr int FEW_GROUP = 64;
 struct FewArgs {
   const uint16_t *x, *w, *a, *b, *bias, *res;
   int64_t ldx, ldw, lda, a_stride, ldb, b_stride, ldr, ldy;
@@ -272,47 +285,65 @@ constexpr int FEW_WAVES = 4;
 template <class D, int MT, int RB, int NS, bool STAGED>
 __global__ __launch_bounds__(64 * FEW_WAVES) void few_stream_kernel(const FewArgs g) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  constexpr int ROWS = 16 * MT, TILE = 16 * RB, RING = STAGED ? Stream<MT, RB, NS>::BYTES : 0;
+  constexpr int TILE = 16 * RB, ARB = RB < 2 ? 1 : 2, ATILE = 16 * ARB;  // rows of W, and of an A
+  constexpr int RING = STAGED ? most(Stream<MT, RB, NS>::BYTES, Stream<1, ARB, NS>::BYTES) : 0;
   typedef Part<FEW_WAVES, RB, MT> P;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[most(FEW_WAVES * RING, P::BYTES)];
+  typedef Part<FEW_WAVES, ARB, 1> PA;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[most(FEW_WAVES * RING, most(P::BYTES, PA::BYTES))];
   float *part = reinterpret_cast<float *>(lds);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int tile = blockIdx.x;
-  StreamRows rows = {g.w, g.ldw, g.N};
-  uint64_t mine = ~0ull;
-  const bool adapter = tile >= g.w_tiles;
-  if (adapter) {  // of the slot-th adapter among the tokens
-    const int slot = (tile - g.w_tiles) / g.rank_tiles;
-    tile = (tile - g.w_tiles) % g.rank_tiles;
-    int id = lane < g.M ? g.ids[lane] : -1;
-    if ((uint32_t)id >= (uint32_t)g.n) id = -1;
-    uint64_t todo = __ballot(id >= 0);
-    int a = 0;
-    for (int i = 0; todo && i <= slot; ++i) {
-      a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-      mine = __ballot(id == a);
-      if (i < slot) todo &= ~mine;
-    }
-    if (!todo) return;
-    rows = {g.a + a * g.a_stride, g.lda, g.rank};
-  }
-  const int r0 = tile * TILE, n = rows.rows;
   const int k0 = min(g.K, ((int)blockIdx.y * FEW_WAVES + wave) * g.per), k = min(g.K - k0, g.per);
-  rows.p += r0 * rows.ld + k0;
-  rows.rows -= r0;
-  f32x4 acc[RB][MT];
-  clear(acc);
-  const StreamRows operand[1] = {rows};
-  stream_products<D, 1, RB, MT, NS, STAGED>(acc, operand, {g.x + k0, g.ldx, g.M}, k, lds + wave * RING);
-  __syncthreads();
-  P::put(part, wave, acc, 0);
-  __syncthreads();
-  float *out = adapter ? g.part_s : g.part_y;
-  for (int o = threadIdx.x; o < ROWS * TILE; o += 64 * FEW_WAVES) {
-    const int t = o / TILE, r = o % TILE;
-    if (t < g.M && r0 + r < n && (mine >> t & 1))
-      out[((int64_t)blockIdx.y * g.M + t) * n + r0 + r] = P::sum(part, t, r);
+  const int t0 = blockIdx.z * FEW_GROUP, M = min(g.M - t0, FEW_GROUP);
+  const uint16_t *x = g.x + t0 * g.ldx + k0;
+  int tile = blockIdx.x;
+  if (tile < g.w_tiles) {
+    const int r0 = tile * TILE;
+    f32x4 acc[RB][MT];
+    clear(acc);
+    const StreamRows w[1] = {{g.w + r0 * g.ldw + k0, g.ldw, g.N - r0, 0}};
+    stream_products<D, 1, RB, MT, NS, STAGED>(acc, w, {x, g.ldx, M, 0}, k, lds + wave * RING);
+    __syncthreads();
+    P::put(part, wave, acc, 0);
+    __syncthreads();
+    for (int o = threadIdx.x; o < 16 * MT * TILE; o += 64 * FEW_WAVES) {
+      const int t = o / TILE, r = o % TILE;
+      if (t < M && r0 + r < g.N)
+        g.part_y[((int64_t)blockIdx.y * g.M + t0 + t) * g.N + r0 + r] = P::sum(part, t, r);
+    }
+    return;
+  }
+  // of the slot-th adapter among the tokens: its own tokens, 16 at a time
+  const int slot = (tile - g.w_tiles) / g.rank_tiles, r0 = (tile - g.w_tiles) % g.rank_tiles * ATILE;
+  int id = lane < M ? g.ids[t0 + lane] : -1;
+  if ((uint32_t)id >= (uint32_t)g.n) id = -1;
+  uint64_t todo = __ballot(id >= 0), mine = 0;
+  int a = 0;
+  for (int i = 0; todo && i <= slot; ++i) {
+    a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+    mine = __ballot(id == a);
+    if (i < slot) todo &= ~mine;
+  }
+  if (!todo) return;
+  const StreamRows rows[1] = {{g.a + a * g.a_stride + r0 * g.lda + k0, g.lda, g.rank - r0, 0}};
+  while (mine) {
+    uint64_t some = 0;
+    for (int i = 0; i < 16 && mine; ++i, mine &= mine - 1) some |= mine & -mine;
+    f32x4 acc[ARB][1];
+    clear(acc);
+    stream_products<D, 1, ARB, 1, NS, STAGED>(acc, rows, {x, g.ldx, (int)__popcll(some), some}, k,
+                                              lds + wave * RING);
+    __syncthreads();
+    PA::put(part, wave, acc, 0);
+    __syncthreads();
+    for (int o = threadIdx.x; o < 16 * ATILE; o += 64 * FEW_WAVES) {
+      const int i = o / ATILE, r = o % ATILE;
+      if (i >= (int)__popcll(some) || r0 + r >= g.rank) continue;
+      uint64_t left = some;
+      for (int q = 0; q < i; ++q) left &= left - 1;
+      g.part_s[((int64_t)blockIdx.y * g.M + t0 + __builtin_ctzll(left)) * g.rank + r0 + r] = PA::sum(part, i, r);
+    }
+    __syncthreads();
   }
 #endif
 }

@@ -77,9 +77,9 @@ static int shrink(int dtype, const ShrinkArgs &g, hipStream_t st) {
 template <class D, int MT, int RB, int NS>
 static int few_as(FewArgs g, hipStream_t st) {
   g.w_tiles = (g.N + 16 * RB - 1) / (16 * RB);
-  g.rank_tiles = (g.rank + 16 * RB - 1) / (16 * RB);
-  const int slots = g.n < g.M ? g.n : g.M;
-  const dim3 grid(g.w_tiles + slots * g.rank_tiles, g.splits);
+  g.rank_tiles = (g.rank + (RB < 2 ? 15 : 31)) / (RB < 2 ? 16 : 32);
+  const int group = g.M < FEW_GROUP ? g.M : FEW_GROUP, slots = g.n < group ? g.n : group;
+  const dim3 grid(g.w_tiles + slots * g.rank_tiles, g.splits, (g.M + FEW_GROUP - 1) / FEW_GROUP);
   const bool whole = staged(g.x, g.ldx, 0, g.K) && staged(g.w, g.ldw, 0, g.K) &&
                      staged(g.a, g.lda, g.a_stride, g.K);
   const auto kernel =
@@ -93,15 +93,23 @@ template <class D>
 static int few_of(const FewArgs &g, hipStream_t st) {
   if (g.M <= 16) return few_as<D, 1, 1, 4>(g, st);
   if (g.M <= 32) return few_as<D, 2, 2, 3>(g, st);
-  return few_as<D, 4, 2, 2>(g, st);
+  return few_as<D, 4, 4, 2>(g, st);
+}
+// Whether y goes by these kernels: up to 64 tokens, and with a long way through few
+// columns more. (Each token with one of 64 adapters of rank 16, these kernels and
+// the tiles, us: 16 tokens 7168 -> 2048 17 and 32, 2048 -> 7168 17 and 26; 64 tokens 24 and
+// 44, 24 and 27; 128 tokens 34 and 40, 38 and 30, 7168 -> 512 17 and 24; 255 tokens 58 and
+// 41, 66 and 46, 21 and 25.)
+static bool is_few(int64_t T, int64_t I, int64_t O) {
+  return T <= 64 || (T <= 128 && I >= 2 * O) || (T <= 256 && I >= 8 * O);
 }
 static int run_few(const moe_adapter_linear_args *a, Arena &ws, hipStream_t st) {
   FewArgs g = {};
   g.M = (int)a->tokens, g.N = a->out, g.K = a->in, g.rank = a->rank, g.n = a->adapters;
-  // some 4096 waves, of at least 128 k
-  const int blocks = (g.K + 63) / 64, tile = g.M <= 16 ? 16 : 32;
+  // some 2048 waves, of at least 128 k
+  const int blocks = (g.K + 63) / 64, tile = g.M <= 16 ? 16 : g.M <= 32 ? 32 : 64;
   const int tiles = (g.N + tile - 1) / tile;
-  int splits = 1024 / tiles;
+  int splits = 512 / tiles;
   splits = splits < 1 ? 1 : splits > 8 ? 8 : splits;
   g.per = (blocks + splits * FEW_WAVES - 1) / (splits * FEW_WAVES);
   if (g.per < 2) g.per = 2;  // blocks of 64
@@ -121,14 +129,25 @@ static int run_few(const moe_adapter_linear_args *a, Arena &ws, hipStream_t st) 
   return a->dtype == MOE_BF16 ? few_of<Bf16>(g, st) : few_of<F16>(g, st);
 }
 
+// Plan of the product with its low-rank term. Of few rows the epilogue is the longer
+// part, one adapter after the other for every 16 of them, so that it takes the small tiles
+// and, with few of these, ranges of k (by the dense product's plan and this one, us: 100 tokens
+// 2048 -> 7168 38 and 30, 160 tokens 7168 -> 2048 65 and 36, 4096 -> 4096 44 and 37; with
+// 255 tokens 42 and 46, 44 and 45, and with many tiles of a long k 65 tokens 7168 -> 7168 56
+// and 61).
+static Plan low_plan(int64_t T, int64_t I, int64_t O) {
+  const int64_t tiles = (T + 31) / 32 * ((O + 63) / 64);
+  if (T > 192 || (tiles >= 256 && I >= 4096)) return row_plan({}, true, T, O, I);
+  return {TILE_32, tiles < 256 && I >= 4096 ? 4 : 1};
+}
+
 static int run_forward(const moe_adapter_linear_args *a, Arena &ws, hipStream_t st) {
   const int64_t T = a->tokens;
   const int I = a->in, O = a->out;
   int status = MOE_OK;
   if (T == 0) return MOE_OK;
-  if (T <= FEW_ROWS) return run_few(a, ws, st);
-  const moe_expert_rows dense = {};
-  const Plan plan = row_plan(dense, true, T, O, I);
+  if (is_few(T, I, O)) return run_few(a, ws, st);
+  const Plan plan = low_plan(T, I, O);
   float *s = a->s ? a->s : reinterpret_cast<float *>(ws.take((size_t)T * a->rank * sizeof(float)));
   const Operand x = operand(a->x, T, I, 1, ws, st, &status);
   const Operand w = operand(a->w, O, I, 1, ws, st, &status);
