@@ -73,11 +73,14 @@ static int64_t row_blocks(int64_t tokens, int rows, int64_t most) {
 template <class F>
 static int with_shape(int width, F &&f) {
   if (width <= 128) return f(RowShape<16, 1>());
+  if (width <= 256) return f(RowShape<16, 2>());
   if (width <= 512) return f(RowShape<64, 1>());
+  if (width <= 1024) return f(RowShape<64, 2>());
   if (width <= 2048) return f(RowShape<64, 4>());
   if (width <= 4096) return f(RowShape<256, 2>());
   if (width <= 8192) return f(RowShape<256, 4>());
-  return f(RowShape<1024, 4>());
+  if (width <= 16384) return f(RowShape<512, 4>());
+  return f(RowShape<512, 8>());
 }
 
 template <class D>
@@ -94,7 +97,7 @@ static int run_norm(const moe_rms_norm_args *a, hipStream_t st) {
 // Blocks of the backward pass: each has a row of partial sums of dweight.
 template <class S>
 static int64_t backward_blocks(int64_t tokens) {
-  return row_blocks(tokens, S::ROWS, S::THREADS == 256 ? 512 : 256);
+  return row_blocks(tokens, S::ROWS, S::ROWS > 1 ? 1024 : S::THREADS == 256 ? 512 : 256);
 }
 template <class D>
 static int run_norm_backward_of(const moe_rms_norm_args *a, Arena &ws, hipStream_t st) {

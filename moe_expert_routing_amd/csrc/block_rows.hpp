@@ -11,6 +11,30 @@ namespace moe_block {
 
 using namespace moe_ffn;
 
+// Eight elements at column c < n of a row of n columns, zeros past n. The last ones of a
+// row whose n is no multiple of 8 come from the row's last 16 bytes, shifted: load
+// by load, as load8_raw takes them, every row waited for them (30000 rows of 1001,
+// norm's backward pass 72 us).
+__device__ __forceinline__ s16x8 load_row8(const uint16_t *row, int c, int n) {
+  if (n < 8) return load8_raw(row, c, n);
+  const int at = min(c, n - 8);
+  s16x8 w = *reinterpret_cast<const s16x8_any *>(row + at);
+  if (at < c) {
+    typedef unsigned long long u64x2 __attribute__((ext_vector_type(2)));
+    u64x2 v = __builtin_bit_cast(u64x2, w);
+    const int bits = (c - at) * 16;
+    if (bits >= 64) {
+      v.x = v.y >> (bits - 64);
+      v.y = 0;
+    } else {
+      v.x = v.x >> bits | v.y << (64 - bits);
+      v.y >>= bits;
+    }
+    w = __builtin_bit_cast(s16x8, v);
+  }
+  return w;
+}
+
 // ------------------------------------------------------------------- dropout
 
 // Dropout of one call; level 0: none.
@@ -74,9 +98,9 @@ __global__ __launch_bounds__(256) void dropout_kernel(const DropoutArgs a) {
   const Numbers n = numbers_of(a.drop);
   for (int64_t t = (int64_t)blockIdx.y * blockDim.y + threadIdx.y; t < a.tokens;
        t += (int64_t)gridDim.y * blockDim.y) {
-    const s16x8 raw = load8_raw(a.x + t * a.ld_x, c, a.width);
+    const s16x8 raw = load_row8(a.x + t * a.ld_x, c, a.width);
     s16x8 rest = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (a.res) rest = load8_raw(a.res + t * a.ld_res, c, a.width);
+    if (a.res) rest = load_row8(a.res + t * a.ld_res, c, a.width);
     f32x8 v = unpack8<D>(raw);
     if (a.drop.level) v = drop8(v, (uint32_t)t, (uint32_t)c >> 3, a.drop, n);
     if (a.res) {
@@ -132,6 +156,14 @@ __device__ __forceinline__ float row_sum(float v, float (*slots)[16], int slot) 
 
 // ---------------------------------------------------------------------- norm
 
+// Makes the compiler unpack a row's elements again where they are used again, in
+// place of keeping them in fp32 across the row's sum, which takes twice the registers.
+__device__ __forceinline__ void keep_packed(s16x8 &v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("" : "+v"(v));
+#endif
+}
+
 struct NormArgs {
   const uint16_t *x, *res, *weight;
   uint16_t *h, *y;
@@ -177,6 +209,10 @@ template <int L_, int CH_>
 struct RowShape {
   static constexpr int L = L_, CH = CH_, THREADS = L < 256 ? 256 : L, ROWS = THREADS / L;
   static constexpr int WIDTH = L * CH * 8;
+  // The backward pass keeps its columns' sums of dweight in registers, or, where the
+  // threads have none left for them, in LDS. (4096 rows of 32768 with 1024 threads, whose
+  // 128 registers hold neither: 772 us, with the sums in LDS 655.)
+  static constexpr bool SUMS_IN_LDS = CH > 4;
 };
 
 // A row stays in registers from its loads to its stores: one pass over memory. The
@@ -194,7 +230,7 @@ __global__ __launch_bounds__(S::THREADS) void norm_kernel(const NormArgs a) {
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = (i * L + lane) * 8;
-    if (c < a.width) weight[i] = load8_raw(a.weight, c, a.width);
+    if (c < a.width) weight[i] = load_row8(a.weight, c, a.width);
   }
   int slot = 0;
   for (int64_t t = (int64_t)blockIdx.x * S::ROWS + threadIdx.x / L; t < a.tokens;
@@ -205,8 +241,8 @@ __global__ __launch_bounds__(S::THREADS) void norm_kernel(const NormArgs a) {
       const int c = (i * L + lane) * 8;
       row[i] = s16x8{0, 0, 0, 0, 0, 0, 0, 0};
       if (c < a.width) {
-        row[i] = load8_raw(a.x + t * a.ld_x, c, a.width);
-        if (a.res) rest[i] = load8_raw(a.res + t * a.ld_res, c, a.width);
+        row[i] = load_row8(a.x + t * a.ld_x, c, a.width);
+        if (a.res) rest[i] = load_row8(a.res + t * a.ld_res, c, a.width);
       }
     }
     float sum = 0.f;
@@ -231,6 +267,8 @@ __global__ __launch_bounds__(S::THREADS) void norm_kernel(const NormArgs a) {
     sum = row_sum<L>(sum, slots, slot);
     const float rstd = 1.f / sqrtf(fmaf(sum, inv_width, a.eps));
     if (a.rstd && lane == 0) a.rstd[t] = rstd;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) keep_packed(row[i]), keep_packed(weight[i]);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = (i * L + lane) * 8;
@@ -257,18 +295,21 @@ template <class D, class S>
 __global__ __launch_bounds__(S::THREADS) void norm_backward_kernel(const NormArgs a) {
   constexpr int L = S::L, CH = S::CH;
   __shared__ float slots[2][16];
-  __shared__ float join[S::ROWS > 1 ? S::ROWS : 1][S::ROWS > 1 ? S::WIDTH : 1];
+  __shared__ __attribute__((aligned(16))) float join[S::ROWS > 1 ? S::ROWS : 1]
+                                                   [S::ROWS > 1 || S::SUMS_IN_LDS ? S::WIDTH : 1];
   const int lane = threadIdx.x % L;
   const Numbers n = numbers_of(a.drop);
   const float inv_width = 1.f / (float)a.width;
   s16x8 weight[CH];
-  f32x8 dw[CH];
+  const f32x8 zero = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  f32x8 dw[S::SUMS_IN_LDS ? 1 : CH];
+  auto sums = [&](int i) -> f32x8 * { return reinterpret_cast<f32x8 *>(&join[0][(i * L + lane) * 8]); };
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = (i * L + lane) * 8;
     weight[i] = s16x8{0, 0, 0, 0, 0, 0, 0, 0};
-    if (c < a.width) weight[i] = load8_raw(a.weight, c, a.width);
-    dw[i] = f32x8{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (c < a.width) weight[i] = load_row8(a.weight, c, a.width);
+    if constexpr (S::SUMS_IN_LDS) *sums(i) = zero; else dw[i] = zero;
   }
   int slot = 0;
   for (int64_t t = (int64_t)blockIdx.x * S::ROWS + threadIdx.x / L; t < a.tokens;
@@ -279,9 +320,9 @@ __global__ __launch_bounds__(S::THREADS) void norm_backward_kernel(const NormArg
       const int c = (i * L + lane) * 8;
       dy[i] = h[i] = rest[i] = s16x8{0, 0, 0, 0, 0, 0, 0, 0};
       if (c < a.width) {
-        dy[i] = load8_raw(a.dy + t * a.ld_dy, c, a.width);
-        h[i] = load8_raw(a.h + t * a.ld_h, c, a.width);
-        if (a.dh) rest[i] = load8_raw(a.dh + t * a.ld_dh, c, a.width);
+        dy[i] = load_row8(a.dy + t * a.ld_dy, c, a.width);
+        h[i] = load_row8(a.h + t * a.ld_h, c, a.width);
+        if (a.dh) rest[i] = load_row8(a.dh + t * a.ld_dh, c, a.width);
       }
     }
     const float rstd = a.rstd[t];
@@ -290,14 +331,23 @@ __global__ __launch_bounds__(S::THREADS) void norm_backward_kernel(const NormArg
     for (int i = 0; i < CH; ++i) {
       const f32x8 d = unpack8<D>(dy[i]), f = unpack8<D>(h[i]), w = unpack8<D>(weight[i]);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float dn = d[k] * (f[k] * rstd);
-        dw[i][k] += dn;
-        sum = fmaf(dn, w[k], sum);
+      for (int k = 0; k < 8; ++k) sum = fmaf(d[k] * (f[k] * rstd), w[k], sum);
+      if constexpr (S::SUMS_IN_LDS) {
+        if (a.part) {
+          f32x8 t = *sums(i);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) t[k] += d[k] * (f[k] * rstd);
+          *sums(i) = t;
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) dw[i][k] += d[k] * (f[k] * rstd);
       }
     }
     const float mean = row_sum<L>(sum, slots, slot) * inv_width;
     if (!a.dx && !a.dres) continue;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) keep_packed(dy[i]), keep_packed(h[i]), keep_packed(weight[i]);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = (i * L + lane) * 8;
@@ -331,7 +381,7 @@ __global__ __launch_bounds__(S::THREADS) void norm_backward_kernel(const NormArg
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = (i * L + lane) * 8;
-      if (c < a.width) store8_f32(part, c, a.width, dw[i]);
+      if (c < a.width) store8_f32(part, c, a.width, S::SUMS_IN_LDS ? *sums(i) : dw[S::SUMS_IN_LDS ? 0 : i]);
     }
   }
 }
