@@ -84,11 +84,11 @@ _DROPOUT = _Entry("moe_dropout")
 class _Values(_Entry):
     """moe_mxfp8_values, whose arguments are no structure."""
 
-    def __call__(self, args: tuple, dev: torch.device) -> None:
+    def __call__(self, args: tuple, dev: torch.device, ws: Optional[torch.Tensor] = None) -> None:
         if self.fn is None:
             fn = getattr(_ffn._pkg.lib(), self.name)
             self.fn = lambda a, stream: fn(*a, stream)
-        super().__call__(args, dev)
+        super().__call__(args, dev, ws)
 
 
 _VALUES = _Values("moe_mxfp8_values")

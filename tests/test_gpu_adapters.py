@@ -117,8 +117,9 @@ def problem(T, I, O, R, n, kind, dt, seed=0):
     return x, w, a, b, make_ids(kind, T, n, seed), scale
 
 
+# tokens of one block of the gradients that fill its list of tokens more than once,
 # few rows of one, two and four 16s and of several groups of 64, the tiles of 32 to 256 rows, split ranges of k, widths of no tile
-CASES = [(100, 4096, 512, 16, 70, "each"), (200, 2100, 72, 12, 5, "random"), (128, 4096, 264, 8, 128, "each"), (150, 512, 1000, 16, 9, "each"), (40, 2048, 300, 24, 9, "requests"), (64, 96, 7168, 128, 64, "each"), (32, 1000, 33, 16, 2, "random"), (65, 4096, 128, 16, 65, "each"),
+CASES = [(20000, 7168, 64, 8, 1, "one"), (100, 4096, 512, 16, 70, "each"), (200, 2100, 72, 12, 5, "random"), (128, 4096, 264, 8, 128, "each"), (150, 512, 1000, 16, 9, "each"), (40, 2048, 300, 24, 9, "requests"), (64, 96, 7168, 128, 64, "each"), (32, 1000, 33, 16, 2, "random"), (65, 4096, 128, 16, 65, "each"),
          (1, 64, 64, 16, 1, "one"), (1, 7168, 2048, 16, 4, "one"), (3, 1000, 17, 7, 5, "each"), (16, 512, 7168, 16, 16, "each"),
          (16, 129, 515, 1, 3, "random"), (17, 320, 200, 8, 17, "each"), (33, 1024, 96, 12, 40, "each"), (64, 7168, 1024, 16, 64, "each"),
          (100, 2000, 1001, 40, 6, "requests"), (257, 640, 768, 128, 3, "random"), (300, 96, 64, 17, 9, "requests"), (1000, 1000, 1412, 64, 5, "requests"),
