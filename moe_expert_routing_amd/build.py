@@ -17,6 +17,7 @@ import re
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -71,17 +72,29 @@ def build(verbose: bool = False) -> str:
         shutil.rmtree(TEMPS)
     os.makedirs(TEMPS)
     tmp = LIB_PATH + ".tmp"
-    cmd = [hipcc(), *HIP_FLAGS, "-save-temps", "-I", os.path.join(ROOT, "include"), "-I", CSRC,
-           *[s for s in SOURCES if os.path.exists(s)], "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True, cwd=TEMPS)
-    log = "\n".join(l for l in (res.stdout + res.stderr).splitlines()
-                    if not HOST_FEATURE_WARNING.search(l) and "argument unused" not in l)
-    if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({res.returncode}):\n{log}")
-    if verbose and log.strip():
-        print(log, flush=True)
+    compile_flags = [f for f in HIP_FLAGS if f != "-shared"]
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        res = subprocess.run(cmd, capture_output=True, text=True, cwd=TEMPS)
+        log = "\n".join(l for l in (res.stdout + res.stderr).splitlines()
+                        if not HOST_FEATURE_WARNING.search(l) and "argument unused" not in l)
+        if res.returncode != 0:
+            raise RuntimeError(f"hipcc failed ({res.returncode}):\n{log}")
+        if verbose and log.strip():
+            print(log, flush=True)
+
+    def compile_one(source):
+        obj = os.path.join(TEMPS, os.path.basename(source) + ".o")
+        run([hipcc(), *compile_flags, "-save-temps", "-c", source,
+             "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-o", obj])
+        return obj
+
+    # the sources beside each other: some 20 s each
+    with ThreadPoolExecutor(max(1, min(8, os.cpu_count() or 1))) as pool:
+        objects = list(pool.map(compile_one, [s for s in SOURCES if os.path.exists(s)]))
+    run([hipcc(), "-shared", "-fPIC", f"--offload-arch={ARCH}", *objects, "-o", tmp])
     if not glob.glob(os.path.join(TEMPS, "*-hip-amdgcn-amd-amdhsa-*.s")):
         raise RuntimeError("no device assembly kept: the packed FP32 check cannot run")
     hits = packed_fp32_in_device_asm()
