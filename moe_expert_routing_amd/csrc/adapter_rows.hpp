@@ -230,10 +230,9 @@ __global__ __launch_bounds__(64 * WAVES) void shrink_kernel(const ShrinkArgs g) 
   float *part = reinterpret_cast<float *>(lds), *part1 = part + P::BYTES / 4;
   for (int turn = 0; todo; ++turn) {
     uint64_t mine, mine1 = 0;
-    const int a = next(mine);
+    const int a = next(mine), a1 = NS2 && todo ? next(mine1) : -1;
     if (turn % g.turns != my_turn) continue;
-    if (NS2 && todo) {
-      const int a1 = next(mine1);
+    if (a1 >= 0) {
       f32x4 acc[NA * RB][MT];
       clear(acc);
       const StreamRows rows[2] = {rows_of(a), rows_of(a1)};

@@ -54,7 +54,10 @@ static int shrink_as(ShrinkArgs g, int turns, hipStream_t st) {
   });
 }
 // Few rows: 16 a block, of which a decode batch has up to 16 adapters. More: 32, so that
-// A is read half as often.
+// A is read half as often, once that many blocks fill the card. (With the product, us, by 32
+// and by 16: 2048 rows of 7168, rank 32, 91 and 81; 2048 rows of 4096 from 300 requests 122
+// and 105; 8192 rows of 7168, then with half the waves, 218 and 222.) Up to 4096 rows, too, the
+// rounds over a row's adapters are shared, by as many blocks as there is room for.
 template <class D>
 static int shrink_of(const ShrinkArgs &g, hipStream_t st) {
   const int distinct = g.n < 16 ? g.n : 16;
@@ -65,9 +68,16 @@ static int shrink_of(const ShrinkArgs &g, hipStream_t st) {
     if (rb <= 4) return shrink_as<D, 1, 4, 4, 3, 0>(g, distinct, st);
     return shrink_as<D, 1, 8, 4, 2, 0>(g, distinct, st);
   }
-  if (rb == 1) return shrink_as<D, 2, 1, 8, 3, 2>(g, 1, st);
-  if (rb == 2) return shrink_as<D, 2, 2, 4, 4, 3>(g, 1, st);
-  if (rb <= 4) return shrink_as<D, 2, 4, 4, 3, 2>(g, 1, st);
+  if (g.M <= 4096) {
+    const int turns = distinct < 4096 / g.M ? distinct : 4096 / g.M;
+    if (rb == 1) return shrink_as<D, 1, 1, 8, 4, 3>(g, turns, st);
+    if (rb == 2) return shrink_as<D, 1, 2, 4, 4, 3>(g, turns, st);
+    if (rb <= 4) return shrink_as<D, 1, 4, 4, 3, 2>(g, turns, st);
+  } else {
+    if (rb == 1) return shrink_as<D, 2, 1, 8, 3, 2>(g, 1, st);
+    if (rb == 2) return shrink_as<D, 2, 2, 4, 4, 3>(g, 1, st);
+    if (rb <= 4) return shrink_as<D, 2, 4, 4, 3, 2>(g, 1, st);
+  }
   return shrink_as<D, 1, 8, 4, 2, 0>(g, distinct < 2 ? 1 : 2, st);
 }
 static int shrink(int dtype, const ShrinkArgs &g, hipStream_t st) {

@@ -291,6 +291,18 @@ def test_without_adapters_it_is_the_linear_product():
         assert torch.equal(dx, M.linear_backward(dy, x, w)["dx"])
 
 
+@pytest.mark.parametrize("T,K,R,n,kind", [(1025, 520, 16, 30, "each"), (1400, 7168, 8, 40, "requests"), (2100, 200, 48, 9, "random"), (4096, 264, 32, 3, "requests"),
+                                          (1030, 96, 64, 1, "random"), (1100, 203, 13, 25, "each")])
+@pytest.mark.parametrize("dt", [BF, FP], ids=["bf16", "fp16"])
+def test_rows_between_a_thousand_and_four(T, K, R, n, kind, dt):
+    """16 rows a block of s, whose adapters several blocks share."""
+    x, w, a, b, ids, scale = problem(T, K, 72, R, n, kind, dt)
+    check_forward(x, w, a, b, ids, scale, None, None, M.adapter_linear(x, w, a, b, ids, scale=scale, save=True))
+    x, w, a, b, ids, scale = problem(T, 72, K, R, n, kind, dt)
+    dy, s = normal(11, T, K, dt=dt), normal(12, T, R, dt=torch.float32)
+    check_backward(dy, x, w, a, b, ids, scale, s, M.adapter_linear_backward(dy, x, w, a, b, ids, s, scale=scale))
+
+
 def test_many_adapters():
     """More adapters than tokens, and the largest number of them."""
     T, I, O, R, n = 40, 64, 48, 4, 4096
