@@ -11,6 +11,8 @@
 // infinities or NaN in one adapter stay out of the other requests' rows.
 #pragma once
 
+#include <type_traits>
+
 #include "ffn_types.hpp"
 
 namespace moe_ffn {
@@ -33,36 +35,52 @@ __device__ __forceinline__ int exponent_for(float most) {
 // acc[i][j] of a wave: rows row0 + 16 i + fr, columns col0 + 16 j + 4 fq .. 4 fq + 3 in
 // a lane (fr = lane & 15, fq = lane >> 4). For every 16 rows the adapters among them
 // are taken one after the other; the fragments of B stay from one 16 rows to the next
-// while the adapter is the same, as in a prompt's rows.
+// while the adapter is the same, as in a prompt's rows. A prompt's rows pay next to
+// nothing (8192 rows, 7168 -> 2048, rank 16: 180 us, without the term 182). 1200 rows of one token
+// each, 14 adapters among 16, pay 45 us beside 59 (4096 -> 4096): the scan, loads, matrix
+// instructions and selections of an adapter follow each other.
 template <class D, int FM, int FN>
 __device__ __forceinline__ void add_low_rank(f32x4 (&acc)[FM][FN], const LowRank &g, int row0,
                                              int row_end, int col0, int N) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr bool SCALED = D::MAX_EXPONENT < 127;
   const int lane = threadIdx.x & 63, fr = lane & 15, fq = lane >> 4;
-  // 64 rows at a time: their values of s are loaded together
-  constexpr int GROUP = FM < 4 ? FM : 4, AT_ONCE = FN <= 2 ? 8 : 2;
+  // rows whose values of s are loaded together, and adapters whose B is. The waves of the
+  // largest tiles have no registers for more; with 1, 2, 4 and 8 adapters in the others 1200 rows
+  // of one token each take 138, 131, 129 and 130 us, and 1024 rows of 8 prompts 47, 48, 48 and 50.
+  constexpr int GROUP = FM < 4 ? FM : FM > 4 ? 2 : 4, AT_ONCE = FN <= 2 ? 4 : 1;
+  int64_t row_b[FN];
 #pragma unroll
-  for (int i0 = 0; i0 < FM; i0 += GROUP) {
-    int id[GROUP];
-#pragma unroll
-    for (int i = 0; i < GROUP; ++i) {
-      const int m = row0 + 16 * (i0 + i) + fr;
-      id[i] = m < row_end ? g.ids[m] : -1;
-      if ((uint32_t)id[i] >= (uint32_t)g.n) id[i] = -1;
-    }
+  for (int j = 0; j < FN; ++j) row_b[j] = (int64_t)min(col0 + 16 * j + fr, N - 1) * g.ldb;
 #pragma unroll 1
-    for (int k0 = 0; k0 < g.rank; k0 += 32) {
-      const int k = k0 + fq * 8;
-      f32x8 v[GROUP];
+  for (int k0 = 0; k0 < g.rank; k0 += 32) {
+    const int k = k0 + fq * 8, at = min(k, g.rank - 8);
+    int have = -1;  // the adapter of fb[0], where it is there alone
+    s16x8 fb[AT_ONCE][FN];
+#pragma unroll
+    for (int i0 = 0; i0 < FM; i0 += GROUP) {
+      int id[GROUP];
 #pragma unroll
       for (int i = 0; i < GROUP; ++i) {
-        v[i] = f32x8{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (id[i] >= 0)
-          v[i] = load8_f32(g.s + (int64_t)(row0 + 16 * (i0 + i) + fr) * g.lds, k, g.rank);
+        const int m = row0 + 16 * (i0 + i) + fr;
+        id[i] = g.ids[min(m, row_end - 1)];
+        if (m >= row_end || (uint32_t)id[i] >= (uint32_t)g.n) id[i] = -1;
       }
-      int have = -1;  // the adapter of fb[0], where it is there alone
-      s16x8 fb[AT_ONCE][FN];
+      f32x8 v[GROUP];
+      if ((g.rank & 7) == 0) {
+#pragma unroll
+        for (int i = 0; i < GROUP; ++i)
+          v[i] = *reinterpret_cast<const f32x8_any *>(
+              g.s + (int64_t)min(row0 + 16 * (i0 + i) + fr, row_end - 1) * g.lds + at);
+#pragma unroll
+        for (int i = 0; i < GROUP; ++i)
+#pragma unroll
+          for (int t = 0; t < 8; ++t) v[i][t] = at == k ? v[i][t] : 0.f;
+      } else {
+#pragma unroll
+        for (int i = 0; i < GROUP; ++i)
+          v[i] = load8_f32(g.s + (int64_t)min(row0 + 16 * (i0 + i) + fr, row_end - 1) * g.lds, k, g.rank);
+      }
 #pragma unroll
       for (int i = 0; i < GROUP; ++i) {
         uint32_t todo = (uint32_t)__ballot(id[i] >= 0) & 0xffffu;
@@ -89,18 +107,38 @@ __device__ __forceinline__ void add_low_rank(f32x4 (&acc)[FM][FN], const LowRank
             a[q] = todo ? __builtin_amdgcn_readlane(id[i], __builtin_ctz(todo)) : -1;
             if (a[q] >= 0) todo &= ~(uint32_t)__ballot(id[i] == a[q]);
           }
-          if (a[0] != have || a[1] >= 0) {
-            have = a[1] >= 0 ? -1 : a[0];
+          // B of the first adapters (a[0] for those there are not), without a branch between
+          // the loads, which would wait for one after the other
+          auto load_b = [&](auto count) MOE_INLINE {
+            constexpr int Q = decltype(count)::value;
+            if (g.rank < 8) {
 #pragma unroll
-            for (int q = 0; q < AT_ONCE; ++q)
-              if (a[q] >= 0) {
+              for (int q = 0; q < Q; ++q)
 #pragma unroll
                 for (int j = 0; j < FN; ++j)
-                  fb[q][j] = load8_raw(g.b + a[q] * g.stride +
-                                           (int64_t)min(col0 + 16 * j + fr, N - 1) * g.ldb,
-                                       k, g.rank);
-              }
-          }
+                  fb[q][j] = load8_raw(g.b + (a[q] < 0 ? a[0] : a[q]) * g.stride + row_b[j], k, g.rank);
+              return;
+            }
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+#pragma unroll
+              for (int j = 0; j < FN; ++j)
+                fb[q][j] = *reinterpret_cast<const s16x8_any *>(
+                    g.b + (a[q] < 0 ? a[0] : a[q]) * g.stride + row_b[j] + at);
+            if (k0 + 32 <= g.rank) return;
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+#pragma unroll
+              for (int j = 0; j < FN; ++j) fb[q][j] = without_first(fb[q][j], k - at);
+          };
+          const bool several = AT_ONCE > 1 && a[AT_ONCE > 1] >= 0;
+          if (!several && a[0] != have)
+            load_b(std::integral_constant<int, 1>());
+          else if (several && a[AT_ONCE / 2] < 0)
+            load_b(std::integral_constant<int, (AT_ONCE + 1) / 2>());
+          else if (several)
+            load_b(std::integral_constant<int, AT_ONCE>());
+          have = several ? -1 : a[0];
 #pragma unroll
           for (int q = 0; q < AT_ONCE; ++q) {
             if (a[q] < 0) continue;

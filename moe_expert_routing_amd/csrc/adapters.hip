@@ -105,13 +105,13 @@ static int few_of(const FewArgs &g, hipStream_t st) {
   if (g.M <= 32) return few_as<D, 2, 2, 3>(g, st);
   return few_as<D, 4, 4, 2>(g, st);
 }
-// Whether y goes by these kernels: up to 64 tokens, and with a long way through few
-// columns more. (Each token with one of 64 adapters of rank 16, these kernels and
-// the tiles, us: 16 tokens 7168 -> 2048 17 and 32, 2048 -> 7168 17 and 26; 64 tokens 24 and
-// 44, 24 and 27; 128 tokens 34 and 40, 38 and 30, 7168 -> 512 17 and 24; 255 tokens 58 and
-// 41, 66 and 46, 21 and 25.)
+// Whether y goes by these kernels: up to 32 tokens, up to 64 but where many columns come of
+// a short way, and with a long way to few columns up to 128. (Each token with one of 64 adapters
+// of rank 16, these kernels and the tiles, us: 32 tokens 7168 -> 2048 19 and 25, 2048 -> 7168
+// 17 and 20; 64 tokens 23 and 26, 24 and 20, 4096 -> 4096 28 and 25, 7168 -> 7168 40 and 54, 7168
+// -> 512 19 and 25; 100 tokens 32 and 29, 36 and 24, 41 and 26, 61 and 58, 24 and 25.)
 static bool is_few(int64_t T, int64_t I, int64_t O) {
-  return T <= 64 || (T <= 128 && I >= 2 * O) || (T <= 256 && I >= 8 * O);
+  return T <= 32 || (T <= 64 && (I > 4096 || O < 4096)) || (T <= 128 && I >= 8 * O);
 }
 static int run_few(const moe_adapter_linear_args *a, Arena &ws, hipStream_t st) {
   FewArgs g = {};
@@ -140,15 +140,15 @@ static int run_few(const moe_adapter_linear_args *a, Arena &ws, hipStream_t st) 
 }
 
 // Plan of the product with its low-rank term. Of few rows the epilogue is the longer
-// part, one adapter after the other for every 16 of them, so that it takes the small tiles
-// and, with few of these, ranges of k (by the dense product's plan and this one, us: 100 tokens
-// 2048 -> 7168 38 and 30, 160 tokens 7168 -> 2048 65 and 36, 4096 -> 4096 44 and 37; with
-// 255 tokens 42 and 46, 44 and 45, and with many tiles of a long k 65 tokens 7168 -> 7168 56
-// and 61).
+// part, one adapter after the other for every 16 of them, so that it takes the small tiles,
+// and ranges of k where these are few (by the dense product's plan and this one, us: 100 tokens
+// 2048 -> 7168 26 and 24, 160 tokens 7168 -> 2048 46 and 30, 512 tokens 7168 -> 512 44 and 39; past
+// the limits, 255 tokens 2048 -> 7168 33 and 37, 192 tokens 7168 -> 7168 75 and 91).
 static Plan low_plan(int64_t T, int64_t I, int64_t O) {
   const int64_t tiles = (T + 31) / 32 * ((O + 63) / 64);
-  if (T > 192 || (tiles >= 256 && I >= 4096)) return row_plan({}, true, T, O, I);
-  return {TILE_32, tiles < 256 && I >= 4096 ? 4 : 1};
+  if (T <= 512 && tiles < 256 && I >= 4096) return {TILE_32, 4};
+  if (T <= 192 && I < 4096) return {TILE_32, 1};
+  return row_plan({}, true, T, O, I);
 }
 
 static int run_forward(const moe_adapter_linear_args *a, Arena &ws, hipStream_t st) {

@@ -19,19 +19,7 @@ __device__ __forceinline__ s16x8 load_row8(const uint16_t *row, int c, int n) {
   if (n < 8) return load8_raw(row, c, n);
   const int at = min(c, n - 8);
   s16x8 w = *reinterpret_cast<const s16x8_any *>(row + at);
-  if (at < c) {
-    typedef unsigned long long u64x2 __attribute__((ext_vector_type(2)));
-    u64x2 v = __builtin_bit_cast(u64x2, w);
-    const int bits = (c - at) * 16;
-    if (bits >= 64) {
-      v.x = v.y >> (bits - 64);
-      v.y = 0;
-    } else {
-      v.x = v.x >> bits | v.y << (64 - bits);
-      v.y >>= bits;
-    }
-    w = __builtin_bit_cast(s16x8, v);
-  }
+  if (at < c) w = without_first(w, c - at);
   return w;
 }
 

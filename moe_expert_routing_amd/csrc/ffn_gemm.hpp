@@ -66,7 +66,6 @@ typedef __attribute__((address_space(3))) void *lds_ptr_t;
 typedef __attribute__((address_space(3))) s16x4 *lds_s16x4_ptr_t;
 typedef __attribute__((address_space(1))) void *gbl_ptr_t;
 
-#define MOE_INLINE __attribute__((always_inline))  // the kernel's lambdas hold its registers
 
 // Offset past a buffer's end: loads zeros.
 constexpr uint32_t PAST = 0xffffffffu;

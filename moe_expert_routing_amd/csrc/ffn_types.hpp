@@ -7,6 +7,8 @@
 
 #include "../../include/moe_ffn.h"
 
+#define MOE_INLINE __attribute__((always_inline))  // the kernels' lambdas hold their registers
+
 namespace moe_ffn {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -130,6 +132,16 @@ __device__ __forceinline__ s16x8 load8_raw(const uint16_t *row, int c, int n) {
   for (int i = 0; i < 8; ++i)
     if (c + i < n) w[i] = (short)row[c + i];
   return w;
+}
+// w from its element d on, with zeros behind.
+__device__ __forceinline__ s16x8 without_first(s16x8 w, int d) {
+  typedef unsigned long long u64x2 __attribute__((ext_vector_type(2)));
+  u64x2 v = __builtin_bit_cast(u64x2, w);
+  const int bits = d * 16, low = bits & 63;
+  if (bits >= 64) v = u64x2{v.y, 0};
+  if (bits >= 128) v.x = 0;
+  if (low) v = u64x2{v.x >> low | v.y << (64 - low), v.y >> low};
+  return __builtin_bit_cast(s16x8, v);
 }
 template <class D>
 __device__ __forceinline__ f32x8 load8(const uint16_t *row, int c, int n) {
