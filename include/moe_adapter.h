@@ -43,8 +43,8 @@ extern "C" {
  *       u^T x and of dy^T s, zeros for one without tokens.
  * W has no gradient here (moe_linear_backward computes it). Any of dx, da and db
  * may be left out (p NULL).
- * s and u are fp32: the matrix cores take them in two halves of the type each,
- * at a power of two of their own where the type is fp16.
+ * s and u are fp32, and so is what is multiplied with them, or the matrix cores take
+ * them in two halves of the type each, at a power of two of their own in fp16.
  */
 typedef struct moe_adapter_linear_args {
   int32_t dtype, rank;

@@ -181,10 +181,16 @@ struct ShrinkArgs {
 // adapter among the rows the block goes through K once, or with NS2 for two of them
 // at a time (that many stages then): requests lie together, so a prompt's rows have one
 // or two, and with one block to a compute unit those that went through K twice took as
-// long again as all others (8192 rows of 7168, 16 requests: 33 us). A decode batch's
-// rows may have 16, which the blocks of `turns` rounds over the rows share. (The rounds
-// follow each other: with the blocks of the same rows side by side every second one ends
-// at once, and as they go to the XCDs in turn, half of these stood idle: 66 us.)
+// long again as all others (8192 rows of 7168, 16 requests, rank 16: 33 us, now 28). A
+// decode batch's rows may have 16, which the blocks of `turns` rounds over the rows share.
+// (The rounds follow each other: with the blocks of the same rows side by side every second
+// one ends at once, and as they go to the XCDs in turn, half of these stood idle: 66 us.)
+//
+// Bound by reading x: 8192 rows of 7168 with one adapter of rank 16 20 us (6 TB/s, part of x in
+// the last cache), of rank 64 26. Rows with three and more adapters take a second way through
+// K and are what the 16 requests pay for; each XCD with rows side by side, so that its L2
+// holds few adapters, gained nothing (217 and 218 us with the product; 32768 rows 963 and
+// 950), nor did one more block of x on its way in the pairs.
 template <class D, int MT, int RB, int WAVES, int NS, int NS2, bool STAGED>
 __global__ __launch_bounds__(64 * WAVES) void shrink_kernel(const ShrinkArgs g) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -267,6 +273,9 @@ __global__ __launch_bounds__(64 * WAVES) void shrink_kernel(const ShrinkArgs g) 
 // each of which leaves fp32 sums. Second launch: the sums added in their order, s B_a^T in
 // fp32 without halves, bias and residual, one rounding.
 // Tokens go in groups of 64, each with blocks of its own.
+// 16 tokens, 7168 -> 2048, an adapter of rank 16 each: 10.5 us (33 MB, 3.2 TB/s with some 4 us of
+// launch and first loads in it) and 4.3, of which a lone block of loads and stores takes 3; 64
+// tokens, 4096 -> 4096, rank 64: 26 and 13.5 (68 MB).
 constexpr int FEW_GROUP = 64;
 struct FewArgs {
   const uint16_t *x, *w, *a, *b, *bias, *res;
@@ -408,6 +417,8 @@ struct PrepArgs {
 // A block for each adapter counts the ids below its own and its own, a wave 64 tokens
 // at a time by ballots, and then writes its tokens: two reads of the ids a block, no
 // order that changes. The blocks after those make the copies, 8 of the rank a thread.
+// Bound by the two reads' latency: 8192 tokens, 8 adapters, 2048 -> 4096 with rank 64 6-8 us in
+// one launch, 512 tokens and 4 adapters 5.
 __global__ __launch_bounds__(PREP_THREADS) void prep_kernel(const PrepArgs g) {
   __shared__ int sames[PREP_WAVES], lesses[PREP_WAVES];
   const int64_t block = blockIdx.x + g.block0;
@@ -528,6 +539,10 @@ constexpr int GRAD_COLS = 256, GRAD_K = 32, GRAD_WAVES = 4, GRAD_WINDOW = 1024;
 // fp16, whose range v may pass, the 32 values of a column of v are taken at a power
 // of two of their own. What is not there (tokens past the end, columns past the width or the
 // rank) is loaded from a few zeros, so that nothing a buffer happens to hold counts.
+// 8192 tokens, 2048 + 4096 columns, rank 64, 8 adapters: 36 us for 101 MB in and 35 MB of
+// sums out (3.8 TB/s; with plain loads 62, with a branch for each missing row 54); rank 16 and 7168
+// + 2048 columns 33 us. 256 columns, so that rows come in whole 512 bytes; 2 blocks of a compute
+// unit cover each other's waits (6 stages in one: slower).
 template <class D, int RB, int NS>
 __global__ __launch_bounds__(64 * GRAD_WAVES, RB <= 4 ? 2 : 1) void grad_kernel(const GradArgs g) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -687,7 +702,8 @@ __global__ __launch_bounds__(64 * GRAD_WAVES, RB <= 4 ? 2 : 1) void grad_kernel(
 }
 
 // The chunks' sums added in their order: da [rank, in], rows of 8 columns a thread; db
-// [out, rank], 8 of the rank a thread and the columns along the lanes.
+// [out, rank], 8 of the rank a thread and the columns along the lanes. Bound by reading the
+// sums, which are still in the caches: 35 MB in 9 us (one chunk's load after the other: 20).
 struct JoinSide {
   const float *part;
   uint16_t *out;
