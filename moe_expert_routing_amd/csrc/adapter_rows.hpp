@@ -181,7 +181,7 @@ struct ShrinkArgs {
 // adapter among the rows the block goes through K once, or with NS2 for two of them
 // at a time (that many stages then): requests lie together, so a prompt's rows have one
 // or two, and with one block to a compute unit those that went through K twice took as
-// long again as all others (8192 rows of 7168, 16 requests, rank 16: 33 us, now 28). A
+// long again as all others (8192 rows of 7168, 16 requests, rank 16: 33 us, now 28-31). A
 // decode batch's rows may have 16, which the blocks of `turns` rounds over the rows share.
 // (The rounds follow each other: with the blocks of the same rows side by side every second
 // one ends at once, and as they go to the XCDs in turn, half of these stood idle: 66 us.)
@@ -274,8 +274,7 @@ __global__ __launch_bounds__(64 * WAVES) void shrink_kernel(const ShrinkArgs g) 
 // fp32 without halves, bias and residual, one rounding.
 // Tokens go in groups of 64, each with blocks of its own.
 // 16 tokens, 7168 -> 2048, an adapter of rank 16 each: 10.5 us (33 MB, 3.2 TB/s with some 4 us of
-// launch and first loads in it) and 4.3, of which a lone block of loads and stores takes 3; 64
-// tokens, 4096 -> 4096, rank 64: 26 and 13.5 (68 MB).
+// launch and first loads in it) and 4.
 constexpr int FEW_GROUP = 64;
 struct FewArgs {
   const uint16_t *x, *w, *a, *b, *bias, *res;
