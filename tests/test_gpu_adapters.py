@@ -303,6 +303,16 @@ def test_rows_between_a_thousand_and_four(T, K, R, n, kind, dt):
     check_backward(dy, x, w, a, b, ids, scale, s, M.adapter_linear_backward(dy, x, w, a, b, ids, s, scale=scale))
 
 
+@pytest.mark.parametrize("T,I,O,R,n,kind", [(65, 4101, 130, 16, 5, "random"), (500, 5002, 200, 12, 40, "each"), (130, 4097, 64, 7, 9, "requests"),
+                                            (512, 7168, 512, 16, 16, "requests"), (48, 8000, 100, 8, 48, "each"), (33, 2048, 4100, 32, 20, "each")])
+@pytest.mark.parametrize("dt", [BF, FP], ids=["bf16", "fp16"])
+def test_ranges_of_a_long_way(T, I, O, R, n, kind, dt):
+    """Small tiles whose ranges of k meet in the workspace, with the term on one of them."""
+    x, w, a, b, ids, scale = problem(T, I, O, R, n, kind, dt)
+    bias, res = normal(9, O, dt=dt), normal(10, T, O, dt=dt)
+    check_forward(x, w, a, b, ids, scale, bias, res, M.adapter_linear(x, w, a, b, ids, scale=scale, bias=bias, residual=res, save=True))
+
+
 def test_many_adapters():
     """More adapters than tokens, and the largest number of them."""
     T, I, O, R, n = 40, 64, 48, 4, 4096
