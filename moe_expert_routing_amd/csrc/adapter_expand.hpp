@@ -37,8 +37,9 @@ __device__ __forceinline__ int exponent_for(float most) {
 // are taken one after the other; the fragments of B stay from one 16 rows to the next
 // while the adapter is the same, as in a prompt's rows. A prompt's rows pay next to
 // nothing (8192 rows, 7168 -> 2048, rank 16: 180 us, without the term 182). 1200 rows of one token
-// each, 14 adapters among 16, pay 45 us beside 59 (4096 -> 4096): the scan, loads, matrix
-// instructions and selections of an adapter follow each other.
+// each, 14 adapters among 16, pay some 35 us beside 59 (4096 -> 4096): the scan, loads, matrix
+// instructions and selections of an adapter follow each other. (The order of the loads' lanes is
+// not what it waits for: all lanes on one address take as long.)
 template <class D, int FM, int FN>
 __device__ __forceinline__ void add_low_rank(f32x4 (&acc)[FM][FN], const LowRank &g, int row0,
                                              int row_end, int col0, int N) {
@@ -46,15 +47,17 @@ __device__ __forceinline__ void add_low_rank(f32x4 (&acc)[FM][FN], const LowRank
   constexpr bool SCALED = D::MAX_EXPONENT < 127;
   const int lane = threadIdx.x & 63, fr = lane & 15, fq = lane >> 4;
   // rows whose values of s are loaded together, and adapters whose B is. The waves of the
-  // largest tiles have no registers for more; with 1, 2, 4 and 8 adapters in the others 1200 rows
-  // of one token each take 138, 131, 129 and 130 us, and 1024 rows of 8 prompts 47, 48, 48 and 50.
+  // largest tiles have no registers for more (two adapters: 221 us for 217); with 4 and 8 adapters
+  // in the others 1200 rows of one token each take 119 and 121 us, 1024 rows of 8 prompts 47 and 49.
   constexpr int GROUP = FM < 4 ? FM : FM > 4 ? 2 : 4, AT_ONCE = FN <= 2 ? 4 : 1;
+  // up to rank 16 one matrix instruction takes both halves, 16 elements of its 32 each
+  const bool both = g.rank <= 16;
   int64_t row_b[FN];
 #pragma unroll
   for (int j = 0; j < FN; ++j) row_b[j] = (int64_t)min(col0 + 16 * j + fr, N - 1) * g.ldb;
 #pragma unroll 1
   for (int k0 = 0; k0 < g.rank; k0 += 32) {
-    const int k = k0 + fq * 8, at = min(k, g.rank - 8);
+    const int k = k0 + (both ? fq & 1 : fq) * 8, at = min(k, g.rank - 8);
     int have = -1;  // the adapter of fb[0], where it is there alone
     s16x8 fb[AT_ONCE][FN];
 #pragma unroll
@@ -98,14 +101,16 @@ __device__ __forceinline__ void add_low_rank(f32x4 (&acc)[FM][FN], const LowRank
         }
         s16x8 hi, lo;
         halves<D>(v[i], hi, lo);
+        if (both && fq >= 2) hi = lo;
         while (todo) {
           // the next adapters' fragments are loaded together: a decode batch's rows
           // have one each
           int a[AT_ONCE];
 #pragma unroll
           for (int q = 0; q < AT_ONCE; ++q) {
-            a[q] = todo ? __builtin_amdgcn_readlane(id[i], __builtin_ctz(todo)) : -1;
-            if (a[q] >= 0) todo &= ~(uint32_t)__ballot(id[i] == a[q]);
+            const int next = __builtin_amdgcn_readlane(id[i], __builtin_ctz(todo | 0x8000u));
+            a[q] = todo ? next : -2;  // -2: no row's
+            todo &= ~(uint32_t)__ballot(id[i] == next);
           }
           // B of the first adapters (a[0] for those there are not), without a branch between
           // the loads, which would wait for one after the other
@@ -125,35 +130,41 @@ __device__ __forceinline__ void add_low_rank(f32x4 (&acc)[FM][FN], const LowRank
               for (int j = 0; j < FN; ++j)
                 fb[q][j] = *reinterpret_cast<const s16x8_any *>(
                     g.b + (a[q] < 0 ? a[0] : a[q]) * g.stride + row_b[j] + at);
-            if (k0 + 32 <= g.rank) return;
+            if (k0 + (both ? 16 : 32) <= g.rank) return;
 #pragma unroll
             for (int q = 0; q < Q; ++q)
 #pragma unroll
               for (int j = 0; j < FN; ++j) fb[q][j] = without_first(fb[q][j], k - at);
           };
           const bool several = AT_ONCE > 1 && a[AT_ONCE > 1] >= 0;
-          if (!several && a[0] != have)
-            load_b(std::integral_constant<int, 1>());
-          else if (several && a[AT_ONCE / 2] < 0)
-            load_b(std::integral_constant<int, (AT_ONCE + 1) / 2>());
-          else if (several)
+          if (several)
             load_b(std::integral_constant<int, AT_ONCE>());
+          else if (a[0] != have)
+            load_b(std::integral_constant<int, 1>());
           have = several ? -1 : a[0];
-#pragma unroll
-          for (int q = 0; q < AT_ONCE; ++q) {
-            if (a[q] < 0) continue;
+          auto add = [&](int q) MOE_INLINE {
             const bool mine = id[i] == a[q];
+            f32x4 sum[FN];
 #pragma unroll
-            for (int j = 0; j < FN; ++j) {
-              f32x4 t = D::mfma(fb[q][j], lo, f32x4{0.f, 0.f, 0.f, 0.f});
-              t = D::mfma(fb[q][j], hi, t);
+            for (int j = 0; j < FN; ++j) sum[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (!both)
+#pragma unroll
+              for (int j = 0; j < FN; ++j) sum[j] = D::mfma(fb[q][j], lo, sum[j]);
+#pragma unroll
+            for (int j = 0; j < FN; ++j) sum[j] = D::mfma(fb[q][j], hi, sum[j]);
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                if constexpr (SCALED) t[e] = __builtin_amdgcn_ldexpf(t[e], -power);
-                acc[i0 + i][j][e] = mine ? acc[i0 + i][j][e] + t[e] : acc[i0 + i][j][e];
+                float t = sum[j][e];
+                if constexpr (SCALED) t = __builtin_amdgcn_ldexpf(t, -power);
+                acc[i0 + i][j][e] = mine ? acc[i0 + i][j][e] + t : acc[i0 + i][j][e];
               }
-            }
-          }
+          };
+          add(0);
+          if (several)
+#pragma unroll
+            for (int q = 1; q < AT_ONCE; ++q) add(q);
         }
       }
     }
