@@ -58,7 +58,8 @@ typedef struct moe_dropout_spec {
  *       residual and without dropout h is x: h.p may be NULL, and has to be
  *       given in every other case;
  *   rstd [tokens] fp32 = 1 / sqrt(mean of the row's h^2 + eps) of the rounded
- *       h (NULL: not written; the backward pass reads it);
+ *       h (NULL: not written; the backward pass reads it), also where the
+ *       squares pass fp32's range;
  *   y [tokens, width] = h rstd weight (p NULL: not written);
  *   q [tokens, width] E4M3 codes and q_scale [tokens, width / 32] E8M0 codes
  *       (both NULL: not written; width a multiple of 32) of the unrounded

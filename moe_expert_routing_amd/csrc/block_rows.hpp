@@ -256,7 +256,26 @@ __global__ __launch_bounds__(S::THREADS) void norm_kernel(const NormArgs a) {
       for (int k = 0; k < 8; ++k) sum = fmaf(v[k], v[k], sum);
     }
     sum = row_sum<L>(sum, slots, slot);
-    const float rstd = 1.f / sqrtf(fmaf(sum, inv_width, a.eps));
+    float total = fmaf(sum, inv_width, a.eps), unit = 1.f;
+    if constexpr (D::MAX_EXPONENT >= 127) {
+      // squares past fp32's range, or below what it holds precisely: again, of
+      // elements times a power of two (the same branch in all threads of a row)
+      if (total > 3e38f || total < 0x1p-100f) {
+        unit = total < 1.f ? 0x1p96f : 0x1p-96f;
+        slot ^= 1;
+        sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          keep_packed(row[i]);
+          const f32x8 v = unpack8<D>(row[i]);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) sum = fmaf(v[k] * unit, v[k] * unit, sum);
+        }
+        sum = row_sum<L>(sum, slots, slot);
+        total = fmaf(sum, inv_width, a.eps * unit * unit);
+      }
+    }
+    const float rstd = unit / sqrtf(total);
     if (a.rstd && lane == 0) a.rstd[t] = rstd;
 #pragma unroll
     for (int i = 0; i < CH; ++i) keep_packed(row[i]), keep_packed(weight[i]);

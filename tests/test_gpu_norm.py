@@ -171,6 +171,21 @@ def test_norm_special_values():
     assert bool((v[~kept.cuda()] == 0).all())
 
 
+@pytest.mark.parametrize("W", [5, 130, 1001, 2056, 7168, 20000])
+def test_norm_of_squares_outside_fp32(W):
+    """bf16 rows whose squares overflow or vanish, between ordinary ones."""
+    T = 37
+    x = normal(1, T, W, dt=BF)
+    size = torch.tensor([1.0, 2.0 ** 70, 2.0 ** 118, 2.0 ** -70, 2.0 ** -110, 2.0 ** 62, 2.0 ** -50], device="cuda")[torch.arange(T, device="cuda") % 7]
+    x = (x.float() * size[:, None]).to(BF)
+    weight = normal(2, W, dt=BF)
+    for eps in (0.0, 1e-6, 1e-35):
+        out = M.rms_norm(x, weight, eps=eps)
+        y, bound, rstd, rbound = norm_y(x, weight, eps, BF)
+        assert bool(((out["rstd"].double().cpu() - rstd).abs() <= rbound).all()), eps
+        assert bool(((out["y"].double().cpu() - y).abs() <= bound).all()), eps
+
+
 def test_norm_large_values_in_fp16():
     """The squares of fp16's largest values pass its range; fp32 sums hold them."""
     x = torch.full((2, 7168), 60000.0, dtype=FP, device="cuda")
