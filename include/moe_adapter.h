@@ -44,7 +44,8 @@ extern "C" {
  * W has no gradient here (moe_linear_backward computes it). Any of dx, da and db
  * may be left out (p NULL).
  * s and u are fp32, and so is what is multiplied with them, or the matrix cores take
- * them in two halves of the type each, at a power of two of their own in fp16.
+ * them in three parts of the type, which hold all of their bits (in fp16, at a power of
+ * two of their own, down to 2^-38 of the largest of 32 values).
  */
 typedef struct moe_adapter_linear_args {
   int32_t dtype, rank;

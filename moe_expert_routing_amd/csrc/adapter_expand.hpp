@@ -1,11 +1,12 @@
 // adapter_expand.hpp - the low-rank term of a product, s B_a^T with the adapter a of
 // each row, added to the sums that the product kernels hold before their epilogue.
 //
-// s is fp32. The matrix cores take it in two halves of the matrices' type, high and low:
-// 16 (bf16) or 22 (fp16) bits of it, so that its rounding stays far below the output's;
-// the second half costs 1/(in / 32) of the product's operations. In fp16, whose range
-// s may pass, a row's values are taken at a power of two that makes the largest of
-// 32 of them lie in [2^14, 2^15).
+// s is fp32. The matrix cores take it in three parts of the matrices' type, which hold
+// its 24 bits between them, so that y is the same sum in fp32 here as where few tokens
+// multiply s itself; each part costs 1/(in / 32) of the product's operations. (Two parts
+// hold 16 bits in bf16: enough beside one rounding of y, not where x W^T and s B^T cancel.)
+// In fp16, whose range s may pass, a row's values are taken at a power of two that makes the
+// largest of 32 of them lie in [2^14, 2^15); its smallest step, 2^-24, is then 2^-38 of it.
 //
 // A row takes only its own adapter's result, by a selection and not by factors of zero:
 // infinities or NaN in one adapter stay out of the other requests' rows.
@@ -17,14 +18,16 @@
 
 namespace moe_ffn {
 
-// v in two halves of the type. What is no finite number stays in the high half.
+// v in three parts of the type, the largest first. What is no finite number stays in
+// the first.
 template <class D>
-__device__ __forceinline__ void halves(f32x8 v, s16x8 &hi, s16x8 &lo) {
-  hi = pack8<D>(v);
-  const f32x8 h = unpack8<D>(hi);
+__device__ __forceinline__ void three_parts(f32x8 v, s16x8 (&part)[3]) {
+  part[0] = pack8<D>(v);
+  const f32x8 h = unpack8<D>(part[0]);
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = __builtin_isfinite(h[i]) ? v[i] - h[i] : 0.f;
-  lo = pack8<D>(v);
+  part[1] = pack8<D>(v);
+  part[2] = pack8<D>(v - unpack8<D>(part[1]));
 }
 // The power of two that takes `most`, the largest of some magnitudes, into [2^14, 2^15).
 __device__ __forceinline__ int exponent_for(float most) {
@@ -50,7 +53,7 @@ __device__ __forceinline__ void add_low_rank(f32x4 (&acc)[FM][FN], const LowRank
   // largest tiles have no registers for more (two adapters: 221 us for 217); with 4 and 8 adapters
   // in the others 1200 rows of one token each take 119 and 121 us, 1024 rows of 8 prompts 47 and 49.
   constexpr int GROUP = FM < 4 ? FM : FM > 4 ? 2 : 4, AT_ONCE = FN <= 2 ? 4 : 1;
-  // up to rank 16 one matrix instruction takes both halves, 16 elements of its 32 each
+  // up to rank 16 one matrix instruction takes two parts, 16 elements of its 32 each
   const bool both = g.rank <= 16;
   int64_t row_b[FN];
 #pragma unroll
@@ -99,9 +102,9 @@ __device__ __forceinline__ void add_low_rank(f32x4 (&acc)[FM][FN], const LowRank
 #pragma unroll
           for (int t = 0; t < 8; ++t) v[i][t] = __builtin_amdgcn_ldexpf(v[i][t], power);
         }
-        s16x8 hi, lo;
-        halves<D>(v[i], hi, lo);
-        if (both && fq >= 2) hi = lo;
+        s16x8 part[3];
+        three_parts<D>(v[i], part);
+        if (both && fq >= 2) part[0] = part[1], part[2] = s16x8{0, 0, 0, 0, 0, 0, 0, 0};
         while (todo) {
           // the next adapters' fragments are loaded together: a decode batch's rows
           // have one each
@@ -147,11 +150,13 @@ __device__ __forceinline__ void add_low_rank(f32x4 (&acc)[FM][FN], const LowRank
             f32x4 sum[FN];
 #pragma unroll
             for (int j = 0; j < FN; ++j) sum[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < FN; ++j) sum[j] = D::mfma(fb[q][j], part[2], sum[j]);
             if (!both)
 #pragma unroll
-              for (int j = 0; j < FN; ++j) sum[j] = D::mfma(fb[q][j], lo, sum[j]);
+              for (int j = 0; j < FN; ++j) sum[j] = D::mfma(fb[q][j], part[1], sum[j]);
 #pragma unroll
-            for (int j = 0; j < FN; ++j) sum[j] = D::mfma(fb[q][j], hi, sum[j]);
+            for (int j = 0; j < FN; ++j) sum[j] = D::mfma(fb[q][j], part[0], sum[j]);
 #pragma unroll
             for (int j = 0; j < FN; ++j)
 #pragma unroll

@@ -271,7 +271,7 @@ __global__ __launch_bounds__(64 * WAVES) void shrink_kernel(const ShrinkArgs g) 
 // First launch: x times the rows of W and of each such A_a together, so that reading
 // the adapters costs no time of its own; k is split over the waves of `splits` blocks,
 // each of which leaves fp32 sums. Second launch: the sums added in their order, s B_a^T in
-// fp32 without halves, bias and residual, one rounding.
+// fp32, bias and residual, one rounding.
 // Tokens go in groups of 64, each with blocks of its own.
 // 16 tokens, 7168 -> 2048, an adapter of rank 16 each: 10.5 us (33 MB, 3.2 TB/s with some 4 us of
 // launch and first loads in it) and 4.
@@ -534,7 +534,8 @@ constexpr int GRAD_COLS = 256, GRAD_K = 32, GRAD_WAVES = 4, GRAD_WINDOW = 1024;
 // up each adapter among them apart: the part of adapter a in chunk k goes to slot
 // a + k, of which there is one for each pair that meets. 32 tokens at a time go through
 // LDS, NS stages deep: m as it lies, read through the transposing LDS load, and v in fp32,
-// which each wave takes into two halves of the type in the registers of its fragments. In
+// which each wave takes into three parts of the type in the registers of its fragments, so
+// that none of its 24 bits is lost where tokens cancel. In
 // fp16, whose range v may pass, the 32 values of a column of v are taken at a power
 // of two of their own. What is not there (tokens past the end, columns past the width or the
 // rank) is loaded from a few zeros, so that nothing a buffer happens to hold counts.
@@ -670,19 +671,21 @@ __global__ __launch_bounds__(64 * GRAD_WAVES, RB <= 4 ? 2 : 1) void grad_kernel(
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = __builtin_amdgcn_ldexpf(v[e], power);
           }
-          s16x8 high, low;
-          halves<D>(v, high, low);
+          s16x8 piece[3];
+          three_parts<D>(v, piece);
 #pragma unroll
           for (int j = 0; j < J; ++j) {
-            if constexpr (SCALED) {
-              f32x4 t = D::mfma(fm[j], low, f32x4{0.f, 0.f, 0.f, 0.f});
-              t = D::mfma(fm[j], high, t);
+            f32x4 t = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int q = 2; q >= 0; --q) {
+              if constexpr (SCALED)
+                t = D::mfma(fm[j], piece[q], t);
+              else
+                acc[r][j] = D::mfma(fm[j], piece[q], acc[r][j]);
+            }
+            if constexpr (SCALED)
 #pragma unroll
               for (int e = 0; e < 4; ++e) acc[r][j][e] += __builtin_amdgcn_ldexpf(t[e], -power);
-            } else {
-              acc[r][j] = D::mfma(fm[j], low, acc[r][j]);
-              acc[r][j] = D::mfma(fm[j], high, acc[r][j]);
-            }
           }
         }
       }
