@@ -42,7 +42,9 @@ extern "C" {
  *   da [rank, in] and db [out, rank] of each adapter = sum over its tokens of
  *       u^T x and of dy^T s, zeros for one without tokens.
  * W has no gradient here (moe_linear_backward computes it). Any of dx, da and db
- * may be left out (p NULL).
+ * may be left out (p NULL). The workspace holds a transposed copy of A and B for as many
+ * adapters as there are tokens at most, and sums of a size that does not grow with the
+ * adapters beyond that.
  * s and u are fp32, and so is what is multiplied with them, or the matrix cores take
  * them in three parts of the type, which hold all of their bits (in fp16, at a power of
  * two of their own, down to 2^-38 of the largest of 32 values).

@@ -401,14 +401,18 @@ constexpr int PREP_THREADS = 1024, PREP_WAVES = PREP_THREADS / 64;
 // perm: the tokens with an adapter, by adapter and then by number; offsets[a]: where
 // those of adapter a begin. s4: s with rows of whole 16 bytes (NULL: not needed). zeros:
 // 16 bytes that the gradients' loads take for what is not there.
+// Where there are more adapters than tokens, the copies are made for the tokens' adapters
+// alone, that of the first token t with each of them at place t: own[t] is the place of token
+// t's adapter (-1: none), own_scale[place] its scale. Else the places are the adapters.
 struct PrepArgs {
   const int32_t *ids;
   int32_t *offsets, *perm;
   const uint16_t *a, *b;
   int64_t lda, a_stride, ldb, b_stride;
   uint16_t *at, *bt;
-  const float *s;
-  float *s4, *zeros;
+  const float *s, *scale;
+  float *s4, *zeros, *own_scale;
+  int32_t *own;
   int32_t T, n, in, out, rank, rank4, rank8, out8;
   int64_t block0, copy_block;  // numbers of the launch's first block, and of the first that copies s
 };
@@ -418,6 +422,7 @@ struct PrepArgs {
 // order that changes. The blocks after those make the copies, 8 of the rank a thread.
 // Bound by the two reads' latency: 8192 tokens, 8 adapters, 2048 -> 4096 with rank 64 6-8 us in
 // one launch, 512 tokens and 4 adapters 5.
+template <bool OWN>
 __global__ __launch_bounds__(PREP_THREADS) void prep_kernel(const PrepArgs g) {
   __shared__ int sames[PREP_WAVES], lesses[PREP_WAVES];
   const int64_t block = blockIdx.x + g.block0;
@@ -479,8 +484,24 @@ __global__ __launch_bounds__(PREP_THREADS) void prep_kernel(const PrepArgs g) {
   }
   const int runs = g.rank8 / 8, a_items = g.at ? g.in * runs : 0, items = a_items + g.out * runs;
   const int blocks = (items + PREP_THREADS - 1) / PREP_THREADS;
-  const int a = (int)((block - g.n) / blocks);
+  const int place = (int)((block - g.n) / blocks);
   int i = (int)((block - g.n) % blocks) * PREP_THREADS + threadIdx.x;
+  int a = place;
+  if constexpr (OWN) {
+    a = g.ids[place];
+    if (threadIdx.x == 0) sames[0] = place;
+    __syncthreads();
+    for (int t = threadIdx.x; t < place; t += PREP_THREADS)
+      if (g.ids[t] == a) {
+        atomicMin(&sames[0], t);
+        break;
+      }
+    __syncthreads();
+    const int first = (uint32_t)a < (uint32_t)g.n ? sames[0] : -1;
+    if (i == 0) g.own[place] = first;
+    if (i == 0 && first == place && g.scale) g.own_scale[place] = g.scale[a];
+    if (first != place) return;
+  }
   if (i < a_items) {
     const int c = i / runs, r = i % runs * 8;  // a row's 16-byte runs side by side
     const uint16_t *src = g.a + a * g.a_stride + c;
@@ -488,12 +509,12 @@ __global__ __launch_bounds__(PREP_THREADS) void prep_kernel(const PrepArgs g) {
 #pragma unroll
     for (int v = 0; v < 8; ++v)
       if (r + v < g.rank) w[v] = (short)src[(r + v) * g.lda];
-    *reinterpret_cast<s16x8 *>(g.at + ((int64_t)a * g.in + c) * g.rank8 + r) = w;
+    *reinterpret_cast<s16x8 *>(g.at + ((int64_t)place * g.in + c) * g.rank8 + r) = w;
   } else if (i < items) {
     i -= a_items;
     const int c = i / runs, r = i % runs * 8;
     const s16x8 w = load8_raw(g.b + a * g.b_stride + c * g.ldb, r, g.rank);
-    uint16_t *dst = g.bt + (int64_t)a * g.rank * g.out8 + c;
+    uint16_t *dst = g.bt + (int64_t)place * g.rank * g.out8 + c;
 #pragma unroll
     for (int v = 0; v < 8; ++v)
       if (r + v < g.rank) dst[(int64_t)(r + v) * g.out8] = (uint16_t)w[v];
@@ -509,6 +530,8 @@ struct GradSide {
   int64_t ld;
   const float *v;     // [T, rank], rows ldv elements (whole 16 bytes) apart
   float *part;        // [slots][rank][width4]
+  uint16_t *out;      // dA [rank, width] or dB [width, rank] of each adapter
+  int64_t ld_out, stride;
   int32_t width, width4, tiles;
 };
 struct GradArgs {
@@ -528,22 +551,31 @@ __device__ __forceinline__ void lds_gather(const void *from, uint8_t *dst) {
 #endif
 }
 
+typedef s16x4 s16x4_any __attribute__((aligned(2)));
 constexpr int GRAD_COLS = 256, GRAD_K = 32, GRAD_WAVES = 4, GRAD_WINDOW = 1024;
 
 // A block takes 256 columns of m and `chunk` tokens of the sorted order, and adds
 // up each adapter among them apart: the part of adapter a in chunk k goes to slot
-// a + k, of which there is one for each pair that meets. 32 tokens at a time go through
-// LDS, NS stages deep: m as it lies, read through the transposing LDS load, and v in fp32,
-// which each wave takes into three parts of the type in the registers of its fragments, so
-// that none of its 24 bits is lost where tokens cancel. In
+// a + k, of which there is one for each pair that meets.
+// WHOLE, for more adapters than chunks: one whose tokens all lie in the chunk is written as it
+// is, and of the others a chunk has two at most, the one that goes on from the chunk before
+// (slot 2 k of chunk k) and the one that begins in it and goes on behind it (slot 2 k + 1).
+// So the parts' memory does not grow with the adapters (4096 of rank 64, 7168 + 7168 columns: 15
+// GB otherwise). A whole backward pass of 4096 tokens of 256 adapters, rank 16, 4096 + 4096
+// columns takes 397 us, by pairs 437; 8192 tokens of 1024, rank 32, 2048 + 2048 columns 831 and
+// 1017. With few adapters the pairs' kernel, which keeps less through the products, is the
+// faster (8192 tokens of 8, as below: gradients and join 50 us, WHOLE 52).
+// 32 tokens at a time go through LDS, NS stages deep: m as it lies, read through the transposing
+// LDS load, and v in fp32, which each wave takes into three parts of the type in the
+// registers of its fragments, so that none of its 24 bits is lost where tokens cancel. In
 // fp16, whose range v may pass, the 32 values of a column of v are taken at a power
 // of two of their own. What is not there (tokens past the end, columns past the width or the
 // rank) is loaded from a few zeros, so that nothing a buffer happens to hold counts.
-// 8192 tokens, 2048 + 4096 columns, rank 64, 8 adapters: 36 us for 101 MB in and 35 MB of
-// sums out (3.8 TB/s; with plain loads 62, with a branch for each missing row 54); rank 16 and 7168
-// + 2048 columns 33 us. 256 columns, so that rows come in whole 512 bytes; 2 blocks of a compute
+// 8192 tokens, 2048 + 4096 columns, rank 64, 8 adapters: 39 us for 101 MB in and 35 MB of
+// sums out (3.5 TB/s; with two parts of v 35; with plain loads 62 where this took 36, with a
+// branch for each missing row 54); rank 16 and 7168 + 2048 columns 33 us. 256 columns, so that rows come in whole 512 bytes; 2 blocks of a compute
 // unit cover each other's waits (6 stages in one: slower).
-template <class D, int RB, int NS>
+template <class D, int RB, int NS, bool WHOLE>
 __global__ __launch_bounds__(64 * GRAD_WAVES, RB <= 4 ? 2 : 1) void grad_kernel(const GradArgs g) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr bool SCALED = D::MAX_EXPONENT < 127;
@@ -690,21 +722,47 @@ __global__ __launch_bounds__(64 * GRAD_WAVES, RB <= 4 ? 2 : 1) void grad_kernel(
         }
       }
     }
-    float *part = sd.part + (int64_t)(a + blockIdx.y) * g.rank * sd.width4;
+    const int c = c0 + my_col + 4 * fq, row = my_rank + fr;
+    const bool before = g.offsets[a] < first, behind = g.offsets[a + 1] > last;
+    if (!WHOLE || before || behind) {
+      const uint32_t slot = WHOLE ? 2 * blockIdx.y + (before ? 0 : 1) : a + blockIdx.y;
+      float *part = sd.part + ((int64_t)slot * g.rank + row) * sd.width4 + c;
 #pragma unroll
-    for (int r = 0; r < RW; ++r)
+      for (int r = 0; r < RW; ++r)
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const int c = c0 + my_col + 16 * j + 4 * fq, row = my_rank + 16 * r + fr;
-        if (row < g.rank && c < sd.width4)
-          *reinterpret_cast<f32x4 *>(part + (int64_t)row * sd.width4 + c) = acc[r][j];
-      }
+        for (int j = 0; j < J; ++j)
+          if (row + 16 * r < g.rank && c + 16 * j < sd.width4)
+            *reinterpret_cast<f32x4 *>(part + (int64_t)16 * r * sd.width4 + 16 * j) = acc[r][j];
+    } else {
+      // elements from one rank, and from one column, to the next; the compiler is not
+      // to keep the addresses and conditions of all of them through the products (which spilled)
+      int64_t by_rank = second ? 1 : sd.ld_out, by_col = second ? sd.ld_out : 1;
+      int ranks = g.rank, cols = sd.width;
+      asm volatile("" : "+s"(by_rank), "+s"(by_col), "+s"(ranks), "+s"(cols));
+      uint16_t *out = sd.out + a * sd.stride + row * by_rank + c * by_col;
+#pragma unroll
+      for (int r = 0; r < RW; ++r)
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const int left = row + 16 * r < ranks ? cols - (c + 16 * j) : 0;
+          uint16_t *to = out + 16 * (r * by_rank + j * by_col);
+          const s16x4 v = __builtin_bit_cast(s16x4, __builtin_convertvector(acc[r][j], typename D::v4));
+          if (!second && left >= 4) {
+            *reinterpret_cast<s16x4_any *>(to) = v;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (e < left) to[e * by_col] = (uint16_t)v[e];
+          }
+        }
+    }
   }
 #endif
 }
 
-// The chunks' sums added in their order: da [rank, in], rows of 8 columns a thread; db
-// [out, rank], 8 of the rank a thread and the columns along the lanes. Bound by reading the
+// The chunks' sums added in their order, and zeros for the adapters without tokens; WHOLE:
+// but for those that grad_kernel has written: da [rank, in], rows of 8 columns a thread; db [out, rank], 8 of
+// the rank a thread and the columns along the lanes. Bound by reading the
 // sums, which are still in the caches: 35 MB in 9 us (one chunk's load after the other: 20).
 struct JoinSide {
   const float *part;
@@ -712,12 +770,14 @@ struct JoinSide {
   int64_t ld, stride;
   int32_t width, width4, blocks;
 };
-template <class D>
+template <class D, bool WHOLE>
 __global__ __launch_bounds__(256) void grad_join_kernel(const JoinSide da, const JoinSide db,
                                                         const int32_t *__restrict__ offsets,
                                                         int rank, int chunk) {
   const int a = blockIdx.y, begin = offsets[a], end = offsets[a + 1];
   const int k0 = begin / chunk, k1 = end > begin ? (end - 1) / chunk : k0 - 1;
+  if (WHOLE && k0 == k1) return;
+  auto slot = [&](int k) MOE_INLINE { return (int64_t)(WHOLE ? 2 * k + (k == k0) : a + k); };
   // four chunks' parts at a time, those past the last one without their value
   constexpr int AT_ONCE = 4;
   f32x8 v = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -730,7 +790,7 @@ __global__ __launch_bounds__(256) void grad_join_kernel(const JoinSide da, const
       f32x8 p[AT_ONCE];
 #pragma unroll
       for (int q = 0; q < AT_ONCE; ++q)
-        p[q] = load8_f32(da.part + ((int64_t)(a + min(k + q, k1)) * rank + r) * da.width4, c, da.width);
+        p[q] = load8_f32(da.part + (slot(min(k + q, k1)) * rank + r) * da.width4, c, da.width);
 #pragma unroll
       for (int q = 0; q < AT_ONCE; ++q)
 #pragma unroll
@@ -747,7 +807,7 @@ __global__ __launch_bounds__(256) void grad_join_kernel(const JoinSide da, const
       for (int q = 0; q < AT_ONCE; ++q)
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          p[q][e] = db.part[((int64_t)(a + min(k + q, k1)) * rank + min(r + e, rank - 1)) * db.width4 + c];
+          p[q][e] = db.part[(slot(min(k + q, k1)) * rank + min(r + e, rank - 1)) * db.width4 + c];
 #pragma unroll
       for (int q = 0; q < AT_ONCE; ++q)
 #pragma unroll

@@ -192,13 +192,13 @@ static int grad_chunk(int64_t tokens, int tiles, int rank) {
   return (int)((each + GRAD_K - 1) / GRAD_K * GRAD_K);
 }
 
-template <class D>
+template <class D, bool WHOLE>
 static int grads_of(const GradArgs &g, dim3 grid, hipStream_t st) {
   const int rb = (g.rank + 15) / 16;
-  const auto kernel = rb == 1   ? grad_kernel<D, 1, 4>
-                      : rb == 2 ? grad_kernel<D, 2, 3>
-                      : rb <= 4 ? grad_kernel<D, 4, 3>
-                                : grad_kernel<D, 8, 4>;
+  const auto kernel = rb == 1   ? grad_kernel<D, 1, 4, WHOLE>
+                      : rb == 2 ? grad_kernel<D, 2, 3, WHOLE>
+                      : rb <= 4 ? grad_kernel<D, 4, 3, WHOLE>
+                                : grad_kernel<D, 8, 4, WHOLE>;
   kernel<<<grid, 64 * GRAD_WAVES, 0, st>>>(g);
   return hip_status();
 }
@@ -214,8 +214,13 @@ static int run_backward(const moe_adapter_linear_args *a, Arena &ws, hipStream_t
   int32_t *offsets = reinterpret_cast<int32_t *>(ws.take((size_t)(n + 1) * 4));
   int32_t *perm = reinterpret_cast<int32_t *>(ws.take((size_t)T * 4));
   float *zeros = reinterpret_cast<float *>(ws.take(16));
-  uint16_t *at = dx ? ws.take((size_t)n * I * R8 * 2) : nullptr;
-  uint16_t *bt = needs_u ? ws.take((size_t)n * R * O8 * 2) : nullptr;
+  // copies of A and B: of every adapter, or of the tokens' where these are fewer
+  const bool by_token = needs_u && n > T;
+  const int places = by_token ? (int)T : n;
+  uint16_t *at = dx ? ws.take((size_t)places * I * R8 * 2) : nullptr;
+  uint16_t *bt = needs_u ? ws.take((size_t)places * R * O8 * 2) : nullptr;
+  int32_t *own = by_token ? reinterpret_cast<int32_t *>(ws.take((size_t)T * 4)) : nullptr;
+  float *own_scale = by_token && a->scale ? reinterpret_cast<float *>(ws.take((size_t)T * 4)) : nullptr;
   float *u = needs_u ? reinterpret_cast<float *>(ws.take((size_t)T * R4 * 4)) : nullptr;
   // s where its rows are whole 16 bytes, else a copy of it whose rows are
   const bool copy_s = db && T > 0 && (R != R4 || (uintptr_t)a->s % 16 != 0);
@@ -233,12 +238,16 @@ static int run_backward(const moe_adapter_linear_args *a, Arena &ws, hipStream_t
     p.b = (const uint16_t *)a->b.p, p.ldb = a->b.ld, p.b_stride = a->b.stride;
     p.at = at, p.bt = bt, p.in = I, p.out = O, p.rank = R, p.rank4 = R4, p.rank8 = R8, p.out8 = O8;
     p.s = a->s, p.s4 = s4, p.zeros = zeros;
+    p.scale = a->scale, p.own = own, p.own_scale = own_scale;
     const int64_t items = (int64_t)((dx ? I : 0) + (needs_u ? O : 0)) * (R8 / 8);
-    p.copy_block = n + n * ((items + PREP_THREADS - 1) / PREP_THREADS);
+    p.copy_block = n + places * ((items + PREP_THREADS - 1) / PREP_THREADS);
     const int64_t copies = copy_s ? (T * R4 + PREP_THREADS - 1) / PREP_THREADS : 0;
     MOE_TRY(in_parts(p.copy_block + copies, PREP_THREADS, [&](int64_t first, uint32_t blocks) {
       p.block0 = first;
-      prep_kernel<<<blocks, PREP_THREADS, 0, st>>>(p);
+      if (own)
+        prep_kernel<true><<<blocks, PREP_THREADS, 0, st>>>(p);
+      else
+        prep_kernel<false><<<blocks, PREP_THREADS, 0, st>>>(p);
       return hip_status();
     }));
   }
@@ -246,8 +255,8 @@ static int run_backward(const moe_adapter_linear_args *a, Arena &ws, hipStream_t
     ShrinkArgs k = {};
     k.x = (const uint16_t *)a->dy.p, k.ldx = a->dy.ld;
     k.a = bt, k.lda = O8, k.stride = (int64_t)R * O8;
-    k.ids = a->ids, k.scale = a->scale, k.s = u;
-    k.M = (int)T, k.K = O, k.rank = R, k.lds = R4, k.n = n;
+    k.ids = own ? own : a->ids, k.scale = own_scale ? own_scale : a->scale, k.s = u;
+    k.M = (int)T, k.K = O, k.rank = R, k.lds = R4, k.n = places;
     MOE_TRY(shrink(a->dtype, k, st));
   }
   if (dx) {
@@ -258,17 +267,19 @@ static int run_backward(const moe_adapter_linear_args *a, Arena &ws, hipStream_t
     g.b0 = w.p, g.ldb0 = w.ld;
     g.c0 = (uint16_t *)a->dx.p, g.ldc0 = a->dx.ld;
     g.M = (int)T, g.N = I, g.K = O;
-    g.low = {a->ids, u, at, R8, (int64_t)I * R8, n, R, R4};
+    g.low = {own ? own : a->ids, u, at, R8, (int64_t)I * R8, places, R, R4};
     MOE_TRY(run_product(a->dtype, DGRAD, row_plan(dense, false, T, I, O), g, I, 0, ws, st));
   }
   if (!da && !db) return MOE_OK;
   const int a_tiles = da ? (I + GRAD_COLS - 1) / GRAD_COLS : 0;
   const int b_tiles = db ? (O + GRAD_COLS - 1) / GRAD_COLS : 0;
   const int chunk = grad_chunk(T, a_tiles + b_tiles, R);
-  const int64_t chunks = (T + chunk - 1) / chunk, slots = chunks + n - 1;
+  const int64_t chunks = (T + chunk - 1) / chunk;
+  const bool whole = n - 1 > chunks;
+  const int64_t slots = !whole ? chunks + n - 1 : chunks > 1 ? 2 * chunks : 0;
   GradArgs g = {};
-  g.side[0] = {x.p, x.ld, u, nullptr, I, I4, a_tiles};
-  g.side[1] = {dy.p, dy.ld, s4 ? s4 : a->s, nullptr, O, O4, b_tiles};
+  g.side[0] = {x.p, x.ld, u, nullptr, (uint16_t *)a->da.p, a->da.ld, a->da.stride, I, I4, a_tiles};
+  g.side[1] = {dy.p, dy.ld, s4 ? s4 : a->s, nullptr, (uint16_t *)a->db.p, a->db.ld, a->db.stride, O, O4, b_tiles};
   if (da) g.side[0].part = reinterpret_cast<float *>(ws.take((size_t)slots * R * I4 * 4));
   if (db) g.side[1].part = reinterpret_cast<float *>(ws.take((size_t)slots * R * O4 * 4));
   if (ws.dry) return MOE_OK;
@@ -276,13 +287,15 @@ static int run_backward(const moe_adapter_linear_args *a, Arena &ws, hipStream_t
   g.rank = R, g.ldv = R4, g.n = n, g.chunk = chunk;
   if (T > 0) {
     const dim3 grid(a_tiles + b_tiles, (uint32_t)chunks);
-    MOE_TRY(bf ? grads_of<Bf16>(g, grid, st) : grads_of<F16>(g, grid, st));
+    MOE_TRY(bf ? (whole ? grads_of<Bf16, true>(g, grid, st) : grads_of<Bf16, false>(g, grid, st))
+               : (whole ? grads_of<F16, true>(g, grid, st) : grads_of<F16, false>(g, grid, st)));
   }
   const int64_t a_runs = da ? (int64_t)R * ((I + 7) / 8) : 0;
   const int64_t b_runs = db ? (int64_t)((R + 7) / 8) * O : 0;
   const JoinSide ja = {g.side[0].part, (uint16_t *)a->da.p, a->da.ld, a->da.stride, I, I4, (int)((a_runs + 255) / 256)};
   const JoinSide jb = {g.side[1].part, (uint16_t *)a->db.p, a->db.ld, a->db.stride, O, O4, (int)((b_runs + 255) / 256)};
-  const auto kernel = bf ? grad_join_kernel<Bf16> : grad_join_kernel<F16>;
+  const auto kernel = bf ? (whole ? grad_join_kernel<Bf16, true> : grad_join_kernel<Bf16, false>)
+                         : (whole ? grad_join_kernel<F16, true> : grad_join_kernel<F16, false>);
   kernel<<<dim3(ja.blocks + jb.blocks, n), 256, 0, st>>>(ja, jb, offsets, R, chunk);
   return hip_status();
 }
