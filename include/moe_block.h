@@ -59,7 +59,8 @@ typedef struct moe_dropout_spec {
  *       given in every other case;
  *   rstd [tokens] fp32 = 1 / sqrt(mean of the row's h^2 + eps) of the rounded
  *       h (NULL: not written; the backward pass reads it), also where the
- *       squares pass fp32's range;
+ *       squares pass fp32's range. It is infinite, and y no number, where the mean
+ *       plus eps is 0 or below 2^-256 (eps of 0 alone);
  *   y [tokens, width] = h rstd weight (p NULL: not written);
  *   q [tokens, width] E4M3 codes and q_scale [tokens, width / 32] E8M0 codes
  *       (both NULL: not written; width a multiple of 32) of the unrounded

@@ -204,7 +204,8 @@ struct RowShape {
   static constexpr bool SUMS_IN_LDS = CH > 4;
 };
 
-// A row stays in registers from its loads to its stores: one pass over memory. The
+// A row stays in registers from its loads to its stores: one pass over memory (but
+// for the shape of more than 16384 columns, of which the compiler spills 20 registers a lane). The
 // blocks go down the rows with the weight in registers. h is rounded before it
 // is squared: y is the norm of the h that is stored, which the backward pass
 // reads. Bound by memory: 16384 x 7168 with residual and h, y as E4M3 codes, 830 MB in 165
@@ -301,7 +302,8 @@ __global__ __launch_bounds__(S::THREADS) void norm_kernel(const NormArgs a) {
 // The backward pass: a row in registers again, and each lane keeps its columns' sums
 // of dy n over all rows of its block (fp32, written once a block and added by
 // norm_weight_kernel in the order of the blocks). Bound by memory: 8192 x 7168 with dh 94.5 us
-// (5.0 TB/s); the widest rows, whose sums go through LDS, 4096 x 32768 396 us (2.7 TB/s).
+// (5.0 TB/s). Rows of more than 16384 columns, whose sums go through LDS, do not fit the registers:
+// 113 of a lane are spilled, and 4096 x 32768 takes 396 us (2.7 TB/s), bound by that.
 template <class D, class S>
 __global__ __launch_bounds__(S::THREADS) void norm_backward_kernel(const NormArgs a) {
   constexpr int L = S::L, CH = S::CH;
