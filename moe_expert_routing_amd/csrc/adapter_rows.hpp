@@ -489,15 +489,16 @@ __global__ __launch_bounds__(PREP_THREADS) void prep_kernel(const PrepArgs g) {
   int a = place;
   if constexpr (OWN) {
     a = g.ids[place];
-    if (threadIdx.x == 0) sames[0] = place;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int first = place;
+    for (int t = wave * 64; t < first; t += PREP_THREADS) {
+      const uint64_t all = __ballot(t + lane < place && g.ids[t + lane] == a);
+      if (all) first = t + __builtin_ctzll(all);
+    }
+    if (lane == 0) sames[wave] = first;
     __syncthreads();
-    for (int t = threadIdx.x; t < place; t += PREP_THREADS)
-      if (g.ids[t] == a) {
-        atomicMin(&sames[0], t);
-        break;
-      }
-    __syncthreads();
-    const int first = (uint32_t)a < (uint32_t)g.n ? sames[0] : -1;
+    for (int w = 0; w < PREP_WAVES; ++w) first = min(first, sames[w]);
+    if ((uint32_t)a >= (uint32_t)g.n) first = -1;
     if (i == 0) g.own[place] = first;
     if (i == 0 && first == place && g.scale) g.own_scale[place] = g.scale[a];
     if (first != place) return;
